@@ -14,12 +14,10 @@
 using namespace starkv;
 
 namespace {
-
 thread_local char g_err[512] = "";
+}  // namespace
 
-// Bounds that keep every size product of the checks and launches in range.
-constexpr int kMaxHeads = 1024;
-constexpr int kMaxHidden = 1 << 16;
+namespace starkv {
 
 starkv_status fail(starkv_status code, const char* fmt, ...) {
   va_list ap;
@@ -37,6 +35,14 @@ starkv_status ok() {
 starkv_status cuda_fail(cudaError_t e, const char* what) {
   return fail(STARKV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
+
+}  // namespace starkv
+
+namespace {
+
+// Bounds that keep every size product of the checks and launches in range.
+constexpr int kMaxHeads = 1024;
+constexpr int kMaxHidden = 1 << 16;
 
 int gcd_int(int a, int b) {
   while (b) {
@@ -78,7 +84,9 @@ bool make_geom(int r, double frac, bool fp16, LatentGeom* L) {
   return true;
 }
 
-starkv_status check_config(const starkv_config* c, LatentGeom* key, LatentGeom* val) {
+}  // namespace
+
+starkv_status starkv::check_config(const starkv_config* c, LatentGeom* key, LatentGeom* val) {
   if (!c) return fail(STARKV_ERR_INVALID_ARG, "config is NULL");
   if (c->num_q_heads <= 0 || c->num_kv_heads <= 0 || c->head_dim <= 0 || c->hidden <= 0 ||
       c->rank_k <= 0 || c->rank_v <= 0 || c->max_position <= 0)
@@ -126,6 +134,8 @@ starkv_status check_config(const starkv_config* c, LatentGeom* key, LatentGeom* 
   if (val) *val = v;
   return STARKV_OK;
 }
+
+namespace {
 
 // Per-head key geometry and page offsets (uniform ranks: every head is `uniform`).
 // heads: host [h_kv]; returns the page strides (code bytes, meta words) and the key columns.
@@ -197,22 +207,43 @@ DecodeOutWs decode_out_ws(const Ctx& c, int batch, int max_pages) {
 }  // namespace
 
 namespace starkv {
-bool encode_map_2d(CUtensorMap* map, CUtensorMapDataType type, void* base, uint64_t inner, uint64_t rows,
-                   uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+namespace {
+EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = nullptr;
   if (!fn) {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess || !f ||
         q != cudaDriverEntryPointSuccess)
-      return false;
+      return nullptr;
     fn = (EncodeTiledFn)f;
   }
+  return fn;
+}
+}  // namespace
+
+bool encode_map_2d(CUtensorMap* map, CUtensorMapDataType type, void* base, uint64_t inner, uint64_t rows,
+                   uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+  const EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
   cuuint32_t box[2] = {box_inner, box_rows};
   cuuint32_t es[2] = {1, 1};
   return fn(map, type, 2, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_map_heads(CUtensorMap* map, CUtensorMapDataType type, void* base, uint64_t inner, uint64_t heads,
+                      uint64_t rows, uint64_t row_bytes, uint32_t box_inner, uint32_t box_heads, uint32_t box_rows,
+                      CUtensorMapSwizzle swizzle) {
+  const EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)heads, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)inner * 2, (cuuint64_t)row_bytes};  // 16-bit elements
+  cuuint32_t box[3] = {box_inner, box_heads, box_rows};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(map, type, 3, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 }  // namespace starkv
@@ -503,7 +534,7 @@ starkv_status starkv_workspace_bytes(const starkv_ctx* ctx, int32_t op, int32_t 
     *out = decode_out_ws(*c, batch, max_pages).total;
   } else if (op == STARKV_OP_PREFILL) {
     *out = plan_prefill(*c, batch, max_pages, total_q).ws_bytes;
-  } else {
+  } else if (!full_workspace_bytes(*c, op, batch, max_pages, total_q, out)) {
     return fail(STARKV_ERR_INVALID_ARG, "unknown op %d", op);
   }
   return ok();

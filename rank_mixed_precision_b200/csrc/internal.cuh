@@ -94,9 +94,22 @@ struct Ctx {
   CUtensorMap wo_map;     // TMA map of Wo: box 64 columns x min(256, K / wo_splits) rows, 128-byte swizzle
 };
 
+// Host-side results of the C entries (api.cu): the calling thread's message and status.
+starkv_status fail(starkv_status code, const char* fmt, ...);
+starkv_status ok();
+starkv_status cuda_fail(cudaError_t e, const char* what);
+// Checks a configuration; key, val: the latents' geometry (NULL to skip).
+starkv_status check_config(const starkv_config* c, LatentGeom* key, LatentGeom* val);
+// Workspace of the full-width entries (full_api.cu); false for an op that is none of theirs.
+bool full_workspace_bytes(const Ctx& c, int op, int batch, int max_pages, int64_t total_q, size_t* out);
+
 // 2-D TMA map over a row-major [rows][inner] array (no interleave, zero fill).
 bool encode_map_2d(CUtensorMap* map, CUtensorMapDataType type, void* base, uint64_t inner, uint64_t rows,
                    uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle);
+// 3-D TMA map over [rows][heads][inner] (heads dense, rows row_bytes apart; no interleave, zero fill).
+bool encode_map_heads(CUtensorMap* map, CUtensorMapDataType type, void* base, uint64_t inner, uint64_t heads,
+                      uint64_t rows, uint64_t row_bytes, uint32_t box_inner, uint32_t box_heads, uint32_t box_rows,
+                      CUtensorMapSwizzle swizzle);
 
 // Launch with programmatic stream serialisation (the kernel may start while the
 // previous kernel on the stream finishes; it calls griddepcontrol.wait before

@@ -1,4 +1,4 @@
-"""Python binding of the STAR-KV C ABI (include/starkv.h).
+"""Python binding of the STAR-KV C ABI (include/starkv.h, include/starkv_full.h).
 
 Argument marshalling only: every step of the computation runs in the CUDA
 library ``libstarkv.so``.  Functions carry the C names and take torch tensors
@@ -19,6 +19,7 @@ PAGE_TOKENS = 16
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED_SHAPE, ERR_WORKSPACE_TOO_SMALL, ERR_CUDA, ERR_DEVICE_STATUS = range(6)
 DEV_BAD_PAGE, DEV_BAD_SEQ_LEN, DEV_QUANT_OVERFLOW, DEV_BAD_SLOT, DEV_BAD_QUERY_SPAN, DEV_WAIT_TIMEOUT = 1, 2, 4, 8, 16, 32
 OP_DECODE, OP_PREFILL, OP_DECODE_OUT = 0, 1, 2
+OP_KV4_DECODE = 16
 LATENT_KEY, LATENT_VALUE = 0, 1
 
 # every function include/starkv.h declares
@@ -29,6 +30,12 @@ EXPORTS = [
     "starkv_set_output_projection", "starkv_decode_attn_out",
     "starkv_prefill_attn", "starkv_quantize_pack", "starkv_dequantize", "starkv_read_device_status",
     "starkv_selftest_wait_timeout",
+]
+
+# every function include/starkv_full.h declares
+EXPORTS_FULL = [
+    "starkv_kv4_layout", "starkv_kv4_append", "starkv_kv4_read", "starkv_kv4_decode_attn", "starkv_kv4_evict",
+    "starkv_prompt_attn", "starkv_prompt_weights",
 ]
 
 
@@ -55,6 +62,15 @@ class starkv_cache_sizes(ctypes.Structure):
                 ("key_top", ctypes.c_int32), ("value_top", ctypes.c_int32),
                 ("key_groups", ctypes.c_int32), ("value_groups", ctypes.c_int32),
                 ("key_page_bytes", ctypes.c_int32), ("key_page_meta_bytes", ctypes.c_int32)]
+
+
+class starkv_kv4_cache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("weights", ctypes.c_void_p), ("n_pages", ctypes.c_int64)]
+
+
+class starkv_kv4_sizes(ctypes.Structure):
+    _fields_ = [("pages_bytes", ctypes.c_int64), ("weights_bytes", ctypes.c_int64),
+                ("head_page_bytes", ctypes.c_int32), ("groups", ctypes.c_int32)]
 
 
 class StarKVError(RuntimeError):
@@ -88,6 +104,16 @@ _SIGS = {
     "starkv_dequantize": ([_vp, _i32, _vp, _vp, _i64, _vp, _vp], _i32),
     "starkv_read_device_status": ([_vp, _vp, ctypes.POINTER(ctypes.c_uint32)], _i32),
     "starkv_selftest_wait_timeout": ([_vp, ctypes.c_uint64, _vp], _i32),
+    "starkv_kv4_layout": ([ctypes.POINTER(starkv_config), _i64, ctypes.POINTER(starkv_kv4_sizes)], _i32),
+    "starkv_kv4_append": ([_vp, ctypes.POINTER(starkv_kv4_cache), _vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp], _i32),
+    "starkv_kv4_read": ([_vp, ctypes.POINTER(starkv_kv4_cache), _vp, _vp, _vp, _i32, _i32, _i64, _vp, _vp, _vp], _i32),
+    "starkv_kv4_decode_attn": ([_vp, ctypes.POINTER(starkv_kv4_cache), _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _sz,
+                                _vp], _i32),
+    "starkv_kv4_evict": ([_vp, ctypes.POINTER(starkv_kv4_cache), _vp, _vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp,
+                          _vp], _i32),
+    "starkv_prompt_attn": ([_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp],
+                           _i32),
+    "starkv_prompt_weights": ([_vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i32, _i64, _i64, _i32, _i32, _vp, _vp], _i32),
 }
 
 
@@ -344,6 +370,147 @@ def starkv_read_device_status(ctx, stream=None) -> int:
 
 
 # ---------------------------------------------------------------------------
+# Full-width layers (include/starkv_full.h)
+# ---------------------------------------------------------------------------
+def _rows(t, heads, d, name):
+    """Checks rows [n, heads, d] whose heads are dense; returns their distance in elements."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a torch.bfloat16 tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{name} must be [n, {heads}, {d}], got {tuple(t.shape)}")
+    if t.shape[0] == 0:
+        return heads * d
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: the heads of a row must be dense")
+    return t.stride(0) if t.shape[0] > 1 else heads * d
+
+
+def _one_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"arguments on {first.device} and {t.device}")
+
+
+def starkv_kv4_layout(cfg: starkv_config, n_pages: int) -> dict:
+    out = starkv_kv4_sizes()
+    _check(lib().starkv_kv4_layout(ctypes.byref(cfg), n_pages, ctypes.byref(out)))
+    return {f: getattr(out, f) for f, _ in starkv_kv4_sizes._fields_}
+
+
+def starkv_kv4_append(ctx, cfg, cache: starkv_kv4_cache, k, v, slot_mapping, weights=None, stream=None):
+    """Quantise keys and values [n, num_kv_heads, head_dim] into slots (page * 16 + offset)."""
+    ks, vs = (_rows(t, cfg.num_kv_heads, cfg.head_dim, n) for t, n in ((k, "k"), (v, "v")))
+    _need(slot_mapping, torch.int64, "slot_mapping", 1)
+    if weights is not None:
+        _need(weights, torch.float32, "weights", 2)
+        if tuple(weights.shape) != (k.shape[0], cfg.num_kv_heads):
+            raise ValueError("weights must be [n, num_kv_heads]")
+    if slot_mapping.shape[0] != k.shape[0] or v.shape[0] != k.shape[0]:
+        raise ValueError("k, v and slot_mapping disagree on n")
+    _one_device(k, v, slot_mapping, weights)
+    _check(lib().starkv_kv4_append(ctx, ctypes.byref(cache), _p(k), _p(v), ks, vs, _p(slot_mapping), _p(weights),
+                                   k.shape[0], _stream(stream)))
+
+
+def starkv_kv4_read(ctx, cfg, cache: starkv_kv4_cache, block_table, cu, k_out, v_out, starts=None, stream=None):
+    """Rows cu[b] .. cu[b+1]-1 of k_out and v_out become tokens starts[b] .. of sequence b, in bf16."""
+    _need(block_table, torch.int32, "block_table", 2)
+    _need(cu, torch.int32, "cu", 1)
+    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+        _need(t, torch.bfloat16, n, 3)
+        if t.shape[0] != k_out.shape[0] or tuple(t.shape[1:]) != (cfg.num_kv_heads, cfg.head_dim):
+            raise ValueError(f"{n} must be [total, {cfg.num_kv_heads}, {cfg.head_dim}]")
+    B = block_table.shape[0]
+    if starts is not None:
+        _need(starts, torch.int32, "starts", 1)
+    if cu.shape[0] != B + 1 or (starts is not None and starts.shape[0] != B):
+        raise ValueError("block_table / cu / starts disagree on the batch")
+    _one_device(k_out, v_out, block_table, cu, starts)
+    _check(lib().starkv_kv4_read(ctx, ctypes.byref(cache), _p(block_table), _p(starts), _p(cu), B,
+                                 block_table.shape[1], k_out.shape[0], _p(k_out), _p(v_out), _stream(stream)))
+
+
+def starkv_kv4_decode_attn(ctx, cfg, cache: starkv_kv4_cache, q, block_table, seq_lens, accumulate, out, workspace,
+                           stream=None):
+    """Single-query attention over the 4-bit cache; accumulate: add the probabilities to the cache's weights."""
+    _need(q, torch.bfloat16, "q", 3)
+    _need(block_table, torch.int32, "block_table", 2)
+    _need(seq_lens, torch.int32, "seq_lens", 1)
+    _need(out, torch.bfloat16, "out", 3)
+    B = q.shape[0]
+    if tuple(q.shape[1:]) != (cfg.num_q_heads, cfg.head_dim):
+        raise ValueError(f"q must be [batch, {cfg.num_q_heads}, {cfg.head_dim}]")
+    if block_table.shape[0] != B or seq_lens.shape[0] != B or tuple(out.shape) != tuple(q.shape):
+        raise ValueError("q / block_table / seq_lens / out disagree on the batch")
+    if workspace is not None:
+        _need(workspace, torch.uint8, "workspace", 1)
+    _one_device(q, block_table, seq_lens, out, workspace)
+    _check(lib().starkv_kv4_decode_attn(ctx, ctypes.byref(cache), _p(q), _p(block_table), _p(seq_lens), B,
+                                        block_table.shape[1], int(bool(accumulate)), _p(out), _p(workspace),
+                                        0 if workspace is None else workspace.numel(), _stream(stream)))
+
+
+def starkv_kv4_evict(ctx, cfg, cache: starkv_kv4_cache, block_table, seq_lens, keep_lens, recent, dst_block_table,
+                     new_lens, kept, stream=None):
+    """Gather the kept tokens (the `recent` last and the heaviest others, per KV head) into other pages."""
+    for t, n in ((block_table, "block_table"), (dst_block_table, "dst_block_table")):
+        _need(t, torch.int32, n, 2)
+    B, cap = block_table.shape[0], dst_block_table.shape[1] * PAGE_TOKENS
+    for t, n in ((seq_lens, "seq_lens"), (keep_lens, "keep_lens"), (new_lens, "new_lens")):
+        _need(t, torch.int32, n, 1)
+        if t.shape[0] != B:
+            raise ValueError(f"{n} and block_table disagree on the batch")
+    _need(kept, torch.int32, "kept", 3)
+    if dst_block_table.shape[0] != B or tuple(kept.shape) != (B, cfg.num_kv_heads, cap):
+        raise ValueError(f"dst_block_table must have {B} rows and kept be [{B}, {cfg.num_kv_heads}, {cap}]")
+    _one_device(block_table, seq_lens, keep_lens, dst_block_table, new_lens, kept)
+    _check(lib().starkv_kv4_evict(ctx, ctypes.byref(cache), _p(block_table), _p(seq_lens), _p(keep_lens), int(recent),
+                                  B, block_table.shape[1], _p(dst_block_table), dst_block_table.shape[1],
+                                  _p(new_lens), _p(kept), _stream(stream)))
+
+
+def _packed(cfg, q, k, cu_q, cu_k):
+    qs = _rows(q, cfg.num_q_heads, cfg.head_dim, "q")
+    ks = _rows(k, cfg.num_kv_heads, cfg.head_dim, "k")
+    _need(cu_q, torch.int32, "cu_q", 1)
+    _need(cu_k, torch.int32, "cu_k", 1)
+    if cu_q.shape[0] != cu_k.shape[0] or cu_q.shape[0] < 1:
+        raise ValueError("cu_q and cu_k must be [batch + 1]")
+    return qs, ks
+
+
+def starkv_prompt_attn(ctx, cfg, q, k, v, cu_q, cu_k, max_q_len, out, lse=None, stream=None):
+    """Causal attention of packed sequences over their own keys and values."""
+    qs, ks = _packed(cfg, q, k, cu_q, cu_k)
+    vs = _rows(v, cfg.num_kv_heads, cfg.head_dim, "v")
+    _need(out, torch.bfloat16, "out", 3)
+    if v.shape[0] != k.shape[0] or tuple(out.shape) != tuple(q.shape):
+        raise ValueError("k and v, or q and out, disagree on their rows")
+    if lse is not None:
+        _need(lse, torch.float32, "lse", 2)
+        if tuple(lse.shape) != tuple(q.shape[:2]):
+            raise ValueError("lse must be [total_q, num_q_heads]")
+    _one_device(q, k, v, cu_q, cu_k, out, lse)
+    _check(lib().starkv_prompt_attn(ctx, _p(q), _p(k), _p(v), qs, ks, vs, _p(cu_q), _p(cu_k), cu_q.shape[0] - 1,
+                                    q.shape[0], k.shape[0], int(max_q_len), _p(out), _p(lse), _stream(stream)))
+
+
+def starkv_prompt_weights(ctx, cfg, q, k, lse, cu_q, cu_k, max_k_len, window, weights, stream=None):
+    """The attention weight that each sequence's last `window` queries give to its keys."""
+    qs, ks = _packed(cfg, q, k, cu_q, cu_k)
+    _need(lse, torch.float32, "lse", 2)
+    _need(weights, torch.float32, "weights", 2)
+    if tuple(lse.shape) != tuple(q.shape[:2]) or tuple(weights.shape) != tuple(k.shape[:2]):
+        raise ValueError("lse must be [total_q, num_q_heads] and weights [total_k, num_kv_heads]")
+    _one_device(q, k, lse, cu_q, cu_k, weights)
+    _check(lib().starkv_prompt_weights(ctx, _p(q), _p(k), qs, ks, _p(lse), _p(cu_q), _p(cu_k), cu_q.shape[0] - 1,
+                                       q.shape[0], k.shape[0], int(max_k_len), int(window), _p(weights),
+                                       _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
 # Convenience wrappers (allocation through torch; no arithmetic)
 # ---------------------------------------------------------------------------
 class LatentCache:
@@ -362,6 +529,50 @@ class LatentCache:
 
     def nbytes(self) -> int:
         return sum(self.sizes[k] for k in ("k_codes_bytes", "v_codes_bytes", "k_meta_bytes", "v_meta_bytes"))
+
+
+class KV4Cache:
+    """The 4-bit paged cache of a full-width layer: pages [n_pages, num_kv_heads, head_page_bytes] and, where tokens'
+    accumulated attention weights are kept, weights [n_pages, num_kv_heads, 16].  Allocated with torch, or the caller's."""
+
+    def __init__(self, cfg: starkv_config, n_pages=None, pages=None, weights=None, keep_weights=False, device="cuda"):
+        if pages is None:
+            if n_pages is None:
+                raise ValueError("n_pages or pages")
+            self.sizes = starkv_kv4_layout(cfg, n_pages)
+            pages = torch.zeros((n_pages, cfg.num_kv_heads, self.sizes["head_page_bytes"]), dtype=torch.uint8,
+                                device=device)
+        else:
+            _need(pages, torch.uint8, "pages", 3)
+            if n_pages is not None and n_pages != pages.shape[0]:
+                raise ValueError("n_pages and pages disagree")
+            n_pages = pages.shape[0]
+            self.sizes = starkv_kv4_layout(cfg, n_pages)
+            if tuple(pages.shape[1:]) != (cfg.num_kv_heads, self.sizes["head_page_bytes"]):
+                raise ValueError(f"pages must be [n_pages, {cfg.num_kv_heads}, {self.sizes['head_page_bytes']}]")
+        if weights is None:
+            if keep_weights:
+                weights = torch.zeros((n_pages, cfg.num_kv_heads, PAGE_TOKENS), dtype=torch.float32, device=pages.device)
+        else:
+            _need(weights, torch.float32, "weights", 3)
+            if tuple(weights.shape) != (n_pages, cfg.num_kv_heads, PAGE_TOKENS):
+                raise ValueError(f"weights must be [{n_pages}, {cfg.num_kv_heads}, {PAGE_TOKENS}]")
+            _one_device(pages, weights)
+        self.n_pages, self.pages, self.weights = n_pages, pages, weights
+        self.struct = starkv_kv4_cache(pages.data_ptr(), None if weights is None else weights.data_ptr(), n_pages)
+
+    def nbytes(self) -> int:
+        return self.sizes["pages_bytes"] + (self.sizes["weights_bytes"] if self.weights is not None else 0)
+
+
+def _new(shape, dtype, device, stream):
+    """An uninitialised tensor that a call on `stream` may use (it is given back behind that stream's work)."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, torch.cuda.Stream):
+        t.record_stream(stream)
+    elif stream is not None:
+        t.record_stream(torch.cuda.ExternalStream(int(stream), device=device))
+    return t
 
 
 class StarKV:
@@ -406,6 +617,53 @@ class StarKV:
         ws = self.workspace(OP_PREFILL, seq_lens.shape[0], block_table.shape[1], q.shape[0])
         starkv_prefill_attn(self.ctx, cache.struct, q, cu_q, block_table, seq_lens, max_q_len, out, ws, stream)
         return out
+
+    # ---- full-width layers (include/starkv_full.h); outputs and workspaces are new tensors of each call
+    def new_kv4_cache(self, n_pages: int, keep_weights=False) -> KV4Cache:
+        return KV4Cache(self.cfg, n_pages, keep_weights=keep_weights)
+
+    def kv4_append(self, cache: KV4Cache, k, v, slot_mapping, weights=None, stream=None):
+        _one_device(k, cache.pages)
+        starkv_kv4_append(self.ctx, self.cfg, cache.struct, k, v, slot_mapping, weights, stream)
+
+    def kv4_read(self, cache: KV4Cache, block_table, cu, total: int, starts=None, stream=None):
+        """Keys and values [total, num_kv_heads, head_dim] of tokens starts[b] .. of each sequence."""
+        k, v = (_new((total, self.cfg.num_kv_heads, self.cfg.head_dim), torch.bfloat16, cache.pages.device, stream)
+                for _ in range(2))
+        starkv_kv4_read(self.ctx, self.cfg, cache.struct, block_table, cu, k, v, starts, stream)
+        return k, v
+
+    def kv4_decode(self, cache: KV4Cache, q, block_table, seq_lens, accumulate=False, out=None, stream=None):
+        _one_device(q, cache.pages)
+        n = starkv_workspace_bytes(self.ctx, OP_KV4_DECODE, block_table.shape[0], block_table.shape[1], int(accumulate))
+        ws = _new((n,), torch.uint8, q.device, stream) if n else None
+        out = _new(q.shape, q.dtype, q.device, stream) if out is None else out
+        starkv_kv4_decode_attn(self.ctx, self.cfg, cache.struct, q, block_table, seq_lens, accumulate, out, ws, stream)
+        return out
+
+    def kv4_evict(self, cache: KV4Cache, block_table, seq_lens, keep_lens, recent: int, dst_block_table, stream=None):
+        """Gather the kept tokens into dst_block_table's pages: their new lengths [batch], and their indices
+        [batch, num_kv_heads, dst_max_pages * 16] (-1 behind the last)."""
+        _one_device(block_table, cache.pages)
+        B, h = block_table.shape[0], self.cfg.num_kv_heads
+        new_lens = _new((B,), torch.int32, block_table.device, stream)
+        kept = _new((B, h, dst_block_table.shape[1] * PAGE_TOKENS), torch.int32, block_table.device, stream)
+        starkv_kv4_evict(self.ctx, self.cfg, cache.struct, block_table, seq_lens, keep_lens, recent, dst_block_table,
+                         new_lens, kept, stream)
+        return new_lens, kept
+
+    def prompt(self, q, k, v, cu_q, cu_k, max_q_len: int, out=None, stream=None):
+        """Causal attention of packed prompts: (out [total_q, H, d], lse [total_q, H])."""
+        out = _new(q.shape, q.dtype, q.device, stream) if out is None else out
+        lse = _new(q.shape[:2], torch.float32, q.device, stream)
+        starkv_prompt_attn(self.ctx, self.cfg, q, k, v, cu_q, cu_k, max_q_len, out, lse, stream)
+        return out, lse
+
+    def prompt_weights(self, q, k, lse, cu_q, cu_k, max_k_len: int, window: int, stream=None):
+        """Attention weight [total_k, num_kv_heads] that each sequence's last `window` queries give to its keys."""
+        weights = _new(k.shape[:2], torch.float32, k.device, stream)
+        starkv_prompt_weights(self.ctx, self.cfg, q, k, lse, cu_q, cu_k, max_k_len, window, weights, stream)
+        return weights
 
     def status(self, stream=None) -> int:
         return starkv_read_device_status(self.ctx, stream)

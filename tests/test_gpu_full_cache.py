@@ -1,0 +1,370 @@
+"""GPU tests of the 4-bit cache of full-width layers: append, read back, decode attention, eviction."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import full_oracle as F
+
+from _full import SHAPES, bf16, context, cu_of, fill, i32, keys, score_error, skv, tables
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------------------------------------------------
+# append and read
+# ---------------------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("new", [[1], [0, 17, 1], [40, 33]])
+def test_append_writes_the_oracles_bytes_and_no_others(shape, new):
+    H, h, d = shape
+    rng = np.random.default_rng(len(new) + H)
+    kv = context(*shape)
+    starts = [5 + 3 * b for b in range(len(new))]
+    t, _, n_pages = tables(rng, [s + n for s, n in zip(starts, new)])
+    pages = rng.integers(0, 256, (n_pages, h, F.page_bytes(d)), dtype=np.uint8)
+    n = sum(new)
+    kd, k = keys(rng, n, h, d)
+    vd, v = bf16(rng, n, h, d)
+    slots = np.concatenate([F.slots_of(t[b], m, s) for b, (s, m) in enumerate(zip(starts, new))])
+    slots[-1:] = -1 if n > 1 else slots[-1:]  # a token that is skipped
+    w0 = rng.standard_normal((n_pages, h, 16)).astype(np.float32)
+    first = rng.standard_normal((n, h)).astype(np.float32)
+    for given in (None, first):
+        want, ww = pages.copy(), w0.copy()
+        F.write(want, k, v, slots)
+        for i, s in enumerate(slots):
+            if s >= 0:
+                ww[s // 16, :, s % 16] = 0 if given is None else given[i]
+        cache = skv().KV4Cache(kv.cfg, pages=torch.from_numpy(pages.copy()).cuda(), weights=torch.from_numpy(w0.copy()).cuda())
+        kv.kv4_append(cache, kd, vd, torch.from_numpy(slots).cuda(), None if given is None else torch.from_numpy(given).cuda())
+        assert kv.status() == 0
+        np.testing.assert_array_equal(cache.pages.cpu().numpy(), want)
+        np.testing.assert_array_equal(cache.weights.cpu().numpy(), ww)
+
+
+def test_append_of_rows_that_are_parts_of_one_projection():
+    H, h, d = 8, 2, 64
+    rng = np.random.default_rng(3)
+    kv = context(H, h, d)
+    qkvd, qkv = bf16(rng, 21, H + 2 * h, d)
+    t, _, n_pages = tables(rng, [21])
+    slots = F.slots_of(t[0], 21)
+    want = np.zeros((n_pages, h, F.page_bytes(d)), np.uint8)
+    F.write(want, qkv[:, H:H + h], qkv[:, H + h:], slots)
+    cache = kv.new_kv4_cache(n_pages)
+    kv.kv4_append(cache, qkvd[:, H:H + h], qkvd[:, H + h:], torch.from_numpy(slots).cuda())
+    np.testing.assert_array_equal(cache.pages.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan"), 1e30, -1e6])
+def test_append_of_a_group_that_fp16_cannot_hold(value):
+    S = skv()
+    H, h, d = 4, 2, 128
+    rng = np.random.default_rng(4)
+    kv = context(H, h, d)
+    kd, _ = keys(rng, 3, h, d)
+    vd, _ = bf16(rng, 3, h, d)
+    kd[1, 0, 40] = value
+    k, v = kd.float().cpu().numpy(), vd.float().cpu().numpy()
+    want = np.zeros((1, h, F.page_bytes(d)), np.uint8)
+    assert F.write(want, k, v, [3, 4, 5])
+    cache = kv.new_kv4_cache(1)
+    kv.kv4_append(cache, kd, vd, torch.tensor([3, 4, 5], device="cuda"))
+    assert kv.status() == S.DEV_QUANT_OVERFLOW
+    np.testing.assert_array_equal(cache.pages.cpu().numpy(), want)
+
+
+def test_append_of_equal_channels_and_bad_slots():
+    S = skv()
+    H, h, d = 4, 4, 64
+    rng = np.random.default_rng(5)
+    kv = context(H, h, d)
+    kd, k = keys(rng, 4, h, d)
+    vd = torch.full((4, h, d), 0.3, device="cuda").bfloat16()  # no spread: code 0, scale 0
+    slots = [7, 32, 1 << 40, -5]                                # two pages: slot 32 is beyond them
+    want = np.zeros((2, h, F.page_bytes(d)), np.uint8)
+    F.write(want, k, vd.float().cpu().numpy(), [7, -1, -1, -1])
+    cache = kv.new_kv4_cache(2)
+    kv.kv4_append(cache, kd, vd, torch.tensor(slots, device="cuda"))
+    assert kv.status() == S.DEV_BAD_SLOT
+    np.testing.assert_array_equal(cache.pages.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+def test_read_returns_the_stored_values_in_bf16(shape):
+    H, h, d = shape
+    rng = np.random.default_rng(H)
+    kv = context(*shape)
+    lens, starts = [35, 0, 1, 20], [3, 0, 0, 7]
+    pages, t, _ = fill(rng, [n + s for n, s in zip(lens, starts)], h, d)
+    cache = skv().KV4Cache(kv.cfg, pages=torch.from_numpy(pages).cuda())
+    got = kv.kv4_read(cache, i32(t), i32(cu_of(lens)), sum(lens), starts=i32(starts))
+    assert kv.status() == 0
+    slots = np.concatenate([F.slots_of(t[b], n, s) for b, (n, s) in enumerate(zip(lens, starts))])
+    for x, y in zip(got, F.values(pages, slots, d)):
+        # code * s + z is one fp32 rounding from the 64-bit value, and bf16 another
+        want = torch.from_numpy(y.astype(np.float32)).bfloat16().float().numpy()
+        np.testing.assert_array_equal(x.float().cpu().numpy(), want)
+
+
+def test_read_of_bad_pages_lengths_and_spans():
+    S = skv()
+    H, h, d = 4, 2, 64
+    rng = np.random.default_rng(6)
+    kv = context(H, h, d)
+    pages, t, _ = fill(rng, [40, 40], h, d)
+    cache = S.KV4Cache(kv.cfg, pages=torch.from_numpy(pages).cuda())
+    good = F.values(pages, F.slots_of(t[0], 40), d)[0]
+    bad = t.copy()
+    bad[0, 1] = len(pages)
+    k, _ = kv.kv4_read(cache, i32(bad), i32([0, 40, 40]), 40)
+    assert kv.status() == S.DEV_BAD_PAGE
+    assert (k[16:32] == 0).all() and np.abs(k[:16].float().cpu().numpy() - good[:16]).max() < 0.1
+    k, _ = kv.kv4_read(cache, i32(t), i32([0, 50, 50]), 50)  # three pages hold 48
+    assert kv.status() == S.DEV_BAD_SEQ_LEN and (k[48:] == 0).all()
+    k, _ = kv.kv4_read(cache, i32(t), i32([0, 9, 4]), 9)     # the last bound is not the row count
+    assert kv.status() == S.DEV_BAD_QUERY_SPAN and (k == 0).all()
+
+
+# ---------------------------------------------------------------------------------------------------------------------
+# decode attention
+# ---------------------------------------------------------------------------------------------------------------------
+def check_decode(shape, lens, accumulate, seed=0, q_scale=1.0, kv=None, stream=None):
+    H, h, d = shape
+    rng = np.random.default_rng(seed)
+    kv = kv or context(*shape)
+    pages, t, _ = fill(rng, lens, h, d)
+    qd, q = bf16(rng, len(lens), H, d, scale=q_scale)
+    w0 = rng.random((len(pages), h, 16)).astype(np.float32)
+    cache = skv().KV4Cache(kv.cfg, pages=torch.from_numpy(pages).cuda(), weights=torch.from_numpy(w0).cuda())
+    torch.cuda.synchronize()
+    out = kv.kv4_decode(cache, qd, i32(t), i32(lens), accumulate=accumulate, stream=stream)
+    assert kv.status(stream) == 0
+    out = out.double().cpu().numpy()
+    want_w, tol_w = w0.astype(np.float64), np.zeros(w0.shape)
+    for b, n in enumerate(lens):
+        slots = F.slots_of(t[b], n)
+        k, v = F.values(pages, slots, d)
+        o, _, p, mag = F.attend(q[b:b + 1].astype(np.float64), k, v, [n])
+        es = score_error(q[b:b + 1], k)[0] if n else np.zeros(H)
+        # v: fp16, 2^-11 of its magnitude (code * s + z may cancel: 2^-11 of the group's largest value instead);
+        # p: fp16 against a maximum whose p is 1, 2^-11 and 2^-25 a token; the score's error twice (numerator, sum)
+        vmax = np.abs(v).max() if n else 0.0
+        tol = 2.0**-8 * np.abs(o[0]) + mag[0] * (2.0**-11 + 2 * es[:, None] + 2.0**-20) + 2.0**-11 * vmax + n * 2.0**-25 * vmax
+        assert (np.abs(out[b] - o[0]) <= tol).all(), (b, n, np.abs(out[b] - o[0]).max())
+        if n:
+            add = p[0].reshape(h, H // h, n).sum(1)
+            err = (p[0] * (2 * es[:, None] + 2.0**-19)).reshape(h, H // h, n).sum(1)  # ex2, 1 / sum, G additions
+            want_w[slots // 16, :, slots % 16] += add.T
+            tol_w[slots // 16, :, slots % 16] += err.T
+    if accumulate:
+        got = cache.weights.double().cpu().numpy()
+        assert (np.abs(got - want_w) <= tol_w + 2.0**-23 * np.abs(want_w)).all()
+    else:
+        np.testing.assert_array_equal(cache.weights.cpu().numpy(), w0)
+    np.testing.assert_array_equal(cache.pages.cpu().numpy(), pages)
+
+
+@pytest.mark.parametrize("shape", SHAPES + [(24, 1, 64), (80, 2, 64)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_decode_small(shape, accumulate):
+    check_decode(shape, [1, 16, 0, 17, 100], accumulate, seed=sum(shape))
+
+
+@pytest.mark.parametrize("shape", [(4, 4, 64), (14, 2, 64), (8, 2, 128)])
+@pytest.mark.parametrize("lens", [[1500], [333, 0, 1027]])
+def test_decode_of_several_splits(shape, lens):
+    check_decode(shape, lens, True, seed=len(lens))
+
+
+def test_decode_with_scores_far_apart():
+    check_decode((8, 2, 128), [400, 90], True, seed=2, q_scale=30.0)
+    check_decode((8, 2, 128), [400, 90], True, seed=2, q_scale=1e-3)
+
+
+def test_decode_of_empty_sequences_only():
+    check_decode((8, 2, 64), [0, 0, 0], True)
+
+
+def test_decode_leaves_out_bad_pages_and_lengths():
+    S = skv()
+    H, h, d = 8, 2, 64
+    rng = np.random.default_rng(8)
+    kv = context(H, h, d)
+    pages, t, _ = fill(rng, [40, 30, 20], h, d)
+    cache = S.KV4Cache(kv.cfg, pages=torch.from_numpy(pages).cuda(), weights=torch.zeros((len(pages), h, 16), device="cuda"))
+    qd, q = bf16(rng, 3, H, d)
+    bad = t.copy()
+    bad[1, 0] = -3
+    out = kv.kv4_decode(cache, qd, i32(bad), i32([40, 30, 99]), accumulate=True).double().cpu().numpy()
+    assert kv.status() == S.DEV_BAD_PAGE | S.DEV_BAD_SEQ_LEN
+    k, v = F.values(pages, F.slots_of(t[1], 30)[16:], d)
+    want = F.attend(q[1:2].astype(np.float64), k, v, [14])[0][0]
+    assert np.abs(out[1] - want).max() < 2.0**-7 * max(1, np.abs(want).max()) + 2.0**-9 * np.abs(v).max()
+    assert (out[2] == 0).all()
+    w = cache.weights.double().cpu().numpy()
+    assert abs(w[t[0, :3]].sum() - H) < 1e-4 and abs(w[t[1, 1]].sum() - H) < 1e-4 and w.sum() < 2 * H + 1e-3
+
+
+def test_decode_is_the_same_each_time_and_on_another_stream():
+    S = skv()
+    H, h, d = 14, 2, 64
+    rng = np.random.default_rng(9)
+    kv = context(H, h, d)
+    pages, t, _ = fill(rng, [700, 300], h, d)
+    cache = S.KV4Cache(kv.cfg, pages=torch.from_numpy(pages).cuda())
+    qd, _ = bf16(rng, 2, H, d)
+    td, ld = i32(t), i32([700, 300])
+    first = kv.kv4_decode(cache, qd, td, ld)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(4):
+        other = kv.kv4_decode(cache, qd, td, ld, stream=side)
+        again = kv.kv4_decode(cache, qd, td, ld)  # two calls at once
+        torch.cuda.synchronize()
+        assert torch.equal(first, again) and torch.equal(first, other)
+
+
+# ---------------------------------------------------------------------------------------------------------------------
+# eviction
+# ---------------------------------------------------------------------------------------------------------------------
+def check_evict(shape, lens, keeps, recent, seed=0, weights=None, alias=False):
+    S = skv()
+    H, h, d = shape
+    rng = np.random.default_rng(seed)
+    kv = context(*shape)
+    room = [-(-min(n, k) // 16) for n, k in zip(lens, keeps)]
+    pages, t, spare = fill(rng, lens, h, d, extra=sum(room))
+    dst = np.zeros((len(lens), max(1, max(room))), np.int32)
+    at = 0
+    for b, r in enumerate(room):
+        dst[b, :r] = spare[at:at + r]
+        at += r
+    w0 = np.exp(1.5 * rng.standard_normal((len(pages), h, 16))).astype(np.float32) if weights is None else weights(rng, (len(pages), h, 16))
+    cache = S.KV4Cache(kv.cfg, pages=torch.from_numpy(pages.copy()).cuda(), weights=torch.from_numpy(w0.copy()).cuda())
+    ld, kd = i32(lens), i32(keeps)
+    if alias:
+        kept = torch.empty((len(lens), h, dst.shape[1] * 16), dtype=torch.int32, device="cuda")
+        S.starkv_kv4_evict(kv.ctx, kv.cfg, cache.struct, i32(t), ld, kd, recent, i32(dst), ld, kept)
+        new = ld
+    else:
+        new, kept = kv.kv4_evict(cache, i32(t), ld, kd, recent, i32(dst))
+    assert kv.status() == 0
+    np.testing.assert_array_equal(new.cpu().numpy(), np.minimum(lens, keeps))
+    want_p, want_w = pages.copy(), w0.copy()
+    want_kept = np.full((len(lens), h, dst.shape[1] * 16), -1, np.int32)
+    ng = d // 32
+    planes = [(0, d // 2), (8 * d, d // 2), (16 * d, 4 * ng), (16 * d + 64 * ng, 4 * ng)]
+    for b, (n, keep) in enumerate(zip(lens, keeps)):
+        src = F.slots_of(t[b], n)
+        for head in range(h):
+            stay = F.kept_tokens(w0[src // 16, head, src % 16], n, keep, recent)
+            want_kept[b, head, :len(stay)] = stay
+            for i, j in enumerate(stay):
+                s, o = src[j], F.slots_of(dst[b], 1, i)[0]
+                for base, row in planes:
+                    want_p[o // 16, head, base + o % 16 * row:base + (o % 16 + 1) * row] = \
+                        pages[s // 16, head, base + s % 16 * row:base + (s % 16 + 1) * row]
+                want_w[o // 16, head, o % 16] = w0[s // 16, head, s % 16]
+    np.testing.assert_array_equal(kept.cpu().numpy(), want_kept)
+    np.testing.assert_array_equal(cache.pages.cpu().numpy(), want_p)
+    np.testing.assert_array_equal(cache.weights.cpu().numpy().view(np.int32), want_w.view(np.int32))
+
+
+@pytest.mark.parametrize("shape", [(4, 4, 64), (8, 2, 128)])
+@pytest.mark.parametrize("recent", [0, 1, 8, 10**6])
+def test_evict(shape, recent):
+    check_evict(shape, [100, 0, 1, 33, 16], [40, 5, 1, 33, 0], recent, seed=recent % 7)
+
+
+def test_evict_with_lengths_written_in_place():
+    check_evict((8, 2, 64), [70, 20, 50], [10, 30, 49], 4, alias=True)
+
+
+@pytest.mark.parametrize("n", [1025, 4000])
+def test_evict_longer(n):
+    check_evict((2, 1, 64), [n], [n // 3], 17, seed=n)
+
+
+def test_evict_of_equal_weights_takes_the_lowest_index():
+    check_evict((4, 2, 64), [90, 50], [30, 20], 4, weights=lambda rng, s: np.zeros(s, np.float32))
+    check_evict((4, 2, 64), [90, 50], [30, 20], 4, weights=lambda rng, s: rng.integers(0, 3, s).astype(np.float32))
+    check_evict((4, 2, 64), [90], [30], 4, weights=lambda rng, s: np.where(rng.random(s) < 0.5, -0.0, 0.0).astype(np.float32))
+
+
+def test_evict_of_weights_that_are_not_finite():
+    def weights(rng, s):
+        w = rng.standard_normal(s).astype(np.float32)
+        kind = rng.integers(0, 4, s)
+        return np.where(kind == 0, np.float32("nan"), np.where(kind == 1, np.float32("inf"), np.where(kind == 2, np.float32("-inf"), w))).astype(np.float32)
+    for keep in (10, 60, 85):
+        check_evict((4, 2, 64), [90], [keep], 3, weights=weights)
+
+
+def test_evict_skips_bad_lengths_and_pages():
+    S = skv()
+    H, h, d = 4, 2, 64
+    rng = np.random.default_rng(11)
+    kv = context(H, h, d)
+    pages, t, spare = fill(rng, [40, 40, 40, 40], h, d, extra=4)
+    w0 = rng.random((len(pages), h, 16)).astype(np.float32)
+    cache = S.KV4Cache(kv.cfg, pages=torch.from_numpy(pages.copy()).cuda(), weights=torch.from_numpy(w0).cuda())
+    bad = t.copy()
+    bad[1, 2] = len(pages)
+    new, kept = kv.kv4_evict(cache, i32(bad), i32([49, 40, -1, 40]), i32([8, 8, 8, 17]), 2, i32(spare.reshape(4, 1)))
+    assert kv.status() == S.DEV_BAD_PAGE | S.DEV_BAD_SEQ_LEN
+    assert new.tolist() == [0, 0, 0, 0] and (kept == -1).all()
+    np.testing.assert_array_equal(cache.pages.cpu().numpy(), pages)
+
+
+# ---------------------------------------------------------------------------------------------------------------------
+# captured
+# ---------------------------------------------------------------------------------------------------------------------
+def test_steps_captured_into_graphs_that_run_in_turn():
+    """Append, decode and evict in two graphs of one context, replayed with other inputs: the same as plain calls."""
+    S = skv()
+    H, h, d = 8, 2, 64
+    rng = np.random.default_rng(12)
+    kv = context(H, h, d)
+    pages, t, spare = fill(rng, [90, 70], h, d, extra=8)
+    td, dst = i32(t), i32(spare.reshape(2, 4))
+    lens, keeps = i32([90, 70]), i32([60, 33])
+    qs = [bf16(rng, 2, H, d)[0] for _ in range(3)]
+    ks = [bf16(rng, 2, h, d)[0] for _ in range(3)]
+    slots = torch.tensor([F.slots_of(t[0], 1, 89)[0], F.slots_of(t[1], 1, 69)[0]], device="cuda")
+
+    def fresh():
+        return S.KV4Cache(kv.cfg, pages=torch.from_numpy(pages.copy()).cuda(), keep_weights=True)
+
+    def step(cache, q, k):
+        kv.kv4_append(cache, k, k, slots)
+        out = kv.kv4_decode(cache, q, td, lens, accumulate=True)
+        return out, *kv.kv4_evict(cache, td, lens, keeps, 5, dst)
+
+    plain, want = fresh(), []
+    for q, k in zip(qs, ks):
+        want.append([x.clone() for x in step(plain, q, k)])
+    graphs = []
+    for _ in range(2):
+        cache, q, k = fresh(), qs[0].clone(), ks[0].clone()
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            step(cache, q, k)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = step(cache, q, k)
+        cache.pages.copy_(torch.from_numpy(pages))
+        cache.weights.zero_()
+        graphs.append((g, cache, q, k, out))
+    for i in range(3):
+        for g, cache, q, k, out in graphs:
+            q.copy_(qs[i])
+            k.copy_(ks[i])
+            g.replay()
+        for g, cache, q, k, out in graphs:
+            for x, y in zip(out, want[i]):
+                assert torch.equal(x, y)
+    for g, cache, *_ in graphs:
+        assert torch.equal(cache.pages, plain.pages) and torch.equal(cache.weights, plain.weights)
+    assert kv.status() == 0

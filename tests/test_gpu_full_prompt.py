@@ -1,0 +1,301 @@
+"""GPU tests of full-width prompts: packed causal attention, its weights, and the run from a prompt to evicted decode."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import full_oracle as F
+
+from _full import SHAPES, bf16, context, cu_of, i32, keys, score_error, skv, tables
+
+pytestmark = pytest.mark.gpu
+
+
+def inputs(rng, shape, n_q, n_k, q_scale=1.0):
+    H, h, d = shape
+    qd, _ = bf16(rng, sum(n_q), H, d, scale=q_scale)
+    kd, _ = keys(rng, sum(n_k), h, d)
+    vd, _ = bf16(rng, sum(n_k), h, d)
+    return qd, kd, vd
+
+
+def check_prompt(kv, shape, q, k, v, n_q, n_k, out, lse, weights=None, window=0):
+    """out, lse (and the weights of the last `window` queries) of device inputs against the oracle."""
+    H, h, d = shape
+    q, k, v = (x.double().cpu().numpy() for x in (q, k, v))
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    cq, ck = cu_of(n_q), cu_of(n_k)
+    for b, (n, m) in enumerate(zip(n_q, n_k)):
+        Q, K, V = q[cq[b]:cq[b + 1]], k[ck[b]:ck[b + 1]], v[ck[b]:ck[b + 1]]
+        seen = [m - n + i + 1 for i in range(n)]
+        o, ls, p, mag = F.attend(Q, K, V, seen)
+        es = score_error(Q, K)
+        got, gl = out[cq[b]:cq[b + 1]], lse[cq[b]:cq[b + 1]]
+        # p in bf16 (2^-8 at most), the result in bf16, the score's error in numerator and sum, ex2 and fp32 sums
+        tol = 2.0**-8 * (np.abs(o) + mag) + mag * (2 * es[..., None] + 2.0**-18)
+        assert (np.abs(got - o) <= tol).all(), (b, n, m, np.abs(got - o).max())
+        none = np.isinf(ls)
+        assert (np.isneginf(gl) == none).all()
+        tl = es + 2.0**-18 + 2.0**-22 * np.abs(np.where(none, 0, ls))
+        assert (np.abs(np.where(none, 0, gl) - np.where(none, 0, ls)) <= tl).all()
+        if weights is not None:
+            w = weights[ck[b]:ck[b + 1]].double().cpu().numpy()
+            x = p[max(0, n - window):] if window else p[:0]
+            e = es[max(0, n - window):] if window else es[:0]
+            want = x.reshape(len(x), h, H // h, m).sum((0, 2)).T
+            # each p by the score's error twice (its own, and lse's), lse's rounding, ex2, and a sum of fewer than 2^12 terms
+            tw = (x * (2 * e[..., None] + 2.0**-17)).reshape(len(x), h, H // h, m).sum((0, 2)).T + 2.0**-24
+            assert (np.abs(w - want) <= tw + 2.0**-14 * want).all(), (b, np.abs(w - want).max())
+
+
+def run(shape, n_q, n_k, window=0, seed=0, q_scale=1.0):
+    rng = np.random.default_rng(seed)
+    kv = context(*shape)
+    q, k, v = inputs(rng, shape, n_q, n_k, q_scale)
+    cq, ck = i32(cu_of(n_q)), i32(cu_of(n_k))
+    out, lse = kv.prompt(q, k, v, cq, ck, max(n_q))
+    w = kv.prompt_weights(q, k, lse, cq, ck, max(n_k), window)
+    assert kv.status() == 0
+    check_prompt(kv, shape, q, k, v, n_q, n_k, out, lse, w, window)
+
+
+@pytest.mark.parametrize("shape", SHAPES + [(40, 1, 64), (150, 1, 64)])
+def test_prompt_small(shape):
+    run(shape, [1, 2, 0, 40], [1, 2, 0, 40], window=7)
+
+
+@pytest.mark.parametrize("shape", [(4, 4, 64), (14, 2, 64), (8, 8, 128), (12, 4, 128)])
+@pytest.mark.parametrize("n_q,n_k", [([130], [130]), ([257, 64], [257, 64]), ([300], [700]), ([5, 1], [513, 300])])
+def test_prompt_tiles(shape, n_q, n_k):
+    run(shape, n_q, n_k, window=50, seed=n_q[0])
+
+
+@pytest.mark.parametrize("shape", [(8, 2, 64), (8, 8, 128)])
+def test_prompt_of_more_queries_than_keys(shape):
+    run(shape, [150, 3, 20], [40, 0, 300], window=10**6, seed=3)
+
+
+def test_prompt_without_any_key():
+    kv = context(8, 2, 64)
+    rng = np.random.default_rng(1)
+    q, k, v = inputs(rng, (8, 2, 64), [5], [0])
+    out, lse = kv.prompt(q, k, v, i32([0, 5]), i32([0, 0]), 5)
+    assert kv.status() == 0 and (out == 0).all() and torch.isneginf(lse).all()
+
+
+def test_weights_without_any_query():
+    kv = context(8, 2, 64)
+    rng = np.random.default_rng(1)
+    q, k, _ = inputs(rng, (8, 2, 64), [0], [200])
+    w = kv.prompt_weights(q, k, torch.empty((0, 8), device="cuda"), i32([0, 0]), i32([0, 200]), 200, 10)
+    assert kv.status() == 0 and (w == 0).all()
+
+
+@pytest.mark.parametrize("window", [0, 1, 64, 129, 1000])
+def test_weights_of_a_window(window):
+    run((14, 2, 64), [200, 0, 33], [260, 0, 33], window=window, seed=window)
+
+
+def test_prompt_with_scores_far_apart():
+    run((8, 2, 128), [200], [200], window=200, q_scale=30.0)   # the running maximum moves often
+    run((8, 2, 128), [200], [200], window=200, q_scale=1e-4)
+
+
+def test_prompt_rising_scores_move_the_maximum():
+    """Keys that grow along the sequence: each tile's scores pass those before by far more than 2^8."""
+    shape = (4, 4, 64)
+    rng = np.random.default_rng(5)
+    kv = context(*shape)
+    q, k, v = inputs(rng, shape, [600], [600])
+    q = q.abs()
+    k = (k.abs() * torch.linspace(0.1, 6, 600, device="cuda")[:, None, None]).bfloat16()
+    cu = i32([0, 600])
+    out, lse = kv.prompt(q, k, v, cu, cu, 600)
+    w = kv.prompt_weights(q, k, lse, cu, cu, 600, 600)
+    assert kv.status() == 0
+    check_prompt(kv, shape, q, k, v, [600], [600], out, lse, w, 600)
+
+
+@pytest.mark.parametrize("shape", [(8, 2, 64), (4, 4, 128)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_values_that_are_not_finite_reach_only_the_rows_that_see_them(shape, bad):
+    H, h, d = shape
+    rng = np.random.default_rng(6)
+    kv = context(*shape)
+    n = [300, 90, 40]
+    q, k, v = inputs(rng, shape, n, n)
+    cu = i32(cu_of(n))
+    clean, _ = kv.prompt(q, k, v, cu, cu, 300)
+    at, ch = 250, 17
+    k2, v2 = k.clone(), v.clone()
+    v2[at, 0, ch] = bad          # inside sequence 0
+    v2[300:, :, :] = bad         # all of sequences 1 and 2, behind sequence 0's last tile
+    k2[300:, :, :] = float("nan")
+    out, lse = kv.prompt(q, k2, v2, cu, cu, 300)
+    a, b = out[:300].clone(), clean[:300].clone()
+    hit = a[at:, :H // h, ch].float()
+    assert (torch.isnan(hit) if bad != bad else hit == bad).all()
+    a[at:, :H // h, ch] = 0
+    b[at:, :H // h, ch] = 0
+    assert torch.equal(a, b)
+    w = kv.prompt_weights(q, k2, lse, cu, cu, 300, 300)
+    assert torch.isfinite(w[:300]).all()
+
+
+def test_queries_that_are_not_finite_stay_in_their_rows():
+    shape = (8, 2, 64)
+    rng = np.random.default_rng(7)
+    kv = context(*shape)
+    q, k, v = inputs(rng, shape, [200, 50], [200, 50])
+    cu = i32([0, 200, 250])
+    clean, lse0 = kv.prompt(q, k, v, cu, cu, 200)
+    q2 = q.clone()
+    q2[60, 3] = float("nan")
+    q2[200:] = float("inf")
+    out, lse = kv.prompt(q2, k, v, cu, cu, 200)
+    assert torch.isnan(out[60, 3]).all() and torch.isnan(lse[60, 3])
+    keep = torch.ones((200, 8), dtype=torch.bool)
+    keep[60, 3] = False
+    assert torch.equal(out[:200][keep], clean[:200][keep]) and torch.equal(lse[:200][keep], lse0[:200][keep])
+    w0 = kv.prompt_weights(q, k, lse0, cu, cu, 200, 100)
+    w = kv.prompt_weights(q2, k, lse, cu, cu, 200, 100)  # query 60 is outside the window
+    assert torch.equal(w[:200], w0[:200])
+
+
+def test_rows_of_one_projection():
+    shape = H, h, d = 8, 2, 64
+    rng = np.random.default_rng(8)
+    kv = context(*shape)
+    x, _ = bf16(rng, 150, H + 2 * h, d)
+    q, k, v = x[:, :H], x[:, H:H + h], x[:, H + h:]
+    cu = i32([0, 150])
+    out, lse = kv.prompt(q, k, v, cu, cu, 150)
+    w = kv.prompt_weights(q, k, lse, cu, cu, 150, 20)
+    again, lse2 = kv.prompt(q.contiguous(), k.contiguous(), v.contiguous(), cu, cu, 150)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    check_prompt(kv, shape, q, k, v, [150], [150], out, lse, w, 20)
+
+
+def test_bad_spans_leave_their_rows():
+    S = skv()
+    shape = (8, 2, 64)
+    rng = np.random.default_rng(9)
+    kv = context(*shape)
+    q, k, v = inputs(rng, shape, [60, 40], [60, 40])
+    out, lse = torch.full_like(q, 7), torch.full((100, 8), 7.0, device="cuda")
+    w = torch.full((100, 2), 7.0, device="cuda")
+    cases = [([0, 60, 40], [0, 60, 100], 60, 100), ([0, 60, 100], [0, 120, 100], 60, 100), ([0, 60, 100], [0, 60, 100], 30, 30)]
+    for cq, ck, mq, mk in cases:
+        S.starkv_prompt_attn(kv.ctx, kv.cfg, q, k, v, i32(cq), i32(ck), mq, out, lse)
+        assert kv.status() == S.DEV_BAD_QUERY_SPAN
+        S.starkv_prompt_weights(kv.ctx, kv.cfg, q, k, torch.zeros_like(lse), i32(cq), i32(ck), mk, 10, w)
+        assert kv.status() == S.DEV_BAD_QUERY_SPAN
+    S.starkv_prompt_attn(kv.ctx, kv.cfg, q, k, v, i32([0, 60, 100]), i32([0, 60, 90]), 60, out, lse)
+    assert kv.status() == S.DEV_BAD_QUERY_SPAN
+    assert (out[60:] == 7).all() and (lse[60:] == 7).all()
+
+
+def test_prompt_captured_and_on_another_stream():
+    shape = (8, 2, 128)
+    rng = np.random.default_rng(10)
+    kv = context(*shape)
+    q, k, v = inputs(rng, shape, [300, 77], [300, 77])
+    cu = i32([0, 300, 377])
+    out, lse = kv.prompt(q, k, v, cu, cu, 300)
+    w = kv.prompt_weights(q, k, lse, cu, cu, 300, 64)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    o2, l2 = kv.prompt(q, k, v, cu, cu, 300, stream=side)
+    o3, l3 = kv.prompt(q, k, v, cu, cu, 300)  # two calls at once
+    w2 = kv.prompt_weights(q, k, l2, cu, cu, 300, 64, stream=side)
+    torch.cuda.synchronize()
+    for a, b in ((o2, out), (o3, out), (l2, lse), (l3, lse), (w2, w)):
+        assert torch.equal(a, b)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o4, l4 = kv.prompt(q, k, v, cu, cu, 300)
+        w4 = kv.prompt_weights(q, k, l4, cu, cu, 300, 64)
+    keep = [x.clone() for x in (q, k, v)]
+    for x in (q, k, v):
+        x.copy_(torch.randn_like(x))
+    g.replay()
+    want = kv.prompt(q, k, v, cu, cu, 300)
+    assert torch.equal(o4, want[0]) and torch.equal(l4, want[1])
+    for x, y in zip((q, k, v), keep):
+        x.copy_(y)
+    g.replay()
+    assert torch.equal(o4, out) and torch.equal(l4, lse) and torch.equal(w4, w)
+    assert kv.status() == 0
+
+
+@pytest.mark.parametrize("shape", [(8, 2, 64), (8, 4, 128)])
+def test_from_a_prompt_in_two_chunks_to_decode_behind_an_eviction(shape):
+    """A full-width layer's life: a first chunk attends and is cached, a second chunk attends to the cache read back and
+    itself, its last queries' weights join the cache, the cache is evicted, and decode steps go on in what is kept."""
+    H, h, d = shape
+    rng = np.random.default_rng(13)
+    kv = context(*shape)
+    n1, n2, keep, recent, window = [70, 33], [40, 90], [50, 60], 8, 16
+    total = [a + b for a, b in zip(n1, n2)]
+    steps = 3
+    room = [-(-(k + steps) // 16) for k in keep]
+    t, spare, n_pages = tables(rng, total, extra=sum(room))
+    dst = np.zeros((2, max(room)), np.int32)
+    dst[0, :room[0]], dst[1, :room[1]] = spare[:room[0]], spare[room[0]:]
+    cache = kv.new_kv4_cache(n_pages, keep_weights=True)
+    td = i32(t)
+
+    def slots(table, starts, lens):
+        return torch.from_numpy(np.concatenate([F.slots_of(table[b], n, s) for b, (s, n) in enumerate(zip(starts, lens))])).cuda()
+
+    # first chunk
+    q1, k1, v1 = inputs(rng, shape, n1, n1)
+    c1 = i32(cu_of(n1))
+    o1, l1 = kv.prompt(q1, k1, v1, c1, c1, max(n1))
+    check_prompt(kv, shape, q1, k1, v1, n1, n1, o1, l1)
+    kv.kv4_append(cache, k1, v1, slots(t, [0, 0], n1))
+    # second chunk: keys and values of the first come back from the cache
+    q2, k2, v2 = inputs(rng, shape, n2, n2)
+    kv.kv4_append(cache, k2, v2, slots(t, n1, n2))
+    ct = i32(cu_of(total))
+    ka, va = kv.kv4_read(cache, td, ct, sum(total))
+    o2, l2 = kv.prompt(q2, ka, va, i32(cu_of(n2)), ct, max(n2))
+    w = kv.prompt_weights(q2, ka, l2, i32(cu_of(n2)), ct, max(total), window)
+    check_prompt(kv, shape, q2, ka, va, n2, total, o2, l2, w, window)
+    # the weights enter with the tokens, and eviction goes by them
+    kv.kv4_append(cache, ka, va, slots(t, [0, 0], total), w)
+    wc = cache.weights.cpu().numpy()
+    pages = cache.pages.cpu().numpy()
+    lens, kept = kv.kv4_evict(cache, td, i32(total), i32(keep), recent, i32(dst))
+    for b in range(2):
+        src = F.slots_of(t[b], total[b])
+        for head in range(h):
+            want = F.kept_tokens(wc[src // 16, head, src % 16], total[b], keep[b], recent)
+            np.testing.assert_array_equal(kept[b, head, :keep[b]].cpu().numpy(), want)
+    # decode steps behind it
+    kk, vv = [], []
+    for b in range(2):
+        k, v = F.values(pages, F.slots_of(t[b], total[b]), d)
+        stay = kept[b, :, :keep[b]].cpu().numpy()
+        kk.append(np.stack([k[stay[i], i] for i in range(h)], 1))
+        vv.append(np.stack([v[stay[i], i] for i in range(h)], 1))
+    lens = lens.cpu().numpy()
+    for step in range(steps):
+        q, k, v = inputs(rng, shape, [1, 1], [1, 1])
+        at = slots(dst, lens, [1, 1])
+        kv.kv4_append(cache, k, v, at)
+        lens = lens + 1
+        out = kv.kv4_decode(cache, q, i32(dst), i32(lens), accumulate=True).double().cpu().numpy()
+        now = cache.pages.cpu().numpy()
+        for b in range(2):
+            k, v = F.values(now, at[b:b + 1].cpu().numpy(), d)
+            kk[b], vv[b] = np.concatenate([kk[b], k]), np.concatenate([vv[b], v])
+            o, _, _, mag = F.attend(q[b:b + 1].double().cpu().numpy(), kk[b], vv[b], [len(kk[b])])
+            assert (np.abs(out[b] - o[0]) <= 2.0**-8 * np.abs(o[0]) + 2.0**-10 * (mag[0] + np.abs(vv[b]).max())).all()
+    got = cache.weights.cpu().numpy()
+    for b in range(2):
+        s = F.slots_of(dst[b], lens[b])
+        src = F.slots_of(t[b], total[b])
+        stay = kept[b, :, :keep[b]].cpu().numpy()
+        before = sum(wc[src[stay[i]] // 16, i, src[stay[i]] % 16].sum() for i in range(h))
+        assert abs(got[s // 16, :, s % 16].sum() - before - steps * H) < 1e-3 * steps * H
+    assert kv.status() == 0
