@@ -53,7 +53,7 @@ enum {
  *     V codes  [16][d/8]  channels 8 w .. + 7 at word w
  *     K meta   [16][NG]   scale in the low 16 bits, zero in the high 16 bits
  *     V meta   [16][NG]
- * weights: [n_pages][num_kv_heads][16] fp32, the attention weight that each token has
+ * weights: [n_pages][num_kv_heads][16] fp32, 16-byte aligned, the attention weight that each token has
  *   drawn so far, summed over the query heads that share the KV head; NULL where the
  *   caller keeps none. */
 typedef struct starkv_kv4_cache {

@@ -46,11 +46,11 @@ cudaError_t launch_kv4_evict(const Ctx& c, const starkv_kv4_cache& cache, const 
 
 // ---- kv4_decode.cu
 struct Kv4DecodePlan {
-  int chunk;            // pages of one split
-  int splits;           // splits of the longest sequence the block table can hold
+  int ctas;             // CTAs that share the batch's pages (0: one per sequence and unit)
   int head_blocks;      // blocks of at most 8 query heads of a KV head
+  int units;            // num_kv_heads * head_blocks
   int score_heads;      // floats of a token's scores in the workspace (0: not kept)
-  size_t off_ml, off_scores, ws_bytes;
+  size_t off_ml, off_unit, off_scores, ws_bytes;
 };
 Kv4DecodePlan plan_kv4_decode(const Ctx& c, int batch, int max_pages, bool accumulate);
 cudaError_t launch_kv4_decode(const Ctx& c, const starkv_kv4_cache& cache, const __nv_bfloat16* q,

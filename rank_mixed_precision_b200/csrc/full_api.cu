@@ -26,8 +26,8 @@ starkv_status check_cache(const starkv_kv4_cache* cache) {
   if (!cache) return fail(STARKV_ERR_INVALID_ARG, "cache is NULL");
   if (cache->n_pages < 0) return fail(STARKV_ERR_INVALID_ARG, "cache.n_pages < 0");
   if (cache->n_pages > 0 && !cache->pages) return fail(STARKV_ERR_INVALID_ARG, "cache.pages is NULL");
-  if (!aligned(cache->pages, 16) || !aligned(cache->weights, 4))
-    return fail(STARKV_ERR_INVALID_ARG, "cache.pages must be 16-byte and cache.weights 4-byte aligned");
+  if (!aligned(cache->pages, 16) || !aligned(cache->weights, 16))
+    return fail(STARKV_ERR_INVALID_ARG, "cache.pages and cache.weights must be 16-byte aligned");
   return STARKV_OK;
 }
 

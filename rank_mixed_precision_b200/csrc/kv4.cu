@@ -10,8 +10,10 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // Append.  Eight channels (one 16-byte load, one code word) per thread; the four
-// threads of a 32-channel group share its minimum and maximum by two shuffles.
-// 2 D/8 threads hold one (token, KV head): K's channels, then V's.
+// threads of a 32-channel group share its minimum and maximum by two shuffles.  A
+// block holds 256 such words of T tokens' rows (K's words, then V's; grid.y covers
+// a row), so that a token's slot is one load for the block and all T rows are asked
+// for before the first is used.
 // ---------------------------------------------------------------------------
 struct AppendArgs {
   const __nv_bfloat16* k;
@@ -24,85 +26,101 @@ struct AppendArgs {
   unsigned int* status;
 };
 
-constexpr int kAppendThreads = 256;
+constexpr int kRowThreads = 256;
+constexpr int kRowTokens = 4;  // tokens a block takes where there are many
 
-template <int D>
-__global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const AppendArgs a) {
+// code of x >= z: clamp(rint(fl((x - z) / s)), 0, 15), inv = fl(1 / s).  (x - z) * inv is
+// within 2^-23 of the quotient (relative; 4e-6 for what is not clamped), so it rounds to
+// the same integer unless it lies that close to a half; there the quotient is taken.
+__device__ __forceinline__ uint32_t code_of(float x, float z, float s, float inv) {
+  const float a = __fsub_rn(x, z);
+  float q = fminf(fmaxf(a * inv, 0.f), 15.f);
+  float r = q + 12582912.f;  // 1.5 2^23: the sum's low bits are rint(q)
+  if (fabsf(q - (r - 12582912.f)) > 0.49999f) r = fminf(fmaxf(__fdiv_rn(a, s), 0.f), 15.f) + 12582912.f;
+  return __float_as_uint(r) & 15u;
+}
+
+template <int D, int T>
+__global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const AppendArgs a) {
   using P = Kv4<D>;
-  constexpr int kPer = 2 * D / 8;  // threads of one (token, head): 32 or 16
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t id = (int64_t)blockIdx.x * kAppendThreads + threadIdx.x;
-  const int64_t th = id / kPer;
-  const int w2 = (int)(id % kPer);
-  const bool is_v = w2 >= D / 8;
-  const int w = is_v ? w2 - D / 8 : w2;
-  const int64_t token = th / a.pool.h_kv;
-  const int head = (int)(th % a.pool.h_kv);
-  const bool live = token < a.n;
-  int64_t slot = live ? a.slots[token] : -1;
-  if (slot >= a.pool.n_pages * kPage) {
-    if (w2 == 0) set_status(a.status, STARKV_DEV_BAD_SLOT);
-    slot = -1;
-  }
-  float x[8];
-  float mn = 0.f, mx = 0.f;
-  bool finite = true;
-  if (slot >= 0) {
-    const __nv_bfloat16* src = (is_v ? a.v + token * a.v_stride : a.k + token * a.k_stride) + head * D + w * 8;
-    const uint4 raw = *reinterpret_cast<const uint4*>(src);
-    const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
+  const int half = a.pool.h_kv * (D / 8);  // words of a token's K row, and of its V row
+  const int word = blockIdx.y * kRowThreads + threadIdx.x;
+  const bool inside = word < 2 * half;  // (2 half is a multiple of 16: a group's four threads agree)
+  const bool is_v = word >= half;
+  const int at_row = is_v ? word - half : word;
+  const int head = at_row / (D / 8), w = at_row % (D / 8);
+  const int64_t token0 = (int64_t)blockIdx.x * T;
+  int64_t slot[T];
+  uint4 raw[T];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(r[i] << 16);
-      x[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
-    }
-    mn = mx = x[0];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      mn = fminf(mn, x[i]);
-      mx = fmaxf(mx, x[i]);
-      finite = finite && isfinite(x[i]);
+  for (int i = 0; i < T; ++i) {
+    const int64_t token = token0 + i;
+    slot[i] = -1;
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (inside && token < a.n) {
+      slot[i] = a.slots[token];
+      raw[i] = *reinterpret_cast<const uint4*>((is_v ? a.v + token * a.v_stride : a.k + token * a.k_stride) + at_row * 8);
     }
   }
 #pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    finite = __shfl_xor_sync(0xffffffffu, (int)finite, o) != 0 && finite;
-  }
-  if (slot < 0) return;
-  __half s16 = __float2half_rn(__fdiv_rn(__fsub_rn(mx, mn), 15.f));
-  __half z16 = __float2half_rn(mn);
-  const float sf = __half2float(s16), zf = __half2float(z16);
-  // decode widens code * s + z in fp16, so the top code must stay inside it too
-  const bool fits = finite && isfinite(sf) && isfinite(zf) && isfinite(__half2float(__float2half_rn(fmaf(15.f, sf, zf))));
-  uint32_t word = 0;
-  if (!fits) {
-    s16 = z16 = __float2half_rn(0.f);
-    if ((w & 3) == 0) set_status(a.status, STARKV_DEV_QUANT_OVERFLOW);
-  } else if (sf != 0.f) {
+  for (int i = 0; i < T; ++i) {
+    const uint32_t r[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+    // minimum and maximum in bf16 (exact); NaN passes through both, so a group whose ends are finite is finite
+    __nv_bfloat162 lo = *reinterpret_cast<const __nv_bfloat162*>(&r[0]), hi = lo;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float c = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[i], zf), sf)), 0.f), 15.f);
-      word |= (uint32_t)c << (4 * i);
+    for (int e = 1; e < 4; ++e) {
+      const __nv_bfloat162 y = *reinterpret_cast<const __nv_bfloat162*>(&r[e]);
+      lo = __hmin2_nan(lo, y);
+      hi = __hmax2_nan(hi, y);
     }
+    __nv_bfloat162 m = __halves2bfloat162(__hmin_nan(__low2bfloat16(lo), __high2bfloat16(lo)),
+                                          __hneg(__hmax_nan(__low2bfloat16(hi), __high2bfloat16(hi))));  // (min, -max)
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) m = __hmin2_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (slot[i] >= a.pool.n_pages * kPage) {
+      if (at_row == 0) set_status(a.status, STARKV_DEV_BAD_SLOT);
+      continue;
+    }
+    if (slot[i] < 0) continue;
+    const float mn = __low2float(m), mx = -__high2float(m);
+    __half s16 = __float2half_rn(__fdiv_rn(__fsub_rn(mx, mn), 15.f));
+    __half z16 = __float2half_rn(mn);
+    const float sf = __half2float(s16), zf = __half2float(z16);
+    // decode widens code * s + z in fp16, so the top code must stay inside it too
+    const bool fits = isfinite(mn) && isfinite(mx) && isfinite(sf) && isfinite(zf) &&
+                      isfinite(__half2float(__float2half_rn(fmaf(15.f, sf, zf))));
+    uint32_t code = 0;
+    if (!fits) {
+      s16 = z16 = __float2half_rn(0.f);
+      if ((w & 3) == 0) set_status(a.status, STARKV_DEV_QUANT_OVERFLOW);
+    } else if (sf != 0.f) {
+      const float inv = __frcp_rn(sf);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        code |= code_of(__uint_as_float(r[e] << 16), zf, sf, inv) << (8 * e);
+        code |= code_of(__uint_as_float(r[e] & 0xffff0000u), zf, sf, inv) << (8 * e + 4);
+      }
+    }
+    const int64_t page = slot[i] / kPage;
+    const int t = (int)(slot[i] % kPage);
+    uint8_t* base = a.pool.pages + (page * a.pool.h_kv + head) * (int64_t)P::kBytes;
+    const int at = is_v ? w : (w & 3) * P::kGroups + (w >> 2);
+    *reinterpret_cast<uint32_t*>(base + (is_v ? P::kV : 0) + t * P::kRow + at * 4) = code;
+    if ((w & 3) == 0)
+      *reinterpret_cast<uint32_t*>(base + (is_v ? P::kVMeta : P::kKMeta) + t * P::kMetaRow + (w >> 2) * 4) =
+          (uint32_t)__half_as_ushort(s16) | ((uint32_t)__half_as_ushort(z16) << 16);
+    if (!is_v && w == 0 && a.pool.weights)
+      a.pool.weights[(page * a.pool.h_kv + head) * kPage + t] =
+          a.weights ? a.weights[(token0 + i) * a.pool.h_kv + head] : 0.f;
   }
-  const int64_t page = slot / kPage;
-  const int t = (int)(slot % kPage);
-  uint8_t* base = a.pool.pages + (page * a.pool.h_kv + head) * (int64_t)P::kBytes;
-  const int at = is_v ? w : (w & 3) * P::kGroups + (w >> 2);
-  *reinterpret_cast<uint32_t*>(base + (is_v ? P::kV : 0) + t * P::kRow + at * 4) = word;
-  if ((w & 3) == 0)
-    *reinterpret_cast<uint32_t*>(base + (is_v ? P::kVMeta : P::kKMeta) + t * P::kMetaRow + (w >> 2) * 4) =
-        (uint32_t)__half_as_ushort(s16) | ((uint32_t)__half_as_ushort(z16) << 16);
-  if (w2 == 0 && a.pool.weights)
-    a.pool.weights[(page * a.pool.h_kv + head) * kPage + t] = a.weights ? a.weights[token * a.pool.h_kv + head] : 0.f;
 }
 
 // ---------------------------------------------------------------------------
-// Read back.  One code word per thread: 4 bytes in, eight bf16 values (16 bytes)
-// out; a row's slot is looked up once per block.
+// Read back.  One code word per thread and token: 4 bytes and the group's scale and
+// zero in, eight bf16 values (16 bytes) out; blocks as in append, each row's slot
+// looked up once per block.
 // ---------------------------------------------------------------------------
 struct ReadArgs {
   const int32_t* block_table;
@@ -116,83 +134,90 @@ struct ReadArgs {
   unsigned int* status;
 };
 
-constexpr int kReadThreads = 256;
-constexpr int kReadRows = 4;
+// The slot of row `row` of the output, -1 (and a status bit) where there is none.
+__device__ int64_t slot_of_row(const ReadArgs& a, int64_t row) {
+  // the last sequence that starts at or before the row (empty ones share its start)
+  int lo = 0, hi = a.batch - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.cu[mid] <= row) lo = mid;
+    else hi = mid - 1;
+  }
+  const int64_t c0 = a.cu[lo], c1 = a.cu[lo + 1];
+  if (a.cu[0] != 0 || a.cu[a.batch] != a.total || row < c0 || row >= c1) {
+    set_status(a.status, STARKV_DEV_BAD_QUERY_SPAN);
+    return -1;
+  }
+  const int64_t t = (a.starts ? a.starts[lo] : 0) + (row - c0);
+  if (t < 0 || t >= (int64_t)a.max_pages * kPage) {
+    set_status(a.status, STARKV_DEV_BAD_SEQ_LEN);
+    return -1;
+  }
+  const int64_t page = a.block_table[(int64_t)lo * a.max_pages + t / kPage];
+  if (page < 0 || page >= a.pool.n_pages) {
+    set_status(a.status, STARKV_DEV_BAD_PAGE);
+    return -1;
+  }
+  return page * kPage + t % kPage;
+}
 
-template <int D>
-__global__ void __launch_bounds__(kReadThreads) kv4_read_kernel(const ReadArgs a) {
+template <int D, int T>
+__global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadArgs a) {
   using P = Kv4<D>;
-  __shared__ int64_t slot_of[kReadRows];
+  __shared__ int64_t slot_of[T];
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t row0 = (int64_t)blockIdx.x * kReadRows;
-  if (threadIdx.x < kReadRows) {
-    const int64_t row = row0 + threadIdx.x;
-    int64_t slot = -1;
-    if (row < a.total) {
-      // the last sequence that starts at or before the row (empty ones share its start)
-      int lo = 0, hi = a.batch - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.cu[mid] <= row) lo = mid;
-        else hi = mid - 1;
-      }
-      const int64_t c0 = a.cu[lo], c1 = a.cu[lo + 1];
-      if (a.cu[0] != 0 || a.cu[a.batch] != a.total || row < c0 || row >= c1) {
-        set_status(a.status, STARKV_DEV_BAD_QUERY_SPAN);
-      } else {
-        const int64_t t = (a.starts ? a.starts[lo] : 0) + (row - c0);
-        if (t < 0 || t >= (int64_t)a.max_pages * kPage) {
-          set_status(a.status, STARKV_DEV_BAD_SEQ_LEN);
-        } else {
-          const int64_t page = a.block_table[(int64_t)lo * a.max_pages + t / kPage];
-          if (page < 0 || page >= a.pool.n_pages) set_status(a.status, STARKV_DEV_BAD_PAGE);
-          else slot = page * kPage + t % kPage;
-        }
-      }
-    }
-    slot_of[threadIdx.x] = slot;
-  }
+  const int64_t row0 = (int64_t)blockIdx.x * T;
+  if (threadIdx.x < T) slot_of[threadIdx.x] = row0 + threadIdx.x < a.total ? slot_of_row(a, row0 + threadIdx.x) : -1;
   __syncthreads();
-  const int per_row = a.pool.h_kv * (2 * D / 8);
-  const int rows = (int)min((int64_t)kReadRows, a.total - row0);
-  for (int e = threadIdx.x; e < rows * per_row; e += kReadThreads) {
-    const int r = e / per_row, f = e - r * per_row;
-    const int head = f / (2 * D / 8), w2 = f % (2 * D / 8);
-    const bool is_v = w2 >= D / 8;
-    const int w = is_v ? w2 - D / 8 : w2;
-    const int64_t slot = slot_of[r];
-    uint4 o = make_uint4(0, 0, 0, 0);
-    if (slot >= 0) {
-      const int t = (int)(slot % kPage);
-      const uint8_t* base = a.pool.pages + (slot / kPage * a.pool.h_kv + head) * (int64_t)P::kBytes;
-      const int at = is_v ? w : (w & 3) * P::kGroups + (w >> 2);
-      const uint32_t word = *reinterpret_cast<const uint32_t*>(base + (is_v ? P::kV : 0) + t * P::kRow + at * 4);
-      const float2 sz = unpack_meta(
-          *reinterpret_cast<const uint32_t*>(base + (is_v ? P::kVMeta : P::kKMeta) + t * P::kMetaRow + (w >> 2) * 4));
-      uint32_t p[4];
+  const int half = a.pool.h_kv * (D / 8);
+  const int word = blockIdx.y * kRowThreads + threadIdx.x;
+  if (word >= 2 * half) return;
+  const bool is_v = word >= half;
+  const int at_row = is_v ? word - half : word;
+  const int head = at_row / (D / 8), w = at_row % (D / 8);
+  const int code_at = (is_v ? P::kV : 0) + (is_v ? w : (w & 3) * P::kGroups + (w >> 2)) * 4;
+  const int meta_at = (is_v ? P::kVMeta : P::kKMeta) + (w >> 2) * 4;
+  uint32_t code[T], meta[T];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // code * s is exact in fp32: one rounding for the sum, one to bf16
-        const __nv_bfloat162 b =
-            __floats2bfloat162_rn(fmaf((float)((word >> (8 * i)) & 15u), sz.x, sz.y),
-                                  fmaf((float)((word >> (8 * i + 4)) & 15u), sz.x, sz.y));
-        p[i] = *reinterpret_cast<const uint32_t*>(&b);
-      }
-      o = make_uint4(p[0], p[1], p[2], p[3]);
+  for (int i = 0; i < T; ++i) {
+    const int64_t slot = slot_of[i];
+    code[i] = meta[i] = 0;  // a token that is not there reads as zeros
+    if (slot < 0) continue;
+    const int t = (int)(slot % kPage);
+    const uint8_t* base = a.pool.pages + (slot / kPage * a.pool.h_kv + head) * (int64_t)P::kBytes;
+    code[i] = *reinterpret_cast<const uint32_t*>(base + code_at + t * P::kRow);
+    meta[i] = *reinterpret_cast<const uint32_t*>(base + meta_at + t * P::kMetaRow);
+  }
+  __nv_bfloat16* out = (is_v ? a.v : a.k) + at_row * 8;
+#pragma unroll
+  for (int i = 0; i < T; ++i) {
+    if (row0 + i >= a.total) break;
+    const float2 sz = unpack_meta(meta[i]);
+    uint32_t p[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      // 2^23 + code is a pattern; code * s is exact in fp32: one rounding for the sum, one to bf16
+      const float c0 = __uint_as_float(0x4b000000u | ((code[i] >> (8 * e)) & 15u)) - 8388608.f;
+      const float c1 = __uint_as_float(0x4b000000u | ((code[i] >> (8 * e + 4)) & 15u)) - 8388608.f;
+      const __nv_bfloat162 b = __floats2bfloat162_rn(fmaf(c0, sz.x, sz.y), fmaf(c1, sz.x, sz.y));
+      p[e] = *reinterpret_cast<const uint32_t*>(&b);
     }
-    __nv_bfloat16* dst = (is_v ? a.v : a.k) + ((row0 + r) * a.pool.h_kv + head) * (int64_t)D + w * 8;
-    *reinterpret_cast<uint4*>(dst) = o;
+    *reinterpret_cast<uint4*>(out + (row0 + i) * half * 8) = make_uint4(p[0], p[1], p[2], p[3]);
   }
 }
 
 // ---------------------------------------------------------------------------
 // Eviction, step 1: the kept tokens of one (sequence, KV head).
 //
-// Each token gets a 32-bit key that orders like its weight (recent tokens above
-// all, NaN below all); the value of the keep-th largest key is found digit by digit
-// (11, 11 and 10 bits, counts in shared memory), then one ordered pass lists the
-// tokens above it and the first of those equal to it.
+// Each token that may go gets a 32-bit key that orders like its weight (NaN below all).
+// The threads hold the keys in registers (eight tokens of each stretch of 8192 a thread,
+// four stretches; keys of tokens beyond 32768 are read again each time) and find the
+// largest threshold that `need` keys reach bit by bit, from the first bit in which the
+// keys differ: a count in registers, a warp's and a block's sum, one barrier a bit, and
+// an early end where exactly `need` reach it.  (A histogram of digits took three passes,
+// but weights share few leading digits: its atomics on few counters cost 3 times as much.)
+// One ordered pass then lists the tokens above the threshold and the first equal to it.
 // ---------------------------------------------------------------------------
 struct EvictArgs {
   const int32_t* block_table;
@@ -205,12 +230,12 @@ struct EvictArgs {
   int32_t* kept;
   Kv4Pool pool;
   unsigned int* status;
-  int smem_keys;  // keys that shared memory holds (the rest is read again)
 };
 
 constexpr int kSelThreads = 1024;
-constexpr int kBins = 2048;
-constexpr int kKeysInSmem = 48 * 1024;  // beside the bins within 227 KB
+constexpr int kSelEach = 8;                            // tokens of a thread in a stretch
+constexpr int kStretch = kSelThreads * kSelEach;
+constexpr int kHeld = 4;                               // stretches whose keys stay in registers
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (isnan(w)) return 0u;
@@ -220,10 +245,8 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 __global__ void __launch_bounds__(kSelThreads, 1) kv4_select_kernel(const EvictArgs a) {
-  extern __shared__ uint32_t keys[];
-  __shared__ uint32_t bins[kBins];
   __shared__ uint32_t wsum[2][32];
-  __shared__ uint32_t found[2];
+  __shared__ uint32_t ends[2][32];
   __shared__ unsigned bad;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int head = blockIdx.x, b = blockIdx.y;
@@ -233,6 +256,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv4_select_kernel(const EvictA
   const int want = a.keep_lens[b];
   const int cap = a.dst_max_pages * kPage;
   int32_t* kept = a.kept + ((int64_t)b * a.pool.h_kv + head) * cap;
+  const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
   if (tid == 0) bad = 0;
   __syncthreads();
   const int keep = min(n, want);
@@ -240,7 +264,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv4_select_kernel(const EvictA
     if (tid == 0) bad = STARKV_DEV_BAD_SEQ_LEN;
   } else {
     for (int i = tid; i < (n + kPage - 1) / kPage; i += kSelThreads) {
-      const int64_t p = a.block_table[(int64_t)b * a.max_pages + i];
+      const int64_t p = table[i];
       if (p < 0 || p >= a.pool.n_pages) atomicOr(&bad, STARKV_DEV_BAD_PAGE);
     }
     for (int i = tid; i < (keep + kPage - 1) / kPage; i += kSelThreads) {
@@ -259,81 +283,130 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv4_select_kernel(const EvictA
     for (int i = tid; i < n; i += kSelThreads) kept[i] = i;
     return;
   }
-  const int first_recent = n - min(a.recent, keep);
-  auto key_at = [&](int i) -> uint32_t {
-    if (i >= first_recent) return 0xffffffffu;
-    const int64_t p = a.block_table[(int64_t)b * a.max_pages + i / kPage];
-    return weight_key(a.pool.weights[(p * a.pool.h_kv + head) * kPage + i % kPage]);
+  const int recent = min(a.recent, keep);
+  const int old = n - recent;                // tokens that may go
+  uint32_t need = (uint32_t)(keep - recent); // how many of them stay
+  for (int i = tid; i < recent; i += kSelThreads) kept[need + i] = old + i;
+  if (need == 0) return;
+  // keys of tokens i0 .. i0 + 7 (one page's half: 32 contiguous bytes)
+  auto keys_at = [&](int i0, uint32_t (&k)[kSelEach]) {
+#pragma unroll
+    for (int e = 0; e < kSelEach; ++e) k[e] = 0;
+    if (i0 >= old) return;
+    const int64_t p = table[i0 / kPage];
+    const float4* w = reinterpret_cast<const float4*>(a.pool.weights + (p * a.pool.h_kv + head) * kPage + i0 % kPage);
+    const float4 x = w[0], y = w[1];
+    const float v[kSelEach] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int e = 0; e < kSelEach; ++e)
+      if (i0 + e < old) k[e] = weight_key(v[e]);
   };
-  for (int i = tid; i < min(n, a.smem_keys); i += kSelThreads) keys[i] = key_at(i);
-  auto key_of = [&](int i) -> uint32_t { return i < a.smem_keys ? keys[i] : key_at(i); };
-  uint32_t prefix = 0, need = (uint32_t)keep;  // digits found so far; how many still to take among their equals
+  uint32_t held[kHeld][kSelEach];
+#pragma unroll
+  for (int g = 0; g < kHeld; ++g) keys_at(g * kStretch + tid * kSelEach, held[g]);
+  // smallest and largest key: their common leading bits are the threshold's
+  uint32_t lo = 0xffffffffu, hi = 0;
+  auto span = [&](int i0, const uint32_t (&k)[kSelEach]) {
+#pragma unroll
+    for (int e = 0; e < kSelEach; ++e)
+      if (i0 + e < old) {
+        lo = min(lo, k[e]);
+        hi = max(hi, k[e]);
+      }
+  };
+#pragma unroll
+  for (int g = 0; g < kHeld; ++g) span(g * kStretch + tid * kSelEach, held[g]);
+  for (int i0 = kHeld * kStretch + tid * kSelEach; i0 < old; i0 += kStretch) {
+    uint32_t k[kSelEach];
+    keys_at(i0, k);
+    span(i0, k);
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    ends[0][warp] = lo;
+    ends[1][warp] = hi;
+  }
+  __syncthreads();
+  lo = __reduce_min_sync(0xffffffffu, ends[0][lane]);
+  hi = __reduce_max_sync(0xffffffffu, ends[1][lane]);
+  const int bits = lo == hi ? 0 : 32 - __clz(lo ^ hi);
+  uint32_t threshold = bits == 32 ? 0u : hi >> bits << bits;  // at least `need` keys reach it
+  uint32_t above_all = 0;  // keys above the threshold, once it is found
+  bool exact = false;
 #pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const uint32_t digits = pass == 2 ? 1024u : 2048u;
-    for (int i = tid; i < kBins; i += kSelThreads) bins[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += kSelThreads) {
-      const uint32_t k = key_of(i);
-      if (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == prefix) atomicAdd(&bins[(k >> shift) & (digits - 1)], 1u);
+  for (int bit = bits - 1; bit >= 0; --bit) {
+    const uint32_t t = threshold | (1u << bit);
+    uint32_t c = 0;
+#pragma unroll
+    for (int g = 0; g < kHeld; ++g)
+      if (g * kStretch < old) {
+#pragma unroll
+        for (int e = 0; e < kSelEach; ++e) c += held[g][e] >= t;
+      }
+    for (int i0 = kHeld * kStretch + tid * kSelEach; i0 < old; i0 += kStretch) {
+      uint32_t k[kSelEach];
+      keys_at(i0, k);
+#pragma unroll
+      for (int e = 0; e < kSelEach; ++e) c += k[e] >= t;
     }
-    __syncthreads();
-    // thread i owns the two bins 2i, 2i+1 counted from the top: find the one that holds the need-th key
-    const uint32_t top = kBins - 1 - 2 * tid;
-    const uint32_t c0 = bins[top], c1 = bins[top - 1];
-    uint32_t inc = c0 + c1;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0) wsum[bit & 1][warp] = c;
+    __syncthreads();  // (the other buffer was read before the last barrier)
+    c = __reduce_add_sync(0xffffffffu, wsum[bit & 1][lane]);
+    if (c >= need) threshold = t;
+    else above_all = c;
+    if (c == need) {
+      exact = true;  // exactly the keys that reach it stay
+      break;
+    }
+  }
+  if (exact) {
+    threshold -= 1;
+    above_all = need;
+  }
+  const uint32_t equals = need - above_all;  // of the keys equal to the threshold, the first so many stay
+  // the ordered list: a stretch at a time, each thread behind the threads before it
+  uint32_t base = 0, base_eq = 0;
+  auto list = [&](int i0, const uint32_t (&k)[kSelEach], int turn) {
+    uint32_t mine = 0;  // above in the low half, equal in the high half: at most 8192 each in a stretch
+#pragma unroll
+    for (int e = 0; e < kSelEach; ++e)
+      if (i0 + e < old) mine += k[e] > threshold ? 1u : k[e] == threshold ? 0x10000u : 0u;
+    uint32_t inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += v;
     }
-    if (lane == 31) wsum[0][warp] = inc;
     __syncthreads();
-    uint32_t before = inc - c0 - c1;
-    for (int w = 0; w < warp; ++w) before += wsum[0][w];
-    if (before < need && need <= before + c0 + c1) {
-      const bool upper = need <= before + c0;
-      found[0] = upper ? top : top - 1;
-      found[1] = need - (upper ? before : before + c0);
-    }
+    if (lane == 31) wsum[turn & 1][warp] = inc;
     __syncthreads();
-    prefix = (prefix << (pass == 2 ? 10 : 11)) | found[0];
-    need = found[1];
-    __syncthreads();
-  }
-  // the tokens above the threshold, and the first `need` equal to it, in order: each
-  // warp counts its own stretch, then writes behind the counts of the warps before it
-  const int per = ((n + 31) / 32 + 31) / 32 * 32;
-  const int lo = min(n, warp * per), hi = min(n, lo + per);
-  uint32_t above = 0, equal = 0;
-  for (int i0 = lo; i0 < hi; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t k = i < hi ? key_of(i) : 0u;
-    above += __popc(__ballot_sync(0xffffffffu, i < hi && k > prefix));
-    equal += __popc(__ballot_sync(0xffffffffu, i < hi && k == prefix));
-  }
-  if (lane == 0) {
-    wsum[0][warp] = above;
-    wsum[1][warp] = equal;
-  }
-  __syncthreads();
-  above = equal = 0;
-  for (int w = 0; w < warp; ++w) {
-    above += wsum[0][w];
-    equal += wsum[1][w];
-  }
-  const uint32_t below = (1u << lane) - 1u;
-  for (int i0 = lo; i0 < hi; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t k = i < hi ? key_of(i) : 0u;
-    const uint32_t ba = __ballot_sync(0xffffffffu, i < hi && k > prefix);
-    const uint32_t be = __ballot_sync(0xffffffffu, i < hi && k == prefix);
-    const uint32_t e = equal + __popc(be & below);
-    if (i < hi && (k > prefix || (k == prefix && e < need)))
-      kept[above + __popc(ba & below) + min(need, e)] = i;
-    above += __popc(ba);
-    equal += __popc(be);
+    const uint32_t w = wsum[turn & 1][lane];
+    const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u) + inc - mine;
+    const uint32_t total = __reduce_add_sync(0xffffffffu, w);
+    uint32_t up = base + (before & 0xffffu), eq = base_eq + (before >> 16);
+#pragma unroll
+    for (int e = 0; e < kSelEach; ++e)
+      if (i0 + e < old) {
+        if (k[e] > threshold) {
+          kept[up + min(eq, equals)] = i0 + e;
+          ++up;
+        } else if (k[e] == threshold) {
+          if (eq < equals) kept[up + eq] = i0 + e;
+          ++eq;
+        }
+      }
+    base += total & 0xffffu;
+    base_eq += total >> 16;
+  };
+#pragma unroll
+  for (int g = 0; g < kHeld; ++g)
+    if (g * kStretch < old) list(g * kStretch + tid * kSelEach, held[g], g);
+  for (int g = kHeld; g * kStretch < old; ++g) {
+    uint32_t k[kSelEach];
+    keys_at(g * kStretch + tid * kSelEach, k);
+    list(g * kStretch + tid * kSelEach, k, g);
   }
 }
 
@@ -419,24 +492,40 @@ Kv4Pool pool_of(const Ctx& c, const starkv_kv4_cache& cache) {
 
 }  // namespace
 
+// Blocks of kRowTokens tokens where they fill the GPU twice over, else of one (a decode step's write
+// spreads over more SMs).
+static bool many_rows(int64_t n, unsigned gy) { return (n + kRowTokens - 1) / kRowTokens * gy >= 2 * 148; }
+
 cudaError_t launch_kv4_append(const Ctx& c, const starkv_kv4_cache& cache, const __nv_bfloat16* k,
                               const __nv_bfloat16* v, int64_t k_stride, int64_t v_stride, const int64_t* slots,
                               const float* weights, int64_t n, cudaStream_t s) {
   AppendArgs a{k, v, k_stride, v_stride, slots, weights, n, pool_of(c, cache), c.status};
   const int d = c.cfg.head_dim;
-  const int64_t threads = n * c.cfg.num_kv_heads * (2 * d / 8);
-  const int64_t blocks = (threads + kAppendThreads - 1) / kAppendThreads;
-  return launch_chained(d == 64 ? kv4_append_kernel<64> : kv4_append_kernel<128>, dim3((unsigned)blocks),
-                        dim3(kAppendThreads), 0, s, 1u, a);
+  const unsigned gy = (unsigned)((c.cfg.num_kv_heads * (2 * d / 8) + kRowThreads - 1) / kRowThreads);
+  const dim3 block(kRowThreads);
+  if (many_rows(n, gy)) {
+    const dim3 grid((unsigned)((n + kRowTokens - 1) / kRowTokens), gy);
+    return launch_chained(d == 64 ? kv4_append_kernel<64, kRowTokens> : kv4_append_kernel<128, kRowTokens>, grid, block,
+                          0, s, 1u, a);
+  }
+  return launch_chained(d == 64 ? kv4_append_kernel<64, 1> : kv4_append_kernel<128, 1>, dim3((unsigned)n, gy), block, 0,
+                        s, 1u, a);
 }
 
 cudaError_t launch_kv4_read(const Ctx& c, const starkv_kv4_cache& cache, const int32_t* block_table,
                             const int32_t* starts, const int32_t* cu, int batch, int max_pages, int64_t total,
                             __nv_bfloat16* k, __nv_bfloat16* v, cudaStream_t s) {
   ReadArgs a{block_table, starts, cu, batch, max_pages, total, k, v, pool_of(c, cache), c.status};
-  const int64_t blocks = (total + kReadRows - 1) / kReadRows;
-  return launch_chained(c.cfg.head_dim == 64 ? kv4_read_kernel<64> : kv4_read_kernel<128>, dim3((unsigned)blocks),
-                        dim3(kReadThreads), 0, s, 1u, a);
+  const int d = c.cfg.head_dim;
+  const unsigned gy = (unsigned)((c.cfg.num_kv_heads * (2 * d / 8) + kRowThreads - 1) / kRowThreads);
+  const dim3 block(kRowThreads);
+  if (many_rows(total, gy)) {
+    const dim3 grid((unsigned)((total + kRowTokens - 1) / kRowTokens), gy);
+    return launch_chained(d == 64 ? kv4_read_kernel<64, kRowTokens> : kv4_read_kernel<128, kRowTokens>, grid, block, 0,
+                          s, 1u, a);
+  }
+  return launch_chained(d == 64 ? kv4_read_kernel<64, 1> : kv4_read_kernel<128, 1>, dim3((unsigned)total, gy), block, 0,
+                        s, 1u, a);
 }
 
 cudaError_t launch_kv4_evict(const Ctx& c, const starkv_kv4_cache& cache, const int32_t* block_table,
@@ -444,14 +533,8 @@ cudaError_t launch_kv4_evict(const Ctx& c, const starkv_kv4_cache& cache, const 
                              const int32_t* dst_table, int dst_max_pages, int32_t* new_lens, int32_t* kept,
                              cudaStream_t s) {
   EvictArgs a{block_table, seq_lens, keep_lens, recent, max_pages, dst_table, dst_max_pages, new_lens, kept,
-              pool_of(c, cache), c.status, 0};
-  const int64_t most = (int64_t)max_pages * kPage;
-  a.smem_keys = (int)(most < kKeysInSmem ? most : kKeysInSmem);
-  const size_t smem = (size_t)a.smem_keys * 4;
-  cudaError_t e = cudaFuncSetAttribute(kv4_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kKeysInSmem * 4);
-  if (e != cudaSuccess) return e;
-  e = launch_chained(kv4_select_kernel, dim3(c.cfg.num_kv_heads, batch), dim3(kSelThreads), smem, s, 1u, a);
+              pool_of(c, cache), c.status};
+  cudaError_t e = launch_chained(kv4_select_kernel, dim3(c.cfg.num_kv_heads, batch), dim3(kSelThreads), 0, s, 1u, a);
   if (e != cudaSuccess) return e;
   const int per = kMoveThreads / 32;
   return launch_chained(c.cfg.head_dim == 64 ? kv4_move_kernel<64> : kv4_move_kernel<128>,

@@ -1,14 +1,19 @@
 // Decode attention over the 4-bit cache of full-width layers.
 //
-// One CTA takes a chunk of pages of one (sequence, KV head, block of at most eight
-// query heads); its four warps take the chunk's pages in turn, each with its own
-// ring of bulk copies (one 16-token page of one head is one contiguous copy), its
-// own running maximum and sum, and its own output accumulators.  Scores and
-// outputs run on mma.sync m16n8k16: the eight query heads are the N of both
-// products, so a page's codes are read once for all of them.  With N = 8 the
-// products are small (2 x 16 x 8 x D per page) and their operands come out of
-// 4-bit codes in registers, which tcgen05 (operands in shared or tensor memory,
-// N of a whole tile) could only take after a round trip through shared memory.
+// The batch's pages, laid end to end as (sequence, unit, page) with a unit = one KV head
+// and a block of at most eight of its query heads, are cut into equal stretches, one per
+// CTA (four or five CTAs an SM, one round): ragged lengths cost no idle SMs, and a CTA's
+// start (its queries, its first copies) is paid once for about a hundred pages.  A unit
+// that a cut goes through leaves partial results, which a second kernel joins; where the
+// tables are short, a CTA takes a whole unit and there is no second kernel.
+// A CTA's four warps take a stretch's pages in turn, each with its own ring of bulk
+// copies (one 16-token page of one head is one contiguous copy), its own running maximum
+// and sum, and its own output accumulators.  Scores and outputs run on mma.sync
+// m16n8k16: the eight query heads are the N of both products, so a page's codes are read
+// once for all of them.  With N = 8 the products are small (2 x 16 x 8 x D per page) and
+// their operands come out of 4-bit codes in registers, which tcgen05 (operands in shared
+// or tensor memory, N of a whole tile) could only take after a round trip through shared
+// memory.
 //
 //   scores   s[t, h] = sum_g ( sc[t, g] * sum_{c in g} n[t, c] q[h, c] + z[t, g] * sum_{c in g} q[h, c] )
 //     A = the codes n of the page's tokens, B = q.  A masked code (w & 0x000f000f) is
@@ -32,6 +37,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kHeads = 8;            // query heads of one CTA (the N of the products)
+constexpr int kCtas = 4;             // CTAs of an SM
+constexpr int kWholePages = 32;      // tables of at most this many pages: a CTA takes a whole unit
 constexpr float kMoveMax = 8.f;      // the running maximum moves when a score passes it by this (log2)
 constexpr float kNoMax = -1e30f;     // running maximum before the first score
 
@@ -39,23 +46,44 @@ struct DecodeArgs {
   const __nv_bfloat16* q;
   const int32_t* block_table;
   const int32_t* seq_lens;
-  int H, group, head_blocks, max_pages, chunk, splits, score_heads;
+  int H, group, head_blocks, units, batch, max_pages, ctas, score_heads;  // ctas 0: one per (sequence, unit)
   float scale_log2;        // log2(e) / sqrt(D)
   Kv4Pool pool;
   __nv_bfloat16* out;
-  float* part_o;           // [B][h_kv * head_blocks][splits][8][D], relative to the split's maximum
-  float2* part_ml;         // [B][h_kv * head_blocks][splits][8] (maximum, sum)
-  float* scores;           // [B][h_kv][max_pages * 16][score_heads], log2 units
+  float* part_o;           // [ctas][2][8][D], relative to the part's maximum: [0] of a unit that began before the
+  float2* part_ml;         // [ctas][2][8] (maximum, sum)                     CTA's stretch, [1] of one that goes on behind
+  float2* unit_ml;         // [B][units][8], of units within one CTA (NULL: not asked for)
+  float* scores;           // [B][h_kv][max_pages * 16][score_heads], log2 units (NULL: not asked for)
   unsigned int* status;
 };
 
 template <int D>
 struct DecodeSmem {
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 128 ? 4 : 6;
   static constexpr int kRing = kWarps * kStages * Kv4<D>::kBytes;
   static constexpr int kMerge = kWarps * kHeads * D * 4;  // shares the ring's bytes
   static constexpr int kBytes = (kRing > kMerge ? kRing : kMerge);
 };
+
+// Pages of sequence b; 0 where its length is bad.
+__device__ __forceinline__ int pages_of(const DecodeArgs& a, int b) {
+  const int len = a.seq_lens[b];
+  return len < 0 || len > a.max_pages * kPage ? 0 : (len + kPage - 1) / kPage;
+}
+
+// Sum of value over the block's threads (T of them; sum: scratch of T / 32).
+template <int T>
+__device__ __forceinline__ int64_t block_sum(int64_t value, int64_t* sum) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) value += __shfl_xor_sync(0xffffffffu, value, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sum[threadIdx.x >> 5] = value;
+  __syncthreads();
+  value = 0;
+#pragma unroll
+  for (int w = 0; w < T / 32; ++w) value += sum[w];
+  return value;
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -80,8 +108,12 @@ __device__ __forceinline__ uint32_t movm_trans(uint32_t x) {
 // halves of the 32 banks, and so do V's four rows of a load (t = 0..3).
 __device__ __forceinline__ int token_of(int t, int e, int f) { return 8 * f + 4 * e + ((t + e) & 3); }
 
+// Position of the first page of CTA c's stretch, and the CTA whose stretch holds position x.
+__device__ __forceinline__ int64_t cut(int64_t c, int64_t total, int ctas) { return c * total / ctas; }
+__device__ __forceinline__ int64_t cta_of(int64_t x, int64_t total, int ctas) { return ((x + 1) * ctas - 1) / total; }
+
 template <int D>
-__global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtas) kv4_decode_kernel(const DecodeArgs a) {
   using P = Kv4<D>;
   using SM = DecodeSmem<D>;
   constexpr int NG = P::kGroups;
@@ -90,148 +122,216 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const DecodeArg
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ __align__(8) uint64_t full[kWarps * ST];
   __shared__ float2 ml[kWarps][kHeads];
+  __shared__ int64_t sums[kWarps];
+  __shared__ int64_t begin[2];  // the stretch's first sequence, and the pages before it
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int split = blockIdx.x, b = blockIdx.z;
-  const int kv = blockIdx.y / a.head_blocks, hb = blockIdx.y % a.head_blocks;
-  const int heads = min(kHeads, a.group - hb * kHeads);
-  const int h0 = kv * a.group + hb * kHeads;
   if (lane < ST) mbar_init(&full[warp * ST + lane], 1);
   fence_mbar_init();
   pdl_wait();
   pdl_launch_dependents();
-  __syncthreads();
-  int len = a.seq_lens[b];
-  if (len < 0 || len > a.max_pages * kPage) {
-    if (tid == 0 && split == 0) set_status(a.status, STARKV_DEV_BAD_SEQ_LEN);
-    len = 0;
+
+  // ---- the stretch: positions pos .. end - 1, in sequence b (whose first page is at units * before)
+  int b;
+  int64_t pos, end, before;
+  if (a.ctas == 0) {
+    b = blockIdx.x / a.units;
+    before = 0;
+    const int pages = pages_of(a, b);
+    const int u = blockIdx.x % a.units;
+    pos = (int64_t)u * pages;
+    end = pos + pages;
+    if (tid == 0 && u == 0 && pages == 0 && a.seq_lens[b] != 0) set_status(a.status, STARKV_DEV_BAD_SEQ_LEN);
+    if (pages == 0) {
+      const int heads = min(kHeads, a.group - u % a.head_blocks * kHeads);
+      const int h0 = u / a.head_blocks * a.group + u % a.head_blocks * kHeads;
+      for (int i = tid; i < heads * D; i += kThreads) a.out[((int64_t)b * a.H + h0) * D + i] = __float2bfloat16_rn(0.f);
+      return;
+    }
+    __syncthreads();
+  } else {
+    int64_t mine = 0;
+    for (int i = tid; i < a.batch; i += kThreads) {
+      const int pages = pages_of(a, i);
+      if (blockIdx.x == 0 && pages == 0 && a.seq_lens[i] != 0) set_status(a.status, STARKV_DEV_BAD_SEQ_LEN);
+      mine += pages;
+    }
+    const int64_t total = block_sum<kThreads>(mine, sums) * a.units;
+    pos = cut(blockIdx.x, total, a.ctas);
+    end = cut(blockIdx.x + 1, total, a.ctas);
+    if (pos == end) return;
+    // the last sequence that starts at or before pos, among those that have pages
+    int64_t carry = 0;
+    for (int i0 = 0; i0 < a.batch; i0 += kThreads) {
+      const int pages = i0 + tid < a.batch ? pages_of(a, i0 + tid) : 0;
+      int64_t inc = pages;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      __syncthreads();
+      if (lane == 31) sums[warp] = inc;
+      __syncthreads();
+      int64_t first = carry + inc - pages;
+      for (int w = 0; w < warp; ++w) first += sums[w];
+      if (pages > 0 && first * a.units <= pos && pos < (first + pages) * a.units) {
+        begin[0] = i0 + tid;
+        begin[1] = first;
+      }
+      for (int w = 0; w < kWarps; ++w) carry += sums[w];
+    }
+    __syncthreads();
+    b = (int)begin[0];
+    before = begin[1];
   }
-  const int pages = (len + kPage - 1) / kPage;
-  const int p0 = split * a.chunk, p1 = min(pages, p0 + a.chunk);
-  if (p0 >= p1) {
-    // nothing here; an empty sequence's first split writes the zero row
-    if (split == 0 && a.splits == 1)
-      for (int i = tid; i < heads * D; i += kThreads)
-        a.out[((int64_t)b * a.H + h0) * D + i] = __float2bfloat16_rn(0.f);
-    return;
-  }
-  // ---- the warp's copies: pages p0 + warp + 4 i
-  const int mine = (p1 - p0 - warp + kWarps - 1) / kWarps;  // pages of this warp (may be <= 0)
-  const int32_t* table = a.block_table + (int64_t)b * a.max_pages + p0 + warp;
+
   uint8_t* ring = sm + warp * ST * P::kBytes;
   uint64_t* bar = full + warp * ST;
-  int32_t ids = 0;      // lane i: page of iteration (base of 32) + i
-  int32_t ids_next = 0;
-  auto load_ids = [&](int base) -> int32_t {
-    int32_t id = -1;
-    if (base + lane < mine) {
-      id = table[(base + lane) * kWarps];
-      if (id < 0 || id >= a.pool.n_pages) {
-        set_status(a.status, STARKV_DEV_BAD_PAGE);
-        id = -1;
-      }
-    }
-    return id;
-  };
-  ids = load_ids(0);
-  ids_next = load_ids(32);
-  // issue the copy of iteration i (its id is in `ids` or, past the current 32, in `ids_next`)
-  auto issue = [&](int i, int base) {
-    if (i >= mine) return;
-    const int32_t id = __shfl_sync(0xffffffffu, i - base < 32 ? ids : ids_next, i & 31);
-    if (lane == 0) {
-      const int s = i % ST;
-      if (id < 0) {
-        mbar_arrive(&bar[s]);  // nothing to copy: the page is left out
-      } else {
-        mbar_arrive_expect_tx(&bar[s], P::kBytes);
-        bulk_g2s(ring + s * P::kBytes, a.pool.pages + ((int64_t)id * a.pool.h_kv + kv) * P::kBytes, P::kBytes, &bar[s]);
-      }
-    }
-  };
-#pragma unroll 1
-  for (int i = 0; i < ST - 1; ++i) issue(i, 0);
-
-  // ---- q: B operands of the score products, and the sums that the zero-points take
-  uint32_t qb[NG][4];
-  float qsum[NG][2];
-  float fq[2];
-  {
-    const __nv_bfloat16* qrow = a.q + ((int64_t)b * a.H + h0 + g) * D;
-    float x[NG][8];  // channels 32 kp + 8 t + i of head g
-    float top = 0.f;
-#pragma unroll
-    for (int kp = 0; kp < NG; ++kp) {
-      uint4 raw = make_uint4(0, 0, 0, 0);
-      if (g < heads) raw = *reinterpret_cast<const uint4*>(qrow + 32 * kp + 8 * t);
-      const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[kp][2 * i] = __uint_as_float(r[i] << 16);
-        x[kp][2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
-        top = fmaxf(top, fmaxf(fabsf(x[kp][2 * i]), fabsf(x[kp][2 * i + 1])));
-        sum += x[kp][2 * i] + x[kp][2 * i + 1];
-      }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      // D's columns 2t, 2t+1 are heads 2t, 2t+1: their sums sit in lanes 4 h
-      qsum[kp][0] = __shfl_sync(0xffffffffu, sum, 8 * t) * a.scale_log2;
-      qsum[kp][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4) * a.scale_log2;
-    }
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // the head's power of two: its largest |q| in [2^13, 2^14), so that q / 16 too is
-    // exact down to 2^-24 of it; the exponent is kept so that the inverse stays normal
-    int e = 0;
-    if (top > 0.f && isfinite(top)) {
-      frexpf(top, &e);
-      e = max(-100, min(100, 14 - e));
-    }
-    const float up = ldexpf(1.f, e);
-    const float back = ldexpf(a.scale_log2, 24 - e);
-    fq[0] = __shfl_sync(0xffffffffu, back, 8 * t);
-    fq[1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
-#pragma unroll
-    for (int kp = 0; kp < NG; ++kp) {
-      // code i of a word sits at bits 4 i: the pairs are (0, 4), (1, 5), (2, 6), (3, 7)
-      qb[kp][0] = pack_h2(x[kp][0] * up, x[kp][4] * up);
-      qb[kp][1] = pack_h2(x[kp][1] * up * 0.0625f, x[kp][5] * up * 0.0625f);
-      qb[kp][2] = pack_h2(x[kp][2] * up, x[kp][6] * up);
-      qb[kp][3] = pack_h2(x[kp][3] * up * 0.0625f, x[kp][7] * up * 0.0625f);
-    }
-  }
-
-  float o[MT][4];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[m][i] = 0.f;
-  float mx[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f};
+  int s = 0;           // the ring's next stage
+  uint32_t ph = 0;     // and its phase
   const int tok_a = token_of(g >> 1, g & 1, 0);
-  float* srow = a.scores ? a.scores + ((int64_t)b * a.pool.h_kv + kv) * a.max_pages * kPage * a.score_heads : nullptr;
   bool ok = true;
-  int done = 0;
 
 #pragma unroll 1
-  for (int i = 0; i < mine; ++i) {
-    if ((i & 31) == 0 && i > 0) {
-      ids = ids_next;
-      ids_next = load_ids(i + 32);
+  while (pos < end) {
+    const int pages = pages_of(a, b);
+    const int64_t in_seq = pos - before * a.units;
+    if (in_seq >= (int64_t)pages * a.units) {
+      before += pages;
+      ++b;
+      continue;
     }
-    issue(i + ST - 1, i & ~31);
-    const int s = i % ST;
-    if (!__all_sync(0xffffffffu, mbar_wait(&bar[s], (i / ST) & 1))) {
-      ok = false;
-      break;
+    const int len = a.seq_lens[b];
+    const int u = (int)(in_seq / pages);
+    const int p0 = (int)(in_seq - (int64_t)u * pages);
+    const int p1 = (int)min((int64_t)pages, p0 + (end - pos));
+    pos += p1 - p0;
+    const int kv = u / a.head_blocks, hb = u % a.head_blocks;
+    const int heads = min(kHeads, a.group - hb * kHeads);
+    const int h0 = kv * a.group + hb * kHeads;
+    // ---- the warp's copies: pages p0 + warp + 4 i
+    const int mine = (p1 - p0 - warp + kWarps - 1) / kWarps;  // pages of this warp (may be <= 0)
+    const int32_t* table = a.block_table + (int64_t)b * a.max_pages + p0 + warp;
+    const uint8_t* head_pages = a.pool.pages + (int64_t)kv * P::kBytes;
+    int32_t ids = 0, ids_next = 0;  // lane i: page of iteration (base of 32) + i, and of 32 further
+    auto load_ids = [&](int base) -> int32_t {
+      int32_t id = -1;
+      if (base + lane < mine) {
+        id = table[(base + lane) * kWarps];
+        if (id < 0 || id >= a.pool.n_pages) {
+          set_status(a.status, STARKV_DEV_BAD_PAGE);
+          id = -1;
+        }
+      }
+      return id;
+    };
+    ids = load_ids(0);
+    ids_next = load_ids(32);
+    uint32_t there = __ballot_sync(0xffffffffu, ids >= 0);
+    // issue the copy of iteration i to stage st: the lane that holds the page's id does
+    auto issue = [&](int i, int base, int st) {
+      if (lane == (i & 31) && i < mine) {
+        const int32_t id = i - base < 32 ? ids : ids_next;
+        if (id < 0) {
+          mbar_arrive(&bar[st]);  // nothing to copy: the page is left out
+        } else {
+          mbar_arrive_expect_tx(&bar[st], P::kBytes);
+          bulk_g2s(ring + st * P::kBytes, head_pages + (int64_t)id * a.pool.h_kv * P::kBytes, P::kBytes, &bar[st]);
+        }
+      }
+    };
+#pragma unroll 1
+    for (int i = 0; i < ST - 1; ++i) issue(i, 0, s + i < ST ? s + i : s + i - ST);
+
+    // ---- q: B operands of the score products, and the sums that the zero-points take
+    uint32_t qb[NG][4];
+    float qsum[NG][2];
+    float fq[2];
+    {
+      const __nv_bfloat16* qrow = a.q + ((int64_t)b * a.H + h0 + g) * D;
+      float x[NG][8];  // channels 32 kp + 8 t + i of head g
+      float top = 0.f;
+#pragma unroll
+      for (int kp = 0; kp < NG; ++kp) {
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (g < heads) raw = *reinterpret_cast<const uint4*>(qrow + 32 * kp + 8 * t);
+        const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[kp][2 * i] = __uint_as_float(r[i] << 16);
+          x[kp][2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+          top = fmaxf(top, fmaxf(fabsf(x[kp][2 * i]), fabsf(x[kp][2 * i + 1])));
+        }
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // the head's power of two: its largest |q| in [2^13, 2^14), so that q / 16 too is
+      // exact down to 2^-24 of it; the exponent is kept so that the inverse stays normal
+      int e = 0;
+      if (top > 0.f && isfinite(top)) {
+        frexpf(top, &e);
+        e = max(-100, min(100, 14 - e));
+      }
+      const float up = ldexpf(1.f, e);
+      const float back = ldexpf(a.scale_log2, 24 - e);
+      fq[0] = __shfl_sync(0xffffffffu, back, 8 * t);
+      fq[1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+#pragma unroll
+      for (int kp = 0; kp < NG; ++kp) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[kp][i] *= up;
+          sum += x[kp][i];
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        sum *= 5.9604644775390625e-8f;  // 2^-24: the unit of the products' sums
+        // D's columns 2t, 2t+1 are heads 2t, 2t+1: their sums sit in lanes 4 h
+        qsum[kp][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
+        qsum[kp][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+        // code i of a word sits at bits 4 i: the pairs are (0, 4), (1, 5), (2, 6), (3, 7)
+        qb[kp][0] = pack_h2(x[kp][0], x[kp][4]);
+        qb[kp][1] = pack_h2(x[kp][1] * 0.0625f, x[kp][5] * 0.0625f);
+        qb[kp][2] = pack_h2(x[kp][2], x[kp][6]);
+        qb[kp][3] = pack_h2(x[kp][3] * 0.0625f, x[kp][7] * 0.0625f);
+      }
     }
-    done = i + 1;
-    const int page = p0 + warp + i * kWarps;
-    const int left = len - page * kPage;  // tokens of the page (16 or more: all)
-    const bool there = __shfl_sync(0xffffffffu, ids, i & 31) >= 0;
-    const uint8_t* pg = ring + s * P::kBytes;
-    // ---- scores of tokens tok_a (row g) and tok_a + 8 (row g + 8)
-    float sa[2] = {-INFINITY, -INFINITY}, sb[2] = {-INFINITY, -INFINITY};
-    if (there) {
+
+    float o[MT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[m][i] = 0.f;
+    float mx[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f};
+    float* srow = nullptr;  // scores of the warp's page, from token tok_a and head 2 t on
+    if (a.scores && 2 * t < heads)
+      srow = a.scores + (((int64_t)b * a.pool.h_kv + kv) * a.max_pages * kPage + (p0 + warp) * kPage + tok_a) * a.score_heads +
+             hb * kHeads + 2 * t;
+    int left = len - (p0 + warp) * kPage;  // tokens of the page (16 or more: all)
+    int done = 0;
+
+#pragma unroll 1
+    for (int i = 0; i < mine; ++i) {
+      if ((i & 31) == 0 && i > 0) {
+        ids = ids_next;
+        ids_next = load_ids(i + 32);
+        there = __ballot_sync(0xffffffffu, ids >= 0);
+      }
+      issue(i + ST - 1, i & ~31, s == 0 ? ST - 1 : s - 1);
+      if (!__all_sync(0xffffffffu, mbar_test(&bar[s], ph)) && !__all_sync(0xffffffffu, mbar_wait(&bar[s], ph))) {
+        ok = false;
+        break;
+      }
+      done = i + 1;
+      const uint8_t* pg = ring + s * P::kBytes;
+      if (++s == ST) {
+        s = 0;
+        ph ^= 1;
+      }
+      const int held = (there >> (i & 31)) & 1 ? left : 0;  // the page's tokens that count
+      left -= kWarps * kPage;
+      // ---- scores of tokens tok_a (row g) and tok_a + 8 (row g + 8), without fq
       uint32_t ka[NG], kb[NG], ma[NG], mb[NG];
       if constexpr (D == 128) {
         const uint4 x = *reinterpret_cast<const uint4*>(pg + tok_a * P::kRow + t * 16);
@@ -252,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const DecodeArg
         ma[0] = z.x, ma[1] = z.y;
         mb[0] = w.x, mb[1] = w.y;
       }
-      float acc[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, zer[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+      float sa[2] = {0.f, 0.f}, sb[2] = {0.f, 0.f};
 #pragma unroll
       for (int kp = 0; kp < NG; ++kp) {
         float d[4] = {0.f, 0.f, 0.f, 0.f};
@@ -262,29 +362,32 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const DecodeArg
         const float2 sza = unpack_meta(ma[kp]), szb = unpack_meta(mb[kp]);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          acc[0][c] = fmaf(sza.x, d[c], acc[0][c]);
-          acc[1][c] = fmaf(szb.x, d[2 + c], acc[1][c]);
-          zer[0][c] = fmaf(sza.y, qsum[kp][c], zer[0][c]);
-          zer[1][c] = fmaf(szb.y, qsum[kp][c], zer[1][c]);
+          sa[c] = fmaf(sza.x, d[c], fmaf(sza.y, qsum[kp][c], sa[c]));
+          sb[c] = fmaf(szb.x, d[2 + c], fmaf(szb.y, qsum[kp][c], sb[c]));
+        }
+      }
+      if (held < kPage) {  // a sequence's last page, or one that is left out: free slots may hold anything
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (tok_a >= held) sa[c] = -INFINITY;
+          if (tok_a + 8 >= held) sb[c] = -INFINITY;
         }
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        sa[c] = tok_a < left ? fmaf(acc[0][c], fq[c], zer[0][c]) : -INFINITY;
-        sb[c] = tok_a + 8 < left ? fmaf(acc[1][c], fq[c], zer[1][c]) : -INFINITY;
+        sa[c] *= fq[c];
+        sb[c] *= fq[c];
       }
-    }
-    if (srow && 2 * t < heads) {
-      float* d = srow + ((int64_t)page * kPage + tok_a) * a.score_heads + hb * kHeads + 2 * t;
-      if (a.score_heads == 1) {
-        d[0] = sa[0];
-        d[8] = sb[0];
-      } else {
-        *reinterpret_cast<float2*>(d) = make_float2(sa[0], sa[1]);
-        *reinterpret_cast<float2*>(d + 8 * a.score_heads) = make_float2(sb[0], sb[1]);
+      if (srow) {
+        if (a.score_heads == 1) {
+          srow[0] = sa[0];
+          srow[8] = sb[0];
+        } else {
+          *reinterpret_cast<float2*>(srow) = make_float2(sa[0], sa[1]);
+          *reinterpret_cast<float2*>(srow + 8 * a.score_heads) = make_float2(sb[0], sb[1]);
+        }
+        srow += kWarps * kPage * a.score_heads;
       }
-    }
-    if (there) {
       // ---- running maximum (per head; the same in the eight lanes that share its columns)
       const float c0 = fmaxf(sa[0], sb[0]), c1 = fmaxf(sa[1], sb[1]);
       if (__any_sync(0xffffffffu, c0 > mx[0] + kMoveMax || c1 > mx[1] + kMoveMax)) {
@@ -326,7 +429,11 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const DecodeArg
           vw[j][0] = *reinterpret_cast<const uint32_t*>(pg + P::kV + tok * P::kRow + g * 4);
           vm[j] = *reinterpret_cast<const uint32_t*>(pg + P::kVMeta + tok * P::kMetaRow + (g >> 2) * 4);
         }
-        if (tok >= left) vm[j] = 0;  // whatever a free slot holds counts as 0
+      }
+      if (held < kPage) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (token_of(t, j & 1, j >> 1) >= held) vm[j] = 0;
       }
       uint32_t sc[2], ze[2];
 #pragma unroll
@@ -360,71 +467,87 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_kernel(const DecodeArg
         mma16816(o[4 * w + 2], even(x0 >> 8, 0), even(y0 >> 8, 0), even(x1 >> 8, 1), even(y1 >> 8, 1), b0, b1);
         mma16816(o[4 * w + 3], odd(x0 >> 8, 0), odd(y0 >> 8, 0), odd(x1 >> 8, 1), odd(y1 >> 8, 1), b0, b1);
       }
+      __syncwarp();  // every lane has read the stage before its next copy is issued
     }
-    __syncwarp();  // every lane has read the stage before its next copy is issued
-  }
-  if (!ok) {
-    // give up: wait (with a limit) for the copies in flight before the memory is left
-    if (lane == 0) set_status(a.status, kDevWaitTimeout);
-    for (int i = done; i < min(mine, done + ST); ++i) mbar_wait(&bar[i % ST], (i / ST) & 1, 100000000ull);
-  }
-  // ---- join the four warps
-#pragma unroll
-  for (int w = 4; w < 32; w <<= 1) {
-    l[0] += __shfl_xor_sync(0xffffffffu, l[0], w);
-    l[1] += __shfl_xor_sync(0xffffffffu, l[1], w);
-  }
-  if (g == 0) {
-    ml[warp][2 * t] = make_float2(mx[0], l[0]);
-    ml[warp][2 * t + 1] = make_float2(mx[1], l[1]);
-  }
-  __syncthreads();  // the rings are read out; their bytes now hold the warps' outputs [warp][head][D]
-  float* mo = reinterpret_cast<float*>(sm) + warp * kHeads * D;
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int c = g * (D / 8) + (m >> 2) * 8 + (m & 3);  // rows g, g + 8 of tile m: channels c, c + 4
-    mo[(2 * t) * D + c] = o[m][0];
-    mo[(2 * t + 1) * D + c] = o[m][1];
-    mo[(2 * t) * D + c + 4] = o[m][2];
-    mo[(2 * t + 1) * D + c + 4] = o[m][3];
-  }
-  __syncthreads();
-  const float* all = reinterpret_cast<const float*>(sm);
-  const int64_t unit = ((int64_t)b * gridDim.y + blockIdx.y) * a.splits + split;
-  for (int e = tid; e < heads * (D / 4); e += kThreads) {
-    const int h = e / (D / 4), c = (e % (D / 4)) * 4;
-    float top = kNoMax, sum = 0.f;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w][h].x);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float r = ex2(ml[w][h].x - top);
-      sum = fmaf(ml[w][h].y, r, sum);
-      const float4 x = *reinterpret_cast<const float4*>(all + (w * kHeads + h) * D + c);
-      v.x = fmaf(x.x, r, v.x);
-      v.y = fmaf(x.y, r, v.y);
-      v.z = fmaf(x.z, r, v.z);
-      v.w = fmaf(x.w, r, v.w);
+    if (!ok) {
+      // give up: wait (with a limit) for the copies in flight before the memory is left
+      if (lane == 0) set_status(a.status, kDevWaitTimeout);
+      for (int i = done; i < min(mine, done + ST); ++i) {
+        mbar_wait(&bar[s], ph, 100000000ull);
+        if (++s == ST) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
     }
-    if (a.part_ml && c == 0) a.part_ml[unit * kHeads + h] = make_float2(top, sum);
-    if (a.splits > 1) {
-      *reinterpret_cast<float4*>(a.part_o + (unit * kHeads + h) * D + c) = v;
-    } else {
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * inv, v.y * inv);
-      const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z * inv, v.w * inv);
-      uint2 w2;
-      w2.x = *reinterpret_cast<const uint32_t*>(&lo);
-      w2.y = *reinterpret_cast<const uint32_t*>(&hi);
-      *reinterpret_cast<uint2*>(a.out + ((int64_t)b * a.H + h0 + h) * D + c) = w2;
+    // ---- join the four warps
+#pragma unroll
+    for (int w = 4; w < 32; w <<= 1) {
+      l[0] += __shfl_xor_sync(0xffffffffu, l[0], w);
+      l[1] += __shfl_xor_sync(0xffffffffu, l[1], w);
     }
+    if (g == 0) {
+      ml[warp][2 * t] = make_float2(mx[0], l[0]);
+      ml[warp][2 * t + 1] = make_float2(mx[1], l[1]);
+    }
+    const bool stop = __syncthreads_or(!ok);  // the rings are read out; their bytes now hold the warps' outputs [warp][head][D]
+    float* mo = reinterpret_cast<float*>(sm) + warp * kHeads * D;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int c = g * (D / 8) + (m >> 2) * 8 + (m & 3);  // rows g, g + 8 of tile m: channels c, c + 4
+      if (2 * t < heads) {
+        mo[(2 * t) * D + c] = o[m][0];
+        mo[(2 * t) * D + c + 4] = o[m][2];
+      }
+      if (2 * t + 1 < heads) {
+        mo[(2 * t + 1) * D + c] = o[m][1];
+        mo[(2 * t + 1) * D + c + 4] = o[m][3];
+      }
+    }
+    __syncthreads();
+    const float* all = reinterpret_cast<const float*>(sm);
+    const bool whole = p0 == 0 && p1 == pages;
+    const int64_t part = ((int64_t)blockIdx.x * 2 + (p0 == 0)) * kHeads;
+    for (int e = tid; e < heads * (D / 4); e += kThreads) {
+      const int h = e / (D / 4), c = (e % (D / 4)) * 4;
+      float top = kNoMax, sum = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w][h].x);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float r = ex2(ml[w][h].x - top);
+        sum = fmaf(ml[w][h].y, r, sum);
+        const float4 x = *reinterpret_cast<const float4*>(all + (w * kHeads + h) * D + c);
+        v.x = fmaf(x.x, r, v.x);
+        v.y = fmaf(x.y, r, v.y);
+        v.z = fmaf(x.z, r, v.z);
+        v.w = fmaf(x.w, r, v.w);
+      }
+      if (!whole) {
+        if (c == 0) a.part_ml[part + h] = make_float2(top, sum);
+        *reinterpret_cast<float4*>(a.part_o + (part + h) * D + c) = v;
+      } else {
+        if (c == 0 && a.unit_ml) a.unit_ml[((int64_t)b * a.units + u) * kHeads + h] = make_float2(top, sum);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * inv, v.y * inv);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+        uint2 w2;
+        w2.x = *reinterpret_cast<const uint32_t*>(&lo);
+        w2.y = *reinterpret_cast<const uint32_t*>(&hi);
+        *reinterpret_cast<uint2*>(a.out + ((int64_t)b * a.H + h0 + h) * D + c) = w2;
+      }
+    }
+    if (stop) return;
+    fence_async_smem();  // the outputs' bytes become the ring again
+    __syncthreads();
   }
 }
 
 // ---------------------------------------------------------------------------
-// Join of the splits, and the weights.  Block x = 0 of a (sequence, KV head) joins
-// the outputs; blocks x >= 1 add the probabilities of 1024 tokens each.
+// Join of the parts, and the weights.  Block x = 0 of a (sequence, KV head) joins the
+// outputs of its units that a cut went through (and writes an empty sequence's zero
+// rows); blocks x >= 1 add the probabilities of 1024 tokens each.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 constexpr int kJoinTokens = 1024;
@@ -433,58 +556,103 @@ constexpr int kJoinHeads = 32;  // heads whose maximum and 1 / sum a pass holds
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const DecodeArgs a) {
   __shared__ float2 norm[kJoinHeads];  // maximum, 1 / sum
+  __shared__ int64_t sums[kJoinThreads / 32];
+  __shared__ float4 acc[kJoinThreads];
   const int tid = threadIdx.x;
   const int kv = blockIdx.y, b = blockIdx.z;
   pdl_wait();
   pdl_launch_dependents();
-  const int len = a.seq_lens[b];
-  const bool good = len > 0 && len <= a.max_pages * kPage;
-  const int used = good ? ((len + kPage - 1) / kPage + a.chunk - 1) / a.chunk : 0;  // splits that wrote
-  const int units = a.pool.h_kv * a.head_blocks;
+  const int pages = pages_of(a, b);
+  const int len = pages > 0 ? a.seq_lens[b] : 0;
   const int token0 = ((int)blockIdx.x - 1) * kJoinTokens;
-  if (blockIdx.x > 0 && token0 >= (good ? len : 0)) return;
+  if (blockIdx.x > 0 && token0 >= len) return;
+  if (pages == 0) {
+    uint32_t* out = reinterpret_cast<uint32_t*>(a.out + ((int64_t)b * a.H + kv * a.group) * D);
+    if (a.ctas > 0)
+      for (int i = tid; i < a.group * (D / 2); i += kJoinThreads) out[i] = 0u;
+    return;
+  }
+  int64_t before = 0, total = 0;
+  if (a.ctas > 0) {
+    for (int i = tid; i < a.batch; i += kJoinThreads) {
+      const int p = pages_of(a, i);
+      total += p;
+      if (i < b) before += p;
+    }
+    total = block_sum<kJoinThreads>(total, sums) * a.units;
+    before = block_sum<kJoinThreads>(before, sums) * a.units;
+  }
+  // the CTAs whose stretches hold unit u's first and last page
+  auto ctas_of = [&](int u, int64_t& c0, int64_t& c1) {
+    const int64_t first = before + (int64_t)u * pages;
+    c0 = a.ctas > 0 ? cta_of(first, total, a.ctas) : 0;
+    c1 = a.ctas > 0 ? cta_of(first + pages - 1, total, a.ctas) : 0;
+  };
   float add[kJoinTokens / kJoinThreads];
 #pragma unroll
   for (int i = 0; i < kJoinTokens / kJoinThreads; ++i) add[i] = 0.f;
   for (int h0 = 0; h0 < a.group; h0 += kJoinHeads) {
     const int heads = min(kJoinHeads, a.group - h0);
     __syncthreads();
-    // eight threads a head: the sequence's maximum and sum over its splits
+    // eight threads a head: the sequence's maximum and sum over its parts
     {
       const int h = h0 + tid / 8;
-      float top = kNoMax, sum = 0.f;
       const bool mine = tid / 8 < heads;
-      const float2* ml = a.part_ml +
-                         (((int64_t)b * units + kv * a.head_blocks + h / kHeads) * a.splits) * kHeads + h % kHeads;
-      if (mine)
-        for (int s = tid & 7; s < used; s += 8) top = fmaxf(top, ml[(int64_t)s * kHeads].x);
+      float top = kNoMax, sum = 0.f;
+      int64_t c0 = 0, c1 = 0;
+      const int u = kv * a.head_blocks + h / kHeads;
+      if (mine) ctas_of(u, c0, c1);
+      const bool parts = mine && c0 < c1;
+      auto ml = [&](int64_t c) { return a.part_ml[(c * 2 + (c == c0)) * kHeads + h % kHeads]; };
+      if (parts)
+        for (int64_t c = c0 + (tid & 7); c <= c1; c += 8) top = fmaxf(top, ml(c).x);
 #pragma unroll
       for (int w = 1; w < 8; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-      if (mine)
-        for (int s = tid & 7; s < used; s += 8) {
-          const float2 v = ml[(int64_t)s * kHeads];
+      if (parts)
+        for (int64_t c = c0 + (tid & 7); c <= c1; c += 8) {
+          const float2 v = ml(c);
           sum = fmaf(v.y, ex2(v.x - top), sum);
         }
 #pragma unroll
       for (int w = 1; w < 8; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+      if (mine && !parts && a.unit_ml) {
+        const float2 v = a.unit_ml[((int64_t)b * a.units + u) * kHeads + h % kHeads];
+        top = v.x;
+        sum = v.y;
+      }
       if (mine && (tid & 7) == 0) norm[tid / 8] = make_float2(top, sum == 0.f ? 0.f : 1.f / sum);
     }
     __syncthreads();
     if (blockIdx.x == 0) {
-      if (a.splits > 1)
-        for (int e = tid; e < heads * (D / 4); e += kJoinThreads) {
-          const int hh = e / (D / 4), h = h0 + hh, c = (e % (D / 4)) * 4;
-          const int64_t unit0 = ((int64_t)b * units + kv * a.head_blocks + h / kHeads) * a.splits;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int s = 0; s < used; ++s) {
-            const int64_t row = (unit0 + s) * kHeads + h % kHeads;
-            const float r = ex2(a.part_ml[row].x - norm[hh].x);
-            const float4 x = *reinterpret_cast<const float4*>(a.part_o + row * D + c);
-            v.x = fmaf(x.x, r, v.x);
-            v.y = fmaf(x.y, r, v.y);
-            v.z = fmaf(x.z, r, v.z);
-            v.w = fmaf(x.w, r, v.w);
+      // a warp (or half a warp) a part: the threads of a head's row share its parts out, then add up
+      constexpr int kRow = D / 4;                       // threads of a row
+      constexpr int kWays = kJoinThreads / kRow;        // parts looked at together
+      const int c4 = (tid % kRow) * 4, way = tid / kRow;
+      for (int hh = 0; hh < heads; ++hh) {
+        const int h = h0 + hh;
+        int64_t c0, c1;
+        ctas_of(kv * a.head_blocks + h / kHeads, c0, c1);
+        if (c0 == c1) continue;  // (the same for the whole block)
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int64_t c = c0 + way; c <= c1; c += kWays) {
+          const int64_t row = (c * 2 + (c == c0)) * kHeads + h % kHeads;
+          const float r = ex2(a.part_ml[row].x - norm[hh].x);
+          const float4 x = *reinterpret_cast<const float4*>(a.part_o + row * D + c4);
+          v.x = fmaf(x.x, r, v.x);
+          v.y = fmaf(x.y, r, v.y);
+          v.z = fmaf(x.z, r, v.z);
+          v.w = fmaf(x.w, r, v.w);
+        }
+        __syncthreads();
+        acc[tid] = v;
+        __syncthreads();
+        if (way == 0) {
+          for (int w = 1; w < kWays && w <= c1 - c0; ++w) {
+            const float4 x = acc[w * kRow + tid];
+            v.x += x.x;
+            v.y += x.y;
+            v.z += x.z;
+            v.w += x.w;
           }
           const float inv = norm[hh].y;
           const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * inv, v.y * inv);
@@ -492,16 +660,25 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const DecodeArgs
           uint2 w2;
           w2.x = *reinterpret_cast<const uint32_t*>(&lo);
           w2.y = *reinterpret_cast<const uint32_t*>(&hi);
-          *reinterpret_cast<uint2*>(a.out + ((int64_t)b * a.H + kv * a.group + h) * D + c) = w2;
+          *reinterpret_cast<uint2*>(a.out + ((int64_t)b * a.H + kv * a.group + h) * D + c4) = w2;
         }
+      }
     } else {
       const float* rows = a.scores + (((int64_t)b * a.pool.h_kv + kv) * a.max_pages * kPage) * a.score_heads + h0;
 #pragma unroll
       for (int i = 0; i < kJoinTokens / kJoinThreads; ++i) {
         const int tok = token0 + i * kJoinThreads + tid;
-        if (tok < len)
-          for (int h = 0; h < heads; ++h)
-            add[i] = fmaf(ex2(rows[(int64_t)tok * a.score_heads + h] - norm[h].x), norm[h].y, add[i]);
+        if (tok >= len) continue;
+        const float* row = rows + (int64_t)tok * a.score_heads;
+        if (a.score_heads == 1) {
+          add[i] = ex2(row[0] - norm[0].x) * norm[0].y;
+        } else {
+          for (int h = 0; h < heads; h += 2) {
+            const float2 x = *reinterpret_cast<const float2*>(row + h);
+            add[i] = fmaf(ex2(x.x - norm[h].x), norm[h].y, add[i]);
+            if (h + 1 < heads) add[i] = fmaf(ex2(x.y - norm[h + 1].x), norm[h + 1].y, add[i]);
+          }
+        }
       }
     }
   }
@@ -523,37 +700,34 @@ Kv4DecodePlan plan_kv4_decode(const Ctx& c, int batch, int max_pages, bool accum
   Kv4DecodePlan p;
   const starkv_config& f = c.cfg;
   p.head_blocks = (c.group + kHeads - 1) / kHeads;
+  p.units = f.num_kv_heads * p.head_blocks;
   int sms = 148;
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c.device);
-  // chunks of equal pages, so that a batch of ragged sequences makes equal work: about four
-  // rounds of the 4 CTAs that an SM holds, but 8 pages (2 a warp) at least
-  const int64_t units = (int64_t)(batch > 0 ? batch : 1) * f.num_kv_heads * p.head_blocks;
-  const int64_t want = ((int64_t)sms * 16 + units - 1) / units;
-  int64_t chunk = max_pages > 0 ? (max_pages + want - 1) / want : 1;
-  chunk = (chunk + kWarps - 1) / kWarps * kWarps;
-  if (chunk < 8) chunk = 8;
-  p.chunk = (int)chunk;
-  p.splits = max_pages > 0 ? (max_pages + p.chunk - 1) / p.chunk : 1;
+  // One round of CTAs, with 8 pages (2 a warp) at least where the tables are full; a whole unit
+  // each where no table holds more than kWholePages.
+  const int64_t most = (int64_t)batch * p.units * max_pages;
+  const int64_t round = (int64_t)sms * kCtas;
+  p.ctas = max_pages <= kWholePages ? 0 : (int)(most / 8 < round ? most / 8 : round);
   p.score_heads = !accumulate ? 0 : c.group == 1 ? 1 : (c.group + 1) / 2 * 2;
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t rows = (size_t)units * p.splits * kHeads;
-  p.off_ml = p.splits > 1 ? al(rows * f.head_dim * 4) : 0;
-  p.off_scores = p.off_ml + (p.splits > 1 || accumulate ? al(rows * 8) : 0);
-  p.ws_bytes = p.off_scores + al((size_t)(batch > 0 ? batch : 1) * f.num_kv_heads * max_pages * kPage * p.score_heads * 4);
+  const size_t rows = (size_t)p.ctas * 2 * kHeads;
+  p.off_ml = al(rows * f.head_dim * 4);
+  p.off_unit = p.off_ml + al(rows * 8);
+  p.off_scores = p.off_unit + (accumulate ? al((size_t)batch * p.units * kHeads * 8) : 0);
+  p.ws_bytes = p.off_scores + al((size_t)batch * f.num_kv_heads * max_pages * kPage * p.score_heads * 4);
   return p;
 }
 
 template <int D>
-static cudaError_t launch_decode_d(const Ctx& c, const DecodeArgs& a, int batch, const Kv4DecodePlan& plan,
-                                   bool accumulate, cudaStream_t s) {
+static cudaError_t launch_decode_d(const Ctx& c, const DecodeArgs& a, cudaStream_t s) {
   const int smem = DecodeSmem<D>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(kv4_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  e = launch_chained(kv4_decode_kernel<D>, dim3(plan.splits, c.cfg.num_kv_heads * plan.head_blocks, batch),
-                     dim3(kThreads), (size_t)smem, s, 1u, a);
-  if (e != cudaSuccess || (plan.splits == 1 && !accumulate)) return e;
-  const unsigned chunks = accumulate ? (unsigned)(((int64_t)a.max_pages * kPage + kJoinTokens - 1) / kJoinTokens) : 0;
-  return launch_chained(kv4_join_kernel<D>, dim3(1 + chunks, c.cfg.num_kv_heads, batch), dim3(kJoinThreads), 0, s, 1u,
+  const unsigned blocks = a.ctas > 0 ? (unsigned)a.ctas : (unsigned)(a.batch * a.units);
+  e = launch_chained(kv4_decode_kernel<D>, dim3(blocks), dim3(kThreads), (size_t)smem, s, 1u, a);
+  if (e != cudaSuccess || (a.ctas == 0 && !a.scores)) return e;
+  const unsigned chunks = a.scores ? (unsigned)(((int64_t)a.max_pages * kPage + kJoinTokens - 1) / kJoinTokens) : 0;
+  return launch_chained(kv4_join_kernel<D>, dim3(1 + chunks, c.cfg.num_kv_heads, a.batch), dim3(kJoinThreads), 0, s, 1u,
                         a);
 }
 
@@ -568,19 +742,20 @@ cudaError_t launch_kv4_decode(const Ctx& c, const starkv_kv4_cache& cache, const
   a.H = c.cfg.num_q_heads;
   a.group = c.group;
   a.head_blocks = plan.head_blocks;
+  a.units = plan.units;
+  a.batch = batch;
   a.max_pages = max_pages;
-  a.chunk = plan.chunk;
-  a.splits = plan.splits;
+  a.ctas = plan.ctas;
   a.score_heads = plan.score_heads;
   a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)c.cfg.head_dim));
   a.pool = Kv4Pool{(uint8_t*)cache.pages, cache.weights, cache.n_pages, c.cfg.num_kv_heads};
   a.out = out;
-  a.part_o = plan.splits > 1 ? (float*)ws : nullptr;
-  a.part_ml = plan.splits > 1 || accumulate ? (float2*)((char*)ws + plan.off_ml) : nullptr;
+  a.part_o = (float*)ws;
+  a.part_ml = (float2*)((char*)ws + plan.off_ml);
+  a.unit_ml = accumulate ? (float2*)((char*)ws + plan.off_unit) : nullptr;
   a.scores = accumulate ? (float*)((char*)ws + plan.off_scores) : nullptr;
   a.status = c.status;
-  return c.cfg.head_dim == 64 ? launch_decode_d<64>(c, a, batch, plan, accumulate, s)
-                              : launch_decode_d<128>(c, a, batch, plan, accumulate, s);
+  return c.cfg.head_dim == 64 ? launch_decode_d<64>(c, a, s) : launch_decode_d<128>(c, a, s);
 }
 
 }  // namespace starkv

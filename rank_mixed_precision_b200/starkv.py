@@ -378,19 +378,33 @@ def _rows(t, heads, d, name):
         raise TypeError(f"{name} must be a torch.bfloat16 tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
-        raise ValueError(f"{name} must be [n, {heads}, {d}], got {tuple(t.shape)}")
-    if t.shape[0] == 0:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d:
+        raise ValueError(f"{name} must be [n, {heads}, {d}], got {tuple(shape)}")
+    if shape[0] == 0:
         return heads * d
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+    if stride[2] != 1 or (heads > 1 and stride[1] != d):
         raise ValueError(f"{name}: the heads of a row must be dense")
-    return t.stride(0) if t.shape[0] > 1 else heads * d
+    return stride[0] if shape[0] > 1 else heads * d
 
 
 def _one_device(first, *others):
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"arguments on {first.device} and {t.device}")
+    """Every argument lies on the current device (whose stream the call goes to)."""
+    at = torch._C._cuda_getDevice()
+    for t in (first, *others):
+        if t is not None and t.get_device() != at:
+            raise ValueError(f"an argument is on {t.device}, the current device is cuda:{at}")
+
+
+def _on(stream):
+    """The stream's handle; None: the current stream of the current device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def starkv_kv4_layout(cfg: starkv_config, n_pages: int) -> dict:
@@ -410,8 +424,8 @@ def starkv_kv4_append(ctx, cfg, cache: starkv_kv4_cache, k, v, slot_mapping, wei
     if slot_mapping.shape[0] != k.shape[0] or v.shape[0] != k.shape[0]:
         raise ValueError("k, v and slot_mapping disagree on n")
     _one_device(k, v, slot_mapping, weights)
-    _check(lib().starkv_kv4_append(ctx, ctypes.byref(cache), _p(k), _p(v), ks, vs, _p(slot_mapping), _p(weights),
-                                   k.shape[0], _stream(stream)))
+    _check(lib().starkv_kv4_append(ctx, ctypes.byref(cache), _at(k), _at(v), ks, vs, _at(slot_mapping), _at(weights),
+                                   k.shape[0], _on(stream)))
 
 
 def starkv_kv4_read(ctx, cfg, cache: starkv_kv4_cache, block_table, cu, k_out, v_out, starts=None, stream=None):
@@ -428,8 +442,8 @@ def starkv_kv4_read(ctx, cfg, cache: starkv_kv4_cache, block_table, cu, k_out, v
     if cu.shape[0] != B + 1 or (starts is not None and starts.shape[0] != B):
         raise ValueError("block_table / cu / starts disagree on the batch")
     _one_device(k_out, v_out, block_table, cu, starts)
-    _check(lib().starkv_kv4_read(ctx, ctypes.byref(cache), _p(block_table), _p(starts), _p(cu), B,
-                                 block_table.shape[1], k_out.shape[0], _p(k_out), _p(v_out), _stream(stream)))
+    _check(lib().starkv_kv4_read(ctx, ctypes.byref(cache), _at(block_table), _at(starts), _at(cu), B,
+                                 block_table.shape[1], k_out.shape[0], _at(k_out), _at(v_out), _on(stream)))
 
 
 def starkv_kv4_decode_attn(ctx, cfg, cache: starkv_kv4_cache, q, block_table, seq_lens, accumulate, out, workspace,
@@ -447,9 +461,9 @@ def starkv_kv4_decode_attn(ctx, cfg, cache: starkv_kv4_cache, q, block_table, se
     if workspace is not None:
         _need(workspace, torch.uint8, "workspace", 1)
     _one_device(q, block_table, seq_lens, out, workspace)
-    _check(lib().starkv_kv4_decode_attn(ctx, ctypes.byref(cache), _p(q), _p(block_table), _p(seq_lens), B,
-                                        block_table.shape[1], int(bool(accumulate)), _p(out), _p(workspace),
-                                        0 if workspace is None else workspace.numel(), _stream(stream)))
+    _check(lib().starkv_kv4_decode_attn(ctx, ctypes.byref(cache), _at(q), _at(block_table), _at(seq_lens), B,
+                                        block_table.shape[1], int(bool(accumulate)), _at(out), _at(workspace),
+                                        0 if workspace is None else workspace.numel(), _on(stream)))
 
 
 def starkv_kv4_evict(ctx, cfg, cache: starkv_kv4_cache, block_table, seq_lens, keep_lens, recent, dst_block_table,
@@ -466,9 +480,9 @@ def starkv_kv4_evict(ctx, cfg, cache: starkv_kv4_cache, block_table, seq_lens, k
     if dst_block_table.shape[0] != B or tuple(kept.shape) != (B, cfg.num_kv_heads, cap):
         raise ValueError(f"dst_block_table must have {B} rows and kept be [{B}, {cfg.num_kv_heads}, {cap}]")
     _one_device(block_table, seq_lens, keep_lens, dst_block_table, new_lens, kept)
-    _check(lib().starkv_kv4_evict(ctx, ctypes.byref(cache), _p(block_table), _p(seq_lens), _p(keep_lens), int(recent),
-                                  B, block_table.shape[1], _p(dst_block_table), dst_block_table.shape[1],
-                                  _p(new_lens), _p(kept), _stream(stream)))
+    _check(lib().starkv_kv4_evict(ctx, ctypes.byref(cache), _at(block_table), _at(seq_lens), _at(keep_lens), int(recent),
+                                  B, block_table.shape[1], _at(dst_block_table), dst_block_table.shape[1],
+                                  _at(new_lens), _at(kept), _on(stream)))
 
 
 def _packed(cfg, q, k, cu_q, cu_k):
@@ -493,8 +507,8 @@ def starkv_prompt_attn(ctx, cfg, q, k, v, cu_q, cu_k, max_q_len, out, lse=None, 
         if tuple(lse.shape) != tuple(q.shape[:2]):
             raise ValueError("lse must be [total_q, num_q_heads]")
     _one_device(q, k, v, cu_q, cu_k, out, lse)
-    _check(lib().starkv_prompt_attn(ctx, _p(q), _p(k), _p(v), qs, ks, vs, _p(cu_q), _p(cu_k), cu_q.shape[0] - 1,
-                                    q.shape[0], k.shape[0], int(max_q_len), _p(out), _p(lse), _stream(stream)))
+    _check(lib().starkv_prompt_attn(ctx, _at(q), _at(k), _at(v), qs, ks, vs, _at(cu_q), _at(cu_k), cu_q.shape[0] - 1,
+                                    q.shape[0], k.shape[0], int(max_q_len), _at(out), _at(lse), _on(stream)))
 
 
 def starkv_prompt_weights(ctx, cfg, q, k, lse, cu_q, cu_k, max_k_len, window, weights, stream=None):
@@ -505,9 +519,9 @@ def starkv_prompt_weights(ctx, cfg, q, k, lse, cu_q, cu_k, max_k_len, window, we
     if tuple(lse.shape) != tuple(q.shape[:2]) or tuple(weights.shape) != tuple(k.shape[:2]):
         raise ValueError("lse must be [total_q, num_q_heads] and weights [total_k, num_kv_heads]")
     _one_device(q, k, lse, cu_q, cu_k, weights)
-    _check(lib().starkv_prompt_weights(ctx, _p(q), _p(k), qs, ks, _p(lse), _p(cu_q), _p(cu_k), cu_q.shape[0] - 1,
-                                       q.shape[0], k.shape[0], int(max_k_len), int(window), _p(weights),
-                                       _stream(stream)))
+    _check(lib().starkv_prompt_weights(ctx, _at(q), _at(k), qs, ks, _at(lse), _at(cu_q), _at(cu_k), cu_q.shape[0] - 1,
+                                       q.shape[0], k.shape[0], int(max_k_len), int(window), _at(weights),
+                                       _on(stream)))
 
 
 # ---------------------------------------------------------------------------
@@ -531,47 +545,48 @@ class LatentCache:
         return sum(self.sizes[k] for k in ("k_codes_bytes", "v_codes_bytes", "k_meta_bytes", "v_meta_bytes"))
 
 
+_kv4_page_bytes = {}  # head_page_bytes by head_dim, as the library lays pages out
+
+
 class KV4Cache:
     """The 4-bit paged cache of a full-width layer: pages [n_pages, num_kv_heads, head_page_bytes] and, where tokens'
     accumulated attention weights are kept, weights [n_pages, num_kv_heads, 16].  Allocated with torch, or the caller's."""
 
     def __init__(self, cfg: starkv_config, n_pages=None, pages=None, weights=None, keep_weights=False, device="cuda"):
+        h, page = cfg.num_kv_heads, _kv4_page_bytes.get(cfg.head_dim)
+        if page is None:
+            page = _kv4_page_bytes[cfg.head_dim] = starkv_kv4_layout(cfg, 0)["head_page_bytes"]
         if pages is None:
-            if n_pages is None:
-                raise ValueError("n_pages or pages")
-            self.sizes = starkv_kv4_layout(cfg, n_pages)
-            pages = torch.zeros((n_pages, cfg.num_kv_heads, self.sizes["head_page_bytes"]), dtype=torch.uint8,
-                                device=device)
+            if n_pages is None or n_pages < 0:
+                raise ValueError("n_pages (>= 0) or pages")
+            pages = torch.zeros((n_pages, h, page), dtype=torch.uint8, device=device)
         else:
             _need(pages, torch.uint8, "pages", 3)
             if n_pages is not None and n_pages != pages.shape[0]:
                 raise ValueError("n_pages and pages disagree")
             n_pages = pages.shape[0]
-            self.sizes = starkv_kv4_layout(cfg, n_pages)
-            if tuple(pages.shape[1:]) != (cfg.num_kv_heads, self.sizes["head_page_bytes"]):
-                raise ValueError(f"pages must be [n_pages, {cfg.num_kv_heads}, {self.sizes['head_page_bytes']}]")
+            if pages.shape[1] != h or pages.shape[2] != page:
+                raise ValueError(f"pages must be [n_pages, {h}, {page}]")
         if weights is None:
             if keep_weights:
-                weights = torch.zeros((n_pages, cfg.num_kv_heads, PAGE_TOKENS), dtype=torch.float32, device=pages.device)
+                weights = torch.zeros((n_pages, h, PAGE_TOKENS), dtype=torch.float32, device=pages.device)
         else:
             _need(weights, torch.float32, "weights", 3)
-            if tuple(weights.shape) != (n_pages, cfg.num_kv_heads, PAGE_TOKENS):
-                raise ValueError(f"weights must be [{n_pages}, {cfg.num_kv_heads}, {PAGE_TOKENS}]")
-            _one_device(pages, weights)
+            if weights.shape != (n_pages, h, PAGE_TOKENS) or weights.get_device() != pages.get_device():
+                raise ValueError(f"weights must be [{n_pages}, {h}, {PAGE_TOKENS}], on the pages' device")
         self.n_pages, self.pages, self.weights = n_pages, pages, weights
         self.struct = starkv_kv4_cache(pages.data_ptr(), None if weights is None else weights.data_ptr(), n_pages)
 
     def nbytes(self) -> int:
-        return self.sizes["pages_bytes"] + (self.sizes["weights_bytes"] if self.weights is not None else 0)
+        return self.pages.numel() + (0 if self.weights is None else 4 * self.weights.numel())
 
 
-def _new(shape, dtype, device, stream):
-    """An uninitialised tensor that a call on `stream` may use (it is given back behind that stream's work)."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if isinstance(stream, torch.cuda.Stream):
-        t.record_stream(stream)
-    elif stream is not None:
-        t.record_stream(torch.cuda.ExternalStream(int(stream), device=device))
+def _new(like, shape, dtype, stream):
+    """An uninitialised tensor beside `like` that a call on `stream` may use (it is given back behind that stream's work)."""
+    t = like.new_empty(shape, dtype=dtype)
+    if stream is not None:
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                        torch.cuda.ExternalStream(int(stream), device=t.device))
     return t
 
 
@@ -623,45 +638,46 @@ class StarKV:
         return KV4Cache(self.cfg, n_pages, keep_weights=keep_weights)
 
     def kv4_append(self, cache: KV4Cache, k, v, slot_mapping, weights=None, stream=None):
-        _one_device(k, cache.pages)
+        _one_device(cache.pages)
         starkv_kv4_append(self.ctx, self.cfg, cache.struct, k, v, slot_mapping, weights, stream)
 
     def kv4_read(self, cache: KV4Cache, block_table, cu, total: int, starts=None, stream=None):
         """Keys and values [total, num_kv_heads, head_dim] of tokens starts[b] .. of each sequence."""
-        k, v = (_new((total, self.cfg.num_kv_heads, self.cfg.head_dim), torch.bfloat16, cache.pages.device, stream)
-                for _ in range(2))
+        shape = (total, self.cfg.num_kv_heads, self.cfg.head_dim)
+        k = _new(cache.pages, shape, torch.bfloat16, stream)
+        v = _new(cache.pages, shape, torch.bfloat16, stream)
         starkv_kv4_read(self.ctx, self.cfg, cache.struct, block_table, cu, k, v, starts, stream)
         return k, v
 
     def kv4_decode(self, cache: KV4Cache, q, block_table, seq_lens, accumulate=False, out=None, stream=None):
-        _one_device(q, cache.pages)
+        _one_device(cache.pages)
         n = starkv_workspace_bytes(self.ctx, OP_KV4_DECODE, block_table.shape[0], block_table.shape[1], int(accumulate))
-        ws = _new((n,), torch.uint8, q.device, stream) if n else None
-        out = _new(q.shape, q.dtype, q.device, stream) if out is None else out
+        ws = _new(cache.pages, n, torch.uint8, stream) if n else None
+        out = _new(q, q.shape, q.dtype, stream) if out is None else out
         starkv_kv4_decode_attn(self.ctx, self.cfg, cache.struct, q, block_table, seq_lens, accumulate, out, ws, stream)
         return out
 
     def kv4_evict(self, cache: KV4Cache, block_table, seq_lens, keep_lens, recent: int, dst_block_table, stream=None):
         """Gather the kept tokens into dst_block_table's pages: their new lengths [batch], and their indices
         [batch, num_kv_heads, dst_max_pages * 16] (-1 behind the last)."""
-        _one_device(block_table, cache.pages)
+        _one_device(cache.pages)
         B, h = block_table.shape[0], self.cfg.num_kv_heads
-        new_lens = _new((B,), torch.int32, block_table.device, stream)
-        kept = _new((B, h, dst_block_table.shape[1] * PAGE_TOKENS), torch.int32, block_table.device, stream)
+        new_lens = _new(block_table, B, torch.int32, stream)
+        kept = _new(block_table, (B, h, dst_block_table.shape[1] * PAGE_TOKENS), torch.int32, stream)
         starkv_kv4_evict(self.ctx, self.cfg, cache.struct, block_table, seq_lens, keep_lens, recent, dst_block_table,
                          new_lens, kept, stream)
         return new_lens, kept
 
     def prompt(self, q, k, v, cu_q, cu_k, max_q_len: int, out=None, stream=None):
         """Causal attention of packed prompts: (out [total_q, H, d], lse [total_q, H])."""
-        out = _new(q.shape, q.dtype, q.device, stream) if out is None else out
-        lse = _new(q.shape[:2], torch.float32, q.device, stream)
+        out = _new(q, q.shape, q.dtype, stream) if out is None else out
+        lse = _new(q, q.shape[:2], torch.float32, stream)
         starkv_prompt_attn(self.ctx, self.cfg, q, k, v, cu_q, cu_k, max_q_len, out, lse, stream)
         return out, lse
 
     def prompt_weights(self, q, k, lse, cu_q, cu_k, max_k_len: int, window: int, stream=None):
         """Attention weight [total_k, num_kv_heads] that each sequence's last `window` queries give to its keys."""
-        weights = _new(k.shape[:2], torch.float32, k.device, stream)
+        weights = _new(k, k.shape[:2], torch.float32, stream)
         starkv_prompt_weights(self.ctx, self.cfg, q, k, lse, cu_q, cu_k, max_k_len, window, weights, stream)
         return weights
 
