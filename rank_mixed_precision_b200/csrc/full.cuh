@@ -70,6 +70,7 @@ struct PromptArgs {
   int64_t total_q, total_k;
 };
 int64_t prompt_blocks(const Ctx& c, int batch, int max_q_len);
+int64_t weights_items(const Ctx& c, int batch, int max_k_len);
 cudaError_t launch_prompt_attn(const Ctx& c, const PromptArgs& a, int max_q_len, __nv_bfloat16* out, float* lse,
                                cudaStream_t s);
 cudaError_t launch_prompt_weights(const Ctx& c, const PromptArgs& a, const float* lse, int max_k_len, int window,

@@ -216,6 +216,7 @@ starkv_status starkv_prompt_weights(starkv_ctx* ctx, const void* q, const void* 
   if (st) return st;
   if ((total_q > 0 && !lse) || !weights || !aligned(lse, 4) || !aligned(weights, 4))
     return fail(STARKV_ERR_INVALID_ARG, "lse and weights must be given and 4-byte aligned");
+  if (weights_items(*c, batch, max_k_len) > kMaxBlocks) return fail(STARKV_ERR_UNSUPPORTED_SHAPE, "too many key tiles");
   PromptArgs a{(const __nv_bfloat16*)q, (const __nv_bfloat16*)k, nullptr, q_stride, k_stride, 0, cu_q, cu_k, batch,
                total_q, total_k};
   const cudaError_t e = launch_prompt_weights(*c, a, lse, max_k_len, window, weights, (cudaStream_t)stream);

@@ -27,17 +27,48 @@ struct AppendArgs {
 };
 
 constexpr int kRowThreads = 256;
-constexpr int kRowTokens = 4;  // tokens a block takes where there are many
+constexpr int kRowTokens = 4;   // tokens a block takes where there are many: append,
+constexpr int kReadTokens = 8;  // and read
 
-// code of x >= z: clamp(rint(fl((x - z) / s)), 0, 15), inv = fl(1 / s).  (x - z) * inv is
-// within 2^-23 of the quotient (relative; 4e-6 for what is not clamped), so it rounds to
-// the same integer unless it lies that close to a half; there the quotient is taken.
-__device__ __forceinline__ uint32_t code_of(float x, float z, float s, float inv) {
-  const float a = __fsub_rn(x, z);
-  float q = fminf(fmaxf(a * inv, 0.f), 15.f);
-  float r = q + 12582912.f;  // 1.5 2^23: the sum's low bits are rint(q)
-  if (fabsf(q - (r - 12582912.f)) > 0.49999f) r = fminf(fmaxf(__fdiv_rn(a, s), 0.f), 15.f) + 12582912.f;
-  return __float_as_uint(r) & 15u;
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// fl16(fl32(d / 15)).  d * fl(1/15) is within 2^-23 of the quotient (relative), so where both ends
+// of that interval round to the same fp16 number it is the one; else the quotient is taken.
+__device__ __forceinline__ __half scale_of(float d) {
+  const float q = d * 0.0666666666666666666667f;
+  const __half lo = __float2half_rn(q * 0.9999997f), hi = __float2half_rn(q * 1.0000003f);
+  return __half_as_ushort(lo) == __half_as_ushort(hi) ? lo : __float2half_rn(__fdiv_rn(d, 15.f));
+}
+
+// Eight codes clamp(rint(fl(fl(x - z) / s)), 0, 15) in a word, low nibble first; r: the channels
+// in bf16 pairs.  A product with 1 / (15 s) saturates to [0, 1]; 15 of it is within 5e-6 of the
+// clamped quotient and rounds to the same integer unless it lies that close to a half: then (a
+// word in a hundred or fewer) the quotients are taken.
+__device__ __forceinline__ uint32_t codes_of(const uint32_t (&r)[4], float z, float s) {
+  const float inv = rcp_approx(s) * 0.0666666666666666666667f;
+  uint32_t word = 0;
+  float off = 0.f;  // largest distance from an integer
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float x = __uint_as_float(e & 1 ? r[e >> 1] & 0xffff0000u : r[e >> 1] << 16);
+    const float q = __saturatef(__fsub_rn(x, z) * inv);
+    const float n = fmaf(q, 15.f, 12582912.f);  // 1.5 2^23: the sum's low bits are the integer
+    off = fmaxf(off, fabsf(fmaf(q, 15.f, 12582912.f - n)));
+    word += (__float_as_uint(n) - 0x4b400000u) << (4 * e);
+  }
+  if (off > 0.49999f) {
+    word = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = __uint_as_float(e & 1 ? r[e >> 1] & 0xffff0000u : r[e >> 1] << 16);
+      word |= (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x, z), s)), 0.f), 15.f) << (4 * e);
+    }
+  }
+  return word;
 }
 
 template <int D, int T>
@@ -85,7 +116,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const AppendArg
     }
     if (slot[i] < 0) continue;
     const float mn = __low2float(m), mx = -__high2float(m);
-    __half s16 = __float2half_rn(__fdiv_rn(__fsub_rn(mx, mn), 15.f));
+    __half s16 = scale_of(__fsub_rn(mx, mn));
     __half z16 = __float2half_rn(mn);
     const float sf = __half2float(s16), zf = __half2float(z16);
     // decode widens code * s + z in fp16, so the top code must stay inside it too
@@ -96,12 +127,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const AppendArg
       s16 = z16 = __float2half_rn(0.f);
       if ((w & 3) == 0) set_status(a.status, STARKV_DEV_QUANT_OVERFLOW);
     } else if (sf != 0.f) {
-      const float inv = __frcp_rn(sf);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        code |= code_of(__uint_as_float(r[e] << 16), zf, sf, inv) << (8 * e);
-        code |= code_of(__uint_as_float(r[e] & 0xffff0000u), zf, sf, inv) << (8 * e + 4);
-      }
+      code = codes_of(r, zf, sf);
     }
     const int64_t page = slot[i] / kPage;
     const int t = (int)(slot[i] % kPage);
@@ -492,9 +518,9 @@ Kv4Pool pool_of(const Ctx& c, const starkv_kv4_cache& cache) {
 
 }  // namespace
 
-// Blocks of kRowTokens tokens where they fill the GPU twice over, else of one (a decode step's write
+// Blocks of several tokens where they fill the GPU twice over, else of one (a decode step's write
 // spreads over more SMs).
-static bool many_rows(int64_t n, unsigned gy) { return (n + kRowTokens - 1) / kRowTokens * gy >= 2 * 148; }
+static bool many_rows(int64_t n, int each, unsigned gy) { return (n + each - 1) / each * gy >= 2 * 148; }
 
 cudaError_t launch_kv4_append(const Ctx& c, const starkv_kv4_cache& cache, const __nv_bfloat16* k,
                               const __nv_bfloat16* v, int64_t k_stride, int64_t v_stride, const int64_t* slots,
@@ -503,7 +529,7 @@ cudaError_t launch_kv4_append(const Ctx& c, const starkv_kv4_cache& cache, const
   const int d = c.cfg.head_dim;
   const unsigned gy = (unsigned)((c.cfg.num_kv_heads * (2 * d / 8) + kRowThreads - 1) / kRowThreads);
   const dim3 block(kRowThreads);
-  if (many_rows(n, gy)) {
+  if (many_rows(n, kRowTokens, gy)) {
     const dim3 grid((unsigned)((n + kRowTokens - 1) / kRowTokens), gy);
     return launch_chained(d == 64 ? kv4_append_kernel<64, kRowTokens> : kv4_append_kernel<128, kRowTokens>, grid, block,
                           0, s, 1u, a);
@@ -519,9 +545,9 @@ cudaError_t launch_kv4_read(const Ctx& c, const starkv_kv4_cache& cache, const i
   const int d = c.cfg.head_dim;
   const unsigned gy = (unsigned)((c.cfg.num_kv_heads * (2 * d / 8) + kRowThreads - 1) / kRowThreads);
   const dim3 block(kRowThreads);
-  if (many_rows(total, gy)) {
-    const dim3 grid((unsigned)((total + kRowTokens - 1) / kRowTokens), gy);
-    return launch_chained(d == 64 ? kv4_read_kernel<64, kRowTokens> : kv4_read_kernel<128, kRowTokens>, grid, block, 0,
+  if (many_rows(total, kReadTokens, gy)) {
+    const dim3 grid((unsigned)((total + kReadTokens - 1) / kReadTokens), gy);
+    return launch_chained(d == 64 ? kv4_read_kernel<64, kReadTokens> : kv4_read_kernel<128, kReadTokens>, grid, block, 0,
                           s, 1u, a);
   }
   return launch_chained(d == 64 ? kv4_read_kernel<64, 1> : kv4_read_kernel<128, 1>, dim3((unsigned)total, gy), block, 0,

@@ -64,7 +64,7 @@ struct SeqSpan {
 };
 
 struct PromptKArgs {
-  int H, h_kv, group, gb, head_blocks, R, batch, max_q, max_k, qtiles, window;
+  int H, h_kv, group, gb, head_blocks, R, batch, max_q, max_k, qtiles, ktiles, window, mode;
   int64_t total_q, total_k;
   const __nv_bfloat16* v;
   int64_t v_stride;
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       int issued = 0;
       for (; issued < 2 * nt; ++issued) {
         const int s = issued % ST, j = issued >> 1;
-        if (!mbar_wait(&empty[s], ((issued / ST) & 1) ^ 1)) {
+        if (!mbar_wait_short(&empty[s], ((issued / ST) & 1) ^ 1)) {
           ok = false;
           break;
         }
@@ -230,8 +230,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         mma_commit(&sfull[t]);
       };
-      auto wait_full = [&](int i) { return mbar_wait_poll(&full[i % ST], (i / ST) & 1); };
-      ok = mbar_wait_poll(qfull, 0) && wait_full(0);
+      auto wait_full = [&](int i) { return mbar_wait_short(&full[i % ST], (i / ST) & 1); };
+      ok = mbar_wait_short(qfull, 0) && wait_full(0);
       if (ok) {
         tc_fence_after();
         if (ntile[0] > 0) issue_s(0, 0);
@@ -243,13 +243,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ok = wait_full(2 * j + 1);
         if (ok && j >= first_masked) {
           mbar_arrive(look);
-          ok = mbar_wait_poll(clean, looked++ & 1);
+          ok = mbar_wait_short(clean, looked++ & 1);
         }
         if (ok && j + 1 < nt) ok = wait_full(2 * j + 2);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (!ok || j >= ntile[t]) continue;
-          if (!mbar_wait_poll(&pfull[t], j & 1)) {
+          if (!mbar_wait_short(&pfull[t], j & 1)) {
             ok = false;
             continue;
           }
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // behind the sequence, whatever they hold) and, where a row does see them, added at the end.
     for (int j = first_masked; ok && j < nt; ++j) {
       const int i = 2 * j + 1;
-      const bool got = mbar_wait(look, (j - first_masked) & 1) && mbar_wait(&full[i % ST], (i / ST) & 1);
+      const bool got = mbar_wait_short(look, (j - first_masked) & 1) && mbar_wait_short(&full[i % ST], (i / ST) & 1);
       if (!__all_sync(0xffffffffu, got)) {
         ok = false;
         break;
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t ts = trow + t * kTile, to = trow + 256 + t * kTile;
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < ntile[t]; ++j) {
-      if (!__all_sync(0xffffffffu, mbar_wait_poll(&sfull[t], j & 1))) {
+      if (!__all_sync(0xffffffffu, mbar_wait_short(&sfull[t], j & 1))) {
         ok = false;
         break;
       }
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (lane == 0) mbar_arrive(&pfull[t]);
     }
     // ---- O / l, and lse
-    if (ntile[t] > 0 && ok && !__all_sync(0xffffffffu, mbar_wait(odone, 0))) ok = false;
+    if (ntile[t] > 0 && ok && !__all_sync(0xffffffffu, mbar_wait_short(odone, 0))) ok = false;
     if (ok) {
       tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -433,22 +433,117 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // ===========================================================================
 // Attention weights
 // ===========================================================================
-// A CTA takes 128 keys of one (sequence, KV head), holds their K tile and walks the
-// query tiles: S^T = K Q^T into TMEM (four buffers), one key per lane, so that the sum
-// over queries and heads stays in a register.  Warps 0..3 take the even tiles, 4..7 the
-// odd ones, warp 8 copies, warp 9 issues the products, warps 10 and 11 lay out each
-// column's log-sum-exp and the last key it sees.
-constexpr int kWeightThreads = 384;
+// An item is 128 keys of one (sequence, KV head); its steps are the tiles of queries that
+// count and see any of them.  A step's product S^T = K Q^T (TMEM, four buffers) has one
+// key per lane, so that the sum over queries and heads stays in a register of the thread
+// that holds the key.  Warps 0..7 take the even steps, 8..15 the odd ones, half of the
+// columns each (four warps a scheduler keep the exponentials going while others wait for
+// their columns); warp 16 copies, warp 17 issues the products and notes for each what its sums go by, warps 18
+// and 19 lay out each column's log-sum-exp and the last key it sees.  One CTA an SM walks over many items, three ways:
+//   resident  the counting queries of a (sequence, KV head) fit the ring (a window): a CTA
+//             takes an equal stretch of the items in (sequence, KV head, key) order and
+//             loads them once per (sequence, KV head); only K tiles stream.
+//   streamed  items in the order of their first key (those of the first keys have the most
+//             steps), dealt forth and back, so that the CTAs' sums of steps come out alike.
+//   split     where there are few items, a cluster shares one item's steps out and adds the
+//             sums through distributed shared memory, in rank order.
+constexpr int kWeightThreads = 640;
 constexpr int kColNone = -(1 << 30);  // a column that sees no key
+enum { kResident = 0, kStreamed = 1 };  // > 1: split over so many CTAs
 
 template <int D>
 struct WeightSmem {
   static constexpr uint32_t kTileBytes = kTile * D * 2;
-  static constexpr int kStages = 4;
-  static constexpr uint32_t kRing = kTileBytes;  // behind the K tile
-  static constexpr uint32_t kCols = kRing + kStages * kTileBytes;  // [stage][128] (lse in log2 units), [stage][128] last key
-  static constexpr uint32_t kBar = kCols + kStages * kTile * 8;
-  static constexpr uint32_t kBytes = kBar + 256 + 1024;
+  static constexpr int kStages = D == 128 ? 3 : 6;   // Q tiles
+  static constexpr int kKeys = D == 128 ? 3 : 4;     // K tiles
+  static constexpr uint32_t kRing = kKeys * kTileBytes;
+  static constexpr uint32_t kCols = kRing + kStages * kTileBytes;  // [stage][128] lse in log2 units, [stage][128] last key
+  static constexpr uint32_t kSums = kCols + kStages * kTile * 8;   // [2][3][128] sums of warps 4 .. 15
+  static constexpr uint32_t kNotes = kSums + 2 * 3 * kTile * 4;    // [4] what a product's sums go by
+  static constexpr uint32_t kBar = kNotes + 4 * 32;
+  static constexpr uint32_t kBytes = kBar + 512 + 1024;
+};
+
+// One product's note, beside its TMEM buffer.
+struct __align__(16) Note {
+  int flags;     // kWhole: no column is masked for any key; kLast: the item's last step; kLeave: its Q tile's last use; kStop
+  int stage;     // the Q tile's
+  int live;      // columns that hold queries
+  int key0, keys;  // the item's first key, and the keys of its sequence
+  int unused;
+  int64_t row;   // the sequence's first row, times h_kv, plus the KV head
+};
+static_assert(sizeof(Note) == 32, "a note is two 16-byte words");
+enum { kWhole = 1, kLast = 2, kLeave = 4, kStop = 8 };
+
+// The items of a CTA, in order; every role walks its own copy.
+struct Items {
+  const PromptKArgs& a;
+  int64_t at, end;   // resident: positions of the stretch; streamed: the turn
+  int64_t before;    // resident: items of the sequences before b
+  int b, kv, kt, tiles;
+  SeqSpan q;
+  int off, first, per, steps;
+  bool fresh;        // another (sequence, KV head) than the item before
+  bool started;
+
+  __device__ Items(const PromptKArgs& args, int64_t pos, int64_t stop, int seq, int64_t items_before)
+      : a(args), at(pos), end(stop), before(items_before), b(seq), kv(-1), kt(0), tiles(0), started(false) {}
+
+  __device__ void steps_of() {
+    off = q.keys - q.n;
+    // queries first .. n - 1 count; the tile's first key is seen from query kt * 128 - off on
+    // (resident: the sequence's Q tiles serve all its items)
+    first = max(max(0, q.n - a.window), (a.mode == kResident ? 0 : kt * kTile) - off);
+    per = first < q.n ? (q.n - first + a.R - 1) / a.R : 0;
+    steps = per * a.head_blocks;
+  }
+
+  __device__ bool next() {
+    if (a.mode == kResident) {
+      if (at >= end) return false;
+      fresh = true;
+      if (!started) {
+        started = true;
+        q = span_of(a, b);
+        tiles = (q.keys + kTile - 1) / kTile;
+        kv = (int)((at - before) / tiles);
+        kt = (int)((at - before) - (int64_t)kv * tiles);
+      } else if (++kt < tiles) {
+        fresh = false;
+      } else {
+        kt = 0;
+        if (++kv == a.h_kv) {
+          kv = 0;
+          do {  // (a position behind this one is some sequence's)
+            q = span_of(a, ++b);
+            tiles = q.ok ? (q.keys + kTile - 1) / kTile : 0;
+          } while (tiles == 0);
+        }
+      }
+      ++at;
+      if (fresh) steps_of();
+      return true;
+    }
+    const uint32_t each = (uint32_t)a.h_kv * a.batch, items = each * a.ktiles;  // (below 2^32: checked)
+    fresh = true;
+    while (at < end) {
+      // turn i takes item i C + c, or i C + C - 1 - c where i is odd
+      const uint32_t ctas = a.mode > 1 ? items : gridDim.x, c = a.mode > 1 ? blockIdx.x / a.mode : blockIdx.x;
+      const int64_t at_item = at * ctas + (at & 1 ? ctas - 1 - c : c);
+      ++at;
+      if (at_item >= items) continue;
+      const uint32_t w = (uint32_t)at_item;
+      kt = (int)(w / each);
+      kv = (int)(w % each % a.h_kv);
+      b = (int)(w % each / a.h_kv);
+      q = span_of(a, b);
+      if (!q.ok || kt * kTile >= q.keys) continue;
+      steps_of();
+      return true;
+    }
+    return false;
+  }
 };
 
 template <int D>
@@ -457,35 +552,30 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
                           const PromptKArgs a) {
   using SM = WeightSmem<D>;
   constexpr int NSUB = D / 64;
-  constexpr int ST = SM::kStages;
+  constexpr int ST = SM::kStages, KS = SM::kKeys;
   extern __shared__ uint8_t smem_raw[];
+  __shared__ int64_t part[kWeightThreads / 32];
+  __shared__ int64_t begin[2];
   uint8_t* sm = align1024(smem_raw);
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + SM::kBar);
-  uint64_t* kfull = bar;
-  uint64_t* full = bar + 1;        // [ST] Q tile landed
-  uint64_t* cols = full + ST;      // [ST] columns laid out (2 warps)
-  uint64_t* empty = cols + ST;     // [ST] Q tile read by its products, columns by the 4 warps
-  uint64_t* sfull = empty + ST;    // [4]
-  uint64_t* sempty = sfull + 4;    // [4]
-  uint64_t* done = sempty + 4;
+  uint64_t* kfull = bar;           // [KS]
+  uint64_t* kempty = kfull + KS;   // [KS]
+  uint64_t* full = kempty + KS;    // [ST] Q tile landed
+  uint64_t* cols = full + ST;      // [ST] its columns laid out (2 warps)
+  uint64_t* empty = cols + ST;     // [ST] Q tile read by its products, its columns by 8 warps
+  uint64_t* sfull = empty + ST;    // [4] a product and its note are there,
+  uint64_t* sempty = sfull + 4;    // [4] and have been read
+  uint64_t* sums = sempty + 4;     // [2][4] three warps' sums are there
+  uint64_t* taken = sums + 8;      // [2][4] and have been added
+  uint64_t* done = taken + 8;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
   float* lse2 = reinterpret_cast<float*>(sm + SM::kCols);
   int* last = reinterpret_cast<int*>(sm + SM::kCols + ST * kTile * 4);
+  float* other = reinterpret_cast<float*>(sm + SM::kSums);
+  Note* notes = reinterpret_cast<Note*>(sm + SM::kNotes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int kt = blockIdx.x, kv = blockIdx.y, b = blockIdx.z;
-  pdl_wait();
-  pdl_launch_dependents();
-  const SeqSpan q = span_of(a, b);
-  if (!q.ok) {
-    if (tid == 0) set_status(a.status, STARKV_DEV_BAD_QUERY_SPAN);
-    return;
-  }
-  if (kt * kTile >= q.keys) return;
-  const int off = q.keys - q.n;
-  // queries first .. n - 1 count; the tile's first key is seen from query kt * 128 - off on
-  const int first = max(max(0, q.n - a.window), kt * kTile - off);
-  const int per = first < q.n ? (q.n - first + a.R - 1) / a.R : 0;  // query tiles
-  const int nt = per * a.head_blocks;
+  const int split = a.mode > 1 ? a.mode : 1;
+  const int rank = a.mode > 1 ? blockIdx.x % a.mode : 0;  // (clusters are consecutive blocks)
 
   // rows behind the box of a tile stay zero: they are columns of the products
   for (int s = 0; s < ST; ++s)
@@ -495,175 +585,359 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
           make_uint4(0, 0, 0, 0);
     }
   fence_async_smem();
-  if (warp == 9) tmem_alloc(tslot, 512);
+  if (warp == 17) tmem_alloc(tslot, 512);
   if (tid == 0) {
-    mbar_init(kfull, 1);
+    for (int s = 0; s < KS; ++s) {
+      mbar_init(&kfull[s], 1);
+      mbar_init(&kempty[s], 1);
+    }
     for (int s = 0; s < ST; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&cols[s], 2);
-      mbar_init(&empty[s], 5);
+      mbar_init(&empty[s], 9);
     }
     for (int s = 0; s < 4; ++s) {
-      mbar_init(&sfull[s], 1);
-      mbar_init(&sempty[s], 4);
+      mbar_init(&sfull[s], 2);
+      mbar_init(&sempty[s], 8);
+    }
+    for (int s = 0; s < 8; ++s) {
+      mbar_init(&sums[s], 3);
+      mbar_init(&taken[s], 1);
     }
     mbar_init(done, 1);
     fence_mbar_init();
   }
+  pdl_wait();
+  pdl_launch_dependents();
+  // ---- the CTA's items
+  int64_t pos = 0, end = 0, before = 0;
+  int seq = 0;
+  if (a.mode == kResident) {
+    // as many items of each CTA: cut the sequences' items, laid end to end
+    int64_t mine = 0;
+    for (int i = tid; i < a.batch; i += kWeightThreads) {
+      const SeqSpan q = span_of(a, i);
+      if (!q.ok && blockIdx.x == 0) set_status(a.status, STARKV_DEV_BAD_QUERY_SPAN);
+      if (q.ok) mine += (q.keys + kTile - 1) / kTile;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) part[warp] = mine;
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kWeightThreads / 32; ++w) total += part[w];
+    total *= a.h_kv;
+    pos = total * blockIdx.x / gridDim.x;
+    end = total * (blockIdx.x + 1) / gridDim.x;
+    // the sequence that holds pos, warp 0 in steps of 32 sequences
+    if (warp == 0) {
+      int64_t carry = 0;
+      for (int i0 = 0; i0 < a.batch; i0 += 32) {
+        int tiles = 0;
+        if (i0 + lane < a.batch) {
+          const SeqSpan q = span_of(a, i0 + lane);
+          if (q.ok) tiles = (q.keys + kTile - 1) / kTile;
+        }
+        int64_t inc = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += v;
+        }
+        const int64_t s0 = (carry + inc - tiles) * a.h_kv;
+        if (s0 <= pos && pos < s0 + (int64_t)tiles * a.h_kv) {
+          begin[0] = i0 + lane;
+          begin[1] = s0;
+        }
+        carry += __shfl_sync(0xffffffffu, inc, 31);
+      }
+    }
+  } else {
+    const int64_t items = (int64_t)a.ktiles * a.h_kv * a.batch;
+    end = a.mode > 1 ? 1 : (items + gridDim.x - 1) / gridDim.x;
+    if (blockIdx.x == 0)
+      for (int i = tid; i < a.batch; i += kWeightThreads)
+        if (!span_of(a, i).ok) set_status(a.status, STARKV_DEV_BAD_QUERY_SPAN);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (a.mode == kResident && pos < end) {
+    seq = (int)begin[0];
+    before = begin[1];
+  }
   const uint32_t tmem = *tslot;
+  const bool resident = a.mode == kResident;
   bool ok = true;
+  Items it(a, pos, end, seq, before);
+  // Stage and phase of step v, the u-th of this CTA.  Resident: the stage is the step's number, and
+  // `flips` holds the stages' phases (a stage turns when a (sequence, KV head) that used it is done).
+  uint32_t flips = 0;
+  auto stage_of = [&](int v, int u) { return resident ? v : u % ST; };
+  auto phase_of = [&](int v, int u) { return resident ? (flips >> v) & 1u : (uint32_t)(u / ST) & 1u; };
   float acc = 0.f;
 
-  if (warp == 8) {
+  if (warp == 16) {
     // ---------------- copies ----------------
-    if (lane == 0 && nt > 0) {
-      mbar_arrive_expect_tx(kfull, SM::kTileBytes);
-#pragma unroll
-      for (int i = 0; i < NSUB; ++i)
-        tma_load_2d(sm + i * kSub, &k_map, kv * D + i * 64, q.k0 + kt * kTile, kfull);
-      int u = 0;
-      for (; u < nt; ++u) {
-        const int s = u % ST;
-        if (!mbar_wait(&empty[s], ((u / ST) & 1) ^ 1)) {
+    if (lane == 0) {
+      int ki = 0, u = 0;  // K tiles and Q tiles so far
+      while (ok && it.next()) {
+        if (it.steps == 0) continue;
+        const int ks = ki % KS;
+        if (!mbar_wait_short(&kempty[ks], ((ki / KS) & 1) ^ 1)) {
           ok = false;
           break;
         }
-        mbar_arrive_expect_tx(&full[s], NSUB * a.R * a.gb * 128);
-        const int hb = u / per, i0 = first + (u % per) * a.R;
+        mbar_arrive_expect_tx(&kfull[ks], SM::kTileBytes);
 #pragma unroll
         for (int i = 0; i < NSUB; ++i)
-          tma_load_3d(sm + SM::kRing + s * SM::kTileBytes + i * kSub, &q_map, i * 64, kv * a.group + hb * a.gb,
-                      q.q0 + i0, &full[s]);
+          tma_load_2d(sm + ks * SM::kTileBytes + i * kSub, &k_map, it.kv * D + i * 64, it.q.k0 + it.kt * kTile,
+                      &kfull[ks]);
+        ++ki;
+        if (resident && !it.fresh) continue;
+        for (int v = rank; v < it.steps; v += split, ++u) {
+          const int s = stage_of(v, u);
+          const uint32_t ph = phase_of(v, u);
+          if (!mbar_wait_short(&empty[s], ph ^ 1)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[s], NSUB * a.R * a.gb * 128);
+          const int hb = v / it.per, i0 = it.first + (v % it.per) * a.R;
+#pragma unroll
+          for (int i = 0; i < NSUB; ++i)
+            tma_load_3d(sm + SM::kRing + s * SM::kTileBytes + i * kSub, &q_map, i * 64, it.kv * a.group + hb * a.gb,
+                        it.q.q0 + i0, &full[s]);
+        }
+        flips ^= (1u << min(it.steps, ST)) - 1;
       }
       if (!ok) {  // wait (with a limit) for the copies in flight
-        mbar_wait(kfull, 0, 100000000ull);
-        for (int i = max(0, u - ST); i < u; ++i) mbar_wait(&full[i % ST], (i / ST) & 1, 100000000ull);
+        for (int i = max(0, ki - KS); i < ki; ++i) mbar_wait(&kfull[i % KS], (i / KS) & 1, 100000000ull);
+        if (resident)
+          for (int s = 0; s < ST; ++s) mbar_wait(&full[s], ((flips >> s) & 1) ^ 1, 100000000ull);
+        else
+          for (int i = max(0, u - ST); i < u; ++i) mbar_wait(&full[i % ST], (i / ST) & 1, 100000000ull);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ---------------- products ----------------
-    if (lane == 0 && nt > 0) {
+    if (lane == 0) {
       constexpr uint32_t idesc = idesc_bf16(128, kTile, false, false);
-      const uint32_t ka = smem_u32(sm);
-      ok = mbar_wait_poll(kfull, 0);
-      for (int u = 0; ok && u < nt; ++u) {
-        const int s = u % ST, w = u & 3;
-        if (!mbar_wait_poll(&full[s], (u / ST) & 1) || !mbar_wait_poll(&sempty[w], ((u >> 2) & 1) ^ 1)) {
+      int ki = 0, u = 0;
+      auto note = [&](int w, const Note& n) {
+        notes[w] = n;
+        mbar_arrive(&sfull[w]);
+      };
+      bool more = it.next();
+      while (ok && more) {
+        const int steps = it.steps, per = it.per, first = it.first, off = it.off, n = it.q.n, keys = it.q.keys;
+        const int key0 = it.kt * kTile;
+        const int64_t row = (int64_t)it.q.k0 * a.h_kv + it.kv;
+        more = it.next();
+        if (steps == 0) continue;
+        const bool leave = !more || it.fresh;  // resident: the Q tiles' last use
+        const int ks = ki % KS;
+        ok = mbar_wait_short(&kfull[ks], (ki / KS) & 1);
+        ++ki;
+        const uint32_t ka = smem_u32(sm + ks * SM::kTileBytes);
+        int hb = rank / per, i0 = first + rank % per * a.R;  // step v's head block and first query
+        for (int v = rank; ok && v < steps; v += split, ++u) {
+          const int s = stage_of(v, u), w = u & 3;
+          const uint32_t ph = phase_of(v, u);
+          if (!mbar_wait_short(&full[s], ph) || !mbar_wait_short(&cols[s], ph) ||
+              !mbar_wait_short(&sempty[w], ((u >> 2) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t qa = smem_u32(sm + SM::kRing + s * SM::kTileBytes);
+#pragma unroll
+          for (int e = 0; e < D / 16; ++e) {
+            const uint32_t o = (e >> 2) * kSub + (e & 3) * 32;
+            mma_f16(tmem + w * kTile, make_sdesc(ka + o, 16, 1024, 2), make_sdesc(qa + o, 16, 1024, 2), idesc, e > 0);
+          }
+          mma_commit(&sfull[w]);
+          const bool free_q = !resident || leave;
+          if (free_q) mma_commit(&empty[s]);
+          // a column is masked for some key of the tile in the first tiles only
+          const bool whole = off + i0 >= key0 + kTile - 1 && (hb + 1) * a.gb <= a.group;
+          note(w, Note{(whole ? kWhole : 0) | (v + 2 * split >= steps ? kLast : 0) | (free_q ? kLeave : 0), s,
+                       min(a.R, n - i0) * a.gb, key0, keys, 0, row});
+          i0 += split * a.R;
+          while (i0 >= first + per * a.R) {
+            i0 -= per * a.R;
+            ++hb;
+          }
+        }
+        if (ok && rank < steps && rank + split >= steps) {  // one step: the other warps end the item too
+          const int w = u & 3;
+          ok = mbar_wait_short(&sempty[w], ((u >> 2) & 1) ^ 1);
+          mbar_arrive(&sfull[w]);
+          note(w, Note{kLast, 0, 0, key0, keys, 0, row});
+          ++u;
+        }
+        mma_commit(&kempty[ks]);
+        if (leave) flips ^= (1u << min(steps, ST)) - 1;
+      }
+      for (int e = 0; ok && e < 2; ++e, ++u) {  // nothing more
+        const int w = u & 3;
+        ok = mbar_wait_short(&sempty[w], ((u >> 2) & 1) ^ 1);
+        mbar_arrive(&sfull[w]);
+        note(w, Note{kStop, 0, 0, 0, 0, 0, 0});
+      }
+      mma_commit(done);
+      mbar_wait(done, 0, ok ? 2000000000ull : 100000000ull);
+    }
+  } else if (warp >= 18) {
+    // ---------------- columns (and the zeros of keys that no counting query sees) ----------------
+    int u = 0;
+    while (ok && it.next()) {
+      if (it.steps == 0) {
+        for (int r = tid - 18 * 32; r < min(kTile, it.q.keys - it.kt * kTile); r += 64)
+          a.weights[((int64_t)it.q.k0 + it.kt * kTile + r) * a.h_kv + it.kv] = 0.f;
+        continue;
+      }
+      if (resident && !it.fresh) continue;
+      for (int v = rank; v < it.steps; v += split, ++u) {
+        const int s = stage_of(v, u);
+        const uint32_t ph = phase_of(v, u);
+        const int hb = v / it.per, i0 = it.first + (v % it.per) * a.R;
+        const int heads = min(a.gb, a.group - hb * a.gb);
+        float x[2];
+        int k[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int c = (warp - 18) * 64 + e * 32 + lane;
+          const int i = i0 + c / a.gb, hh = c % a.gb;
+          const bool live = c < a.R * a.gb && i < it.q.n && hh < heads;
+          x[e] = 0.f;
+          k[e] = kColNone;
+          if (live) {
+            x[e] = a.lse_in[(int64_t)(it.q.q0 + i) * a.H + it.kv * a.group + hb * a.gb + hh] * kLog2e;
+            k[e] = it.off + i;
+          }
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait_short(&empty[s], ph ^ 1))) {
           ok = false;
           break;
         }
-        tc_fence_after();
-        const uint32_t qa = smem_u32(sm + SM::kRing + s * SM::kTileBytes);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t o = (ks >> 2) * kSub + (ks & 3) * 32;
-          mma_f16(tmem + w * kTile, make_sdesc(ka + o, 16, 1024, 2), make_sdesc(qa + o, 16, 1024, 2), idesc, ks > 0);
+        for (int e = 0; e < 2; ++e) {
+          const int c = (warp - 18) * 64 + e * 32 + lane;
+          lse2[s * kTile + c] = x[e];
+          last[s * kTile + c] = k[e];
         }
-        mma_commit(&sfull[w]);
-        mma_commit(&empty[s]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&cols[s]);
       }
-      mma_commit(done);
-      if (!ok) mbar_wait(done, 0, 100000000ull);
-    }
-  } else if (warp >= 10) {
-    // ---------------- columns ----------------
-    for (int u = 0; u < nt; ++u) {
-      const int s = u % ST;
-      const int hb = u / per, i0 = first + (u % per) * a.R;
-      const int heads = min(a.gb, a.group - hb * a.gb);
-      float x[2];
-      int k[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int c = (warp - 10) * 64 + e * 32 + lane;
-        const int i = i0 + c / a.gb, hh = c % a.gb;
-        const bool live = c < a.R * a.gb && i < q.n && hh < heads;
-        x[e] = 0.f;
-        k[e] = kColNone;
-        if (live) {
-          x[e] = a.lse_in[(int64_t)(q.q0 + i) * a.H + kv * a.group + hb * a.gb + hh] * kLog2e;
-          k[e] = off + i;
-        }
-      }
-      if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ((u / ST) & 1) ^ 1))) {
-        ok = false;
-        break;
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int c = (warp - 10) * 64 + e * 32 + lane;
-        lse2[s * kTile + c] = x[e];
-        last[s * kTile + c] = k[e];
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&cols[s]);
+      flips ^= (1u << min(it.steps, ST)) - 1;
     }
   } else {
     // ---------------- sums: one key per thread ----------------
-    const int g = warp >> 2;
-    const int key = kt * kTile + (warp & 3) * 32 + lane;
-    const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    for (int u = g; u < nt; u += 2) {
-      const int s = u % ST, w = u & 3;
-      const bool got = mbar_wait_poll(&sfull[w], (u >> 2) & 1) && mbar_wait_poll(&cols[s], (u / ST) & 1);
-      if (!__all_sync(0xffffffffu, got)) {
+    const int g = warp >> 2, half = g & 1, row = (warp & 3) * 32 + lane;
+    const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 64;
+    int items = 0;
+    for (int u = g >> 1;; u += 2) {
+      const int w = u & 3;
+      if (!__all_sync(0xffffffffu, mbar_wait_short(&sfull[w], (u >> 2) & 1))) {
         ok = false;
         break;
       }
+      const Note note = notes[w];
+      if (note.flags & kStop) break;
       tc_fence_after();
-      // a column is masked for some key of the tile, or none of a query, in the first and the last tiles only
-      const int i0 = first + (u % per) * a.R;
-      const bool whole = off + i0 >= kt * kTile + kTile - 1 && i0 + a.R <= q.n && a.group % a.gb == 0;
-      const float* x = lse2 + s * kTile;
-      const int* k = last + s * kTile;
+      const int s = note.stage, key = note.key0 + row;
+      const int live = note.live - half * 64;  // of the warp's columns
+      const float* x = lse2 + s * kTile + half * 64;
+      const int* k = last + s * kTile + half * 64;
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-      for (int c = 0; c < kTile; c += 32) {
-        uint32_t v[32];
-        tmem_ld32(trow + w * kTile + c, v);
+      if ((note.flags & kWhole) && live >= 64) {
+        uint32_t y[64];
+        tmem_ld32(trow + w * kTile, *reinterpret_cast<uint32_t(*)[32]>(&y[0]));
+        tmem_ld32(trow + w * kTile + 32, *reinterpret_cast<uint32_t(*)[32]>(&y[32]));
         tmem_ld_wait();
-        if (whole && c + 32 <= a.R * a.gb) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sempty[w]);
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 y = *reinterpret_cast<const float4*>(x + c + e);
-            sum[0] += ex2(fmaf(__uint_as_float(v[e]), a.scale_log2, -y.x));
-            sum[1] += ex2(fmaf(__uint_as_float(v[e + 1]), a.scale_log2, -y.y));
-            sum[2] += ex2(fmaf(__uint_as_float(v[e + 2]), a.scale_log2, -y.z));
-            sum[3] += ex2(fmaf(__uint_as_float(v[e + 3]), a.scale_log2, -y.w));
-          }
-        } else {
+        for (int e = 0; e < 64; e += 4) {
+          const float4 z = *reinterpret_cast<const float4*>(x + e);
+          sum[0] += ex2(fmaf(__uint_as_float(y[e]), a.scale_log2, -z.x));
+          sum[1] += ex2(fmaf(__uint_as_float(y[e + 1]), a.scale_log2, -z.y));
+          sum[2] += ex2(fmaf(__uint_as_float(y[e + 2]), a.scale_log2, -z.z));
+          sum[3] += ex2(fmaf(__uint_as_float(y[e + 3]), a.scale_log2, -z.w));
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < 64 && c < live; c += 32) {
+          uint32_t y[32];
+          tmem_ld32(trow + w * kTile + c, y);
+          tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float p = ex2(fmaf(__uint_as_float(v[e]), a.scale_log2, -x[c + e]));
+            const float p = ex2(fmaf(__uint_as_float(y[e]), a.scale_log2, -x[c + e]));
             sum[e & 3] += key <= k[c + e] ? p : 0.f;
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sempty[w]);
       }
       acc += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sempty[w]);
-        mbar_arrive(&empty[s]);
+      if (note.flags & kLeave) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+      }
+      if (!(note.flags & kLast)) continue;
+      // the four groups' sums: warps 4..15 hand theirs over, warps 0..3 add and store
+      const int buf = items & 1, set = buf * 4 + (warp & 3);
+      const uint32_t ph = (items >> 1) & 1;
+      ++items;
+      if (g > 0) {
+        if (!__all_sync(0xffffffffu, mbar_wait_short(&taken[set], ph ^ 1))) {
+          ok = false;
+          break;
+        }
+        other[(buf * 3 + g - 1) * kTile + row] = acc;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sums[set]);
+        acc = 0.f;
+      } else {
+        if (!__all_sync(0xffffffffu, mbar_wait_short(&sums[set], ph))) {
+          ok = false;
+          break;
+        }
+        const float* o = other + buf * 3 * kTile + row;
+        acc = (acc + o[0]) + (o[kTile] + o[2 * kTile]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&taken[set]);
+        if (split == 1) {
+          if (key < note.keys) a.weights[note.row + (int64_t)key * a.h_kv] = acc;
+          acc = 0.f;
+        }
       }
     }
   }
   if (!ok && lane == 0) set_status(a.status, kDevWaitTimeout);
-  if (warp == 9 && lane == 0 && nt > 0 && ok) mbar_wait(done, 0);
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  // the odd tiles' sums join the even ones' (the columns' memory is free by now)
-  if (warp >= 4 && warp < 8) lse2[tid - 128] = acc;
-  __syncthreads();
-  if (warp < 4 && kt * kTile + tid < q.keys)
-    a.weights[((int64_t)q.k0 + kt * kTile + tid) * a.h_kv + kv] = acc + lse2[tid];
+  if (split > 1) {
+    // one item: the ranks' sums, in rank order (the columns' memory is free by now)
+    if (warp < 4) lse2[tid] = acc;
+    cluster_sync();
+    Items one(a, 0, 1, 0, 0);
+    if (rank == 0 && warp < 4 && one.next() && one.steps > 0 && one.kt * kTile + tid < one.q.keys) {
+      float sum = 0.f;
+      for (int r = 0; r < split; ++r) sum += dsmem_ld_f32(dsmem_addr(&lse2[tid], (uint32_t)r));
+      a.weights[((int64_t)one.q.k0 + one.kt * kTile + tid) * a.h_kv + one.kv] = sum;
+    }
+    cluster_sync();
+  }
 }
 
 PromptKArgs args_of(const Ctx& c, const PromptArgs& p) {
@@ -711,17 +985,31 @@ cudaError_t launch_attn_d(const CUtensorMap& qm, const CUtensorMap& km, const CU
 }
 
 template <int D>
-cudaError_t launch_weights_d(const CUtensorMap& qm, const CUtensorMap& km, const PromptKArgs& a, int ktiles,
-                             cudaStream_t s) {
+cudaError_t launch_weights_d(const CUtensorMap& qm, const CUtensorMap& km, PromptKArgs a, int sms, cudaStream_t s) {
   const size_t smem = WeightSmem<D>::kBytes;
   cudaError_t e =
       cudaFuncSetAttribute(prompt_weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_chained(prompt_weights_kernel<D>, dim3(ktiles, a.h_kv, a.batch), dim3(kWeightThreads), smem, s, 1u, qm,
-                        km, a);
+  const int64_t items = (int64_t)a.ktiles * a.h_kv * a.batch;
+  // steps of an item whose keys every counting query sees
+  const int64_t most = ((int64_t)(a.window < a.max_k ? a.window : a.max_k) + a.R - 1) / a.R * a.head_blocks;
+  a.mode = most <= WeightSmem<D>::kStages ? kResident : kStreamed;
+  unsigned grid = (unsigned)(items < sms ? items : sms), cluster = 1;
+  if (a.mode == kStreamed && items * 2 <= sms) {
+    while (cluster < 8 && items * cluster * 2 <= sms && cluster * 2 <= most) cluster *= 2;
+    if (cluster > 1) {
+      a.mode = (int)cluster;
+      grid = (unsigned)items * cluster;
+    }
+  }
+  return launch_chained(prompt_weights_kernel<D>, dim3(grid), dim3(kWeightThreads), smem, s, cluster, qm, km, a);
 }
 
 }  // namespace
+
+int64_t weights_items(const Ctx& c, int batch, int max_k_len) {
+  return ((int64_t)max_k_len + kTile - 1) / kTile * c.cfg.num_kv_heads * batch;
+}
 
 int64_t prompt_blocks(const Ctx& c, int batch, int max_q_len) {
   PromptArgs p = {};
@@ -755,8 +1043,10 @@ cudaError_t launch_prompt_weights(const Ctx& c, const PromptArgs& p, const float
   if (!map_kv(c, p.k, p.k_stride, p.total_k, &km)) return cudaErrorInvalidValue;
   qm = km;  // no queries at all: nothing is copied
   if (p.total_q > 0 && !map_q(c, p, a, &qm)) return cudaErrorInvalidValue;
-  const int ktiles = (max_k_len + kTile - 1) / kTile;
-  return c.cfg.head_dim == 64 ? launch_weights_d<64>(qm, km, a, ktiles, s) : launch_weights_d<128>(qm, km, a, ktiles, s);
+  a.ktiles = (max_k_len + kTile - 1) / kTile;
+  int sms = 148;
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c.device);
+  return c.cfg.head_dim == 64 ? launch_weights_d<64>(qm, km, a, sms, s) : launch_weights_d<128>(qm, km, a, sms, s);
 }
 
 }  // namespace starkv

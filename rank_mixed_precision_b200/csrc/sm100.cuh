@@ -90,6 +90,22 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
   return false;
 }
 
+// Wait by polling like mbar_wait_poll, but without a look at the global timer (hundreds of
+// cycles) before a thousand polls have failed: for waits that are mostly short.
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, uint64_t limit_ns = 2000000000ull) {
+  if (mbar_test(bar, parity)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; i < (1u << 30); ++i) {
+    if (mbar_test(bar, parity)) return true;
+    if ((i & 1023) == 0) {
+      const uint64_t now = global_ns();
+      if (t0 == 0) t0 = now;
+      else if (now - t0 > limit_ns) return false;
+    }
+  }
+  return false;
+}
+
 // ---------------------------------------------------------------------------
 // Bulk copies (global -> shared), completion counted on an mbarrier
 // ---------------------------------------------------------------------------

@@ -299,3 +299,41 @@ def test_from_a_prompt_in_two_chunks_to_decode_behind_an_eviction(shape):
         before = sum(wc[src[stay[i]] // 16, i, src[stay[i]] % 16].sum() for i in range(h))
         assert abs(got[s // 16, :, s % 16].sum() - before - steps * H) < 1e-3 * steps * H
     assert kv.status() == 0
+
+
+@pytest.mark.parametrize("shape,n_q,n_k,window", [
+    ((8, 2, 64), [3, 70, 0, 200], [900, 70, 300, 1500], 20),      # a window whose queries stay: sequences with fewer of them
+    ((8, 2, 128), [64, 1, 130], [1300, 700, 130], 64),
+    ((16, 4, 64), [3000], [3000], 3000),                          # many steps an item, few items
+    ((4, 4, 64), [700] * 12, [700] * 12, 700),                    # more items than SMs
+    ((16, 1, 128), [300, 500], [300, 500], 100),
+    ((150, 1, 64), [60], [200], 10),                              # two blocks of heads
+    ((8, 2, 64), [900, 40], [100, 40], 900),                      # most queries see nothing
+])
+def test_weights_of_every_way_to_share_the_work(shape, n_q, n_k, window):
+    """The kernel's weights against the formula in 64 bits, from the kernel's own lse."""
+    H, h, d = shape
+    rng = np.random.default_rng(window)
+    kv = context(*shape)
+    q, k, v = inputs(rng, shape, n_q, n_k)
+    cq, ck = i32(cu_of(n_q)), i32(cu_of(n_k))
+    lse = kv.prompt(q, k, v, cq, ck, max(n_q))[1]
+    w = torch.full((sum(n_k), h), 7.0, device="cuda")
+    for _ in range(2):
+        skv().starkv_prompt_weights(kv.ctx, kv.cfg, q, k, lse, cq, ck, max(n_k), window, w)
+        assert kv.status() == 0
+        for b, (n, m) in enumerate(zip(n_q, n_k)):
+            q0, k0 = sum(n_q[:b]), sum(n_k[:b])
+            first = max(0, n - window)
+            for head in range(h):
+                Q = q[q0 + first:q0 + n, head * (H // h):(head + 1) * (H // h)].double()
+                K = k[k0:k0 + m, head].double()
+                z = torch.einsum("igd,jd->igj", Q, K) / d**0.5
+                e = torch.einsum("igd,jd->igj", Q.abs(), K.abs()).amax() * 2.0**-20 / d**0.5 if z.numel() else 0
+                seen = torch.arange(m, device="cuda")[None] <= (m - n + first + torch.arange(n - first, device="cuda"))[:, None]
+                p = torch.exp(z - lse[q0 + first:q0 + n, head * (H // h):(head + 1) * (H // h), None].double())
+                want = torch.where(seen[:, None], p, 0.0).sum((0, 1))
+                # the score's error, ex2's and the difference's (lse < 2^5: 2^-18), and fp32 sums of fewer than 2^10 chunks
+                tol = want * (e + 2.0**-17 + 2.0**-14) + 2.0**-24
+                got = w[k0:k0 + m, head].double()
+                assert ((got - want).abs() <= tol).all(), (b, head, (got - want).abs().max())
