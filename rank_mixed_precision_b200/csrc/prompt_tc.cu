@@ -27,6 +27,65 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Pairs of fp32 in one 64-bit register: one instruction works on both.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(f32x2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// 2^x for x <= 126 on the FMA pipe, for a part of the exponentials (the special function unit
+// takes 16 a cycle and SM, half as long again as the products of the same tile): x = n + f with
+// n = rint(x), 2^f by the polynomial of degree 5 of least relative error on [-1/2, 1/2] (Remez
+// exchange; 7.5e-8, in fp32 2.2e-7, as much as ex2.approx is off), 2^n from the bits of the sum
+// that rounds x.  Below -125 it stays at 2^-125; NaN passes through.
+__device__ __forceinline__ f32x2 ex2_fma(f32x2 x) {
+  float2 y = unpair(x);
+  x = pair(max_nan(y.x, -125.f), max_nan(y.y, -125.f));
+  const float kRound = 12582912.f + 127.f;  // 1.5 2^23, and the bias of an exponent
+  const f32x2 r = add2(x, pair(kRound, kRound));
+  const f32x2 f = add2(x, mul2(add2(r, pair(-kRound, -kRound)), pair(-1.f, -1.f)));
+  f32x2 p = fma2(f, pair(0.001327647245f, 0.001327647245f), pair(0.009675540961f, 0.009675540961f));
+  p = fma2(p, f, pair(0.05550713092f, 0.05550713092f));
+  p = fma2(p, f, pair(0.2402212024f, 0.2402212024f));
+  p = fma2(p, f, pair(0.693146944f, 0.693146944f));
+  p = fma2(p, f, pair(1.000000119f, 1.000000119f));
+  y = unpair(r);
+  return mul2(p, pair(__uint_as_float(__float_as_uint(y.x) << 23), __uint_as_float(__float_as_uint(y.y) << 23)));
+}
+
+// 2^x of a pair on the special function unit.
+__device__ __forceinline__ f32x2 ex2_sfu(f32x2 x) {
+  const float2 y = unpair(x);
+  return pair(ex2(y.x), ex2(y.y));
+}
+
 __device__ __forceinline__ uint32_t pack_bf2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -37,6 +96,14 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool 
   return make_idesc_f16(M, N, a_mn, b_mn) | (1u << 7) | (1u << 10);
 }
 
+// The products are issued by a whole warp that stays together, behind elect.sync: the
+// compiler then keeps descriptors in uniform registers.  (128 x 128 x 128 of products takes 512
+// cycles; issued by a branch on the lane it took 690, from a loop that was not unrolled 1240.)
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
 // D[tmem] (+)= A[tmem] * B[smem]; issued by one thread.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                            uint32_t accumulate) {
@@ -46,6 +113,8 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// A descriptor's start address moved by `bytes` (it stays within the field: shared memory is smaller).
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
 
 // 3-D tiled TMA load (no multicast).
 __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
@@ -216,55 +285,78 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
   } else if (warp == 9) {
     // ---------------- products ----------------
-    if (lane == 0 && nt > 0) {
+    if (nt > 0) {
       constexpr uint32_t idesc_s = idesc_bf16(128, kTile, false, false);
       constexpr uint32_t idesc_o = idesc_bf16(128, D, false, true);
-      const uint32_t ring = smem_u32(sm + SM::kRing), qa = smem_u32(sm);
-      auto issue_s = [&](int t, int j) {
-        const uint32_t ka = ring + (2 * j % ST) * SM::kTileBytes;
+      const bool lead = elected();
+      const uint64_t qd = make_sdesc(smem_u32(sm), 16, 1024, 2);
+      const uint64_t kd = make_sdesc(smem_u32(sm + SM::kRing), 16, 1024, 2);
+      const uint64_t vd = make_sdesc(smem_u32(sm + SM::kRing), kSub, 1024, 2);
+      auto issue_s = [&](int t, int stage) {
+        const uint64_t q0 = desc_at(qd, t * SM::kTileBytes), k0 = desc_at(kd, stage * SM::kTileBytes);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t o = (ks >> 2) * kSub + (ks & 3) * 32;
-          mma_f16(tmem + t * kTile, make_sdesc(qa + t * SM::kTileBytes + o, 16, 1024, 2),
-                  make_sdesc(ka + o, 16, 1024, 2), idesc_s, ks > 0);
+          mma_f16(tmem + t * kTile, desc_at(q0, o), desc_at(k0, o), idesc_s, ks > 0);
         }
         mma_commit(&sfull[t]);
       };
-      auto wait_full = [&](int i) { return mbar_wait_short(&full[i % ST], (i / ST) & 1); };
-      ok = mbar_wait_short(qfull, 0) && wait_full(0);
+      auto all = [&](bool got) { return __all_sync(0xffffffffu, got) != 0; };
+      // the ring's positions: K_j at kst, V_j at vst, each with its phase
+      int kst = 0, vst = 1;
+      uint32_t kph = 0, vph = 0;
+      auto on = [&](int& st, uint32_t& ph) {
+        st += 2;
+        if (st >= ST) {
+          st -= ST;
+          ph ^= 1;
+        }
+      };
+      ok = all(mbar_wait_short(qfull, 0) && mbar_wait_short(&full[0], 0));
       if (ok) {
         tc_fence_after();
-        if (ntile[0] > 0) issue_s(0, 0);
-        if (ntile[1] > 0) issue_s(1, 0);
-        mma_commit(&empty[0]);
-      }
-      int looked = 0;
-      for (int j = 0; ok && j < nt; ++j) {
-        ok = wait_full(2 * j + 1);
-        if (ok && j >= first_masked) {
-          mbar_arrive(look);
-          ok = mbar_wait_short(clean, looked++ & 1);
+        if (lead) {
+          if (ntile[0] > 0) issue_s(0, 0);
+          if (ntile[1] > 0) issue_s(1, 0);
+          mma_commit(&empty[0]);
         }
-        if (ok && j + 1 < nt) ok = wait_full(2 * j + 2);
+        __syncwarp();
+      }
+      uint32_t looked = 0;
+      for (int j = 0; ok && j < nt; ++j) {
+        on(kst, kph);
+        bool got = mbar_wait_short(&full[vst], vph);
+        if (got && j >= first_masked) {
+          if (lane == 0) mbar_arrive(look);
+          got = mbar_wait_short(clean, looked);
+          looked ^= 1;
+        }
+        if (got && j + 1 < nt) got = mbar_wait_short(&full[kst], kph);
+        ok = all(got);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (!ok || j >= ntile[t]) continue;
-          if (!mbar_wait_short(&pfull[t], j & 1)) {
+          if (!all(mbar_wait_short(&pfull[t], j & 1))) {
             ok = false;
             continue;
           }
           tc_fence_after();
-          const uint32_t va = ring + ((2 * j + 1) % ST) * SM::kTileBytes;
+          if (lead) {
+            const uint64_t v0 = desc_at(vd, vst * SM::kTileBytes);
 #pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks)
-            mma_f16_ts(tmem + 256 + t * kTile, tmem + t * kTile + ks * 8, make_sdesc(va + ks * 2048, kSub, 1024, 2),
-                       idesc_o, (j > 0 || ks > 0) ? 1u : 0u);
-          if (t == 1 || j >= ntile[1]) mma_commit(&empty[(2 * j + 1) % ST]);
-          if (j + 1 < ntile[t]) issue_s(t, j + 1);
+            for (int ks = 0; ks < kTile / 16; ++ks)
+              mma_f16_ts(tmem + 256 + t * kTile, tmem + t * kTile + ks * 8, desc_at(v0, ks * 2048), idesc_o,
+                         j > 0 || ks > 0);
+            if (t == 1 || j >= ntile[1]) mma_commit(&empty[vst]);
+            if (j + 1 < ntile[t]) issue_s(t, kst);
+          }
+          __syncwarp();
         }
-        if (ok && j + 1 < nt) mma_commit(&empty[(2 * j + 2) % ST]);
+        if (ok && j + 1 < nt && lead) mma_commit(&empty[kst]);
+        on(vst, vph);
       }
-      mma_commit(odone);  // completes once every product issued above has
+      if (lead) mma_commit(odone);  // completes once every product issued above has
+      __syncwarp();
       if (!ok) mbar_wait(odone, 0, 100000000ull);
     }
   } else if (warp >= 10) {
@@ -448,6 +540,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 //   split     where there are few items, a cluster shares one item's steps out and adds the
 //             sums through distributed shared memory, in rank order.
 constexpr int kWeightThreads = 640;
+#ifndef FMA_EVERY
+#define FMA_EVERY 100
+#endif
+constexpr int kFmaEvery = FMA_EVERY;  // of 4 columns, two go to the FMA pipe in every kFmaEvery-th turn
 constexpr int kColNone = -(1 << 30);  // a column that sees no key
 enum { kResident = 0, kStreamed = 1 };  // > 1: split over so many CTAs
 
@@ -457,7 +553,7 @@ struct WeightSmem {
   static constexpr int kStages = D == 128 ? 3 : 6;   // Q tiles
   static constexpr int kKeys = D == 128 ? 3 : 4;     // K tiles
   static constexpr uint32_t kRing = kKeys * kTileBytes;
-  static constexpr uint32_t kCols = kRing + kStages * kTileBytes;  // [stage][128] lse in log2 units, [stage][128] last key
+  static constexpr uint32_t kCols = kRing + kStages * kTileBytes;  // [stage][128] -lse in log2 units, [stage][128] last key
   static constexpr uint32_t kSums = kCols + kStages * kTile * 8;   // [2][3][128] sums of warps 4 .. 15
   static constexpr uint32_t kNotes = kSums + 2 * 3 * kTile * 4;    // [4] what a product's sums go by
   static constexpr uint32_t kBar = kNotes + 4 * 32;
@@ -561,9 +657,8 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   uint64_t* kfull = bar;           // [KS]
   uint64_t* kempty = kfull + KS;   // [KS]
   uint64_t* full = kempty + KS;    // [ST] Q tile landed
-  uint64_t* cols = full + ST;      // [ST] its columns laid out (2 warps)
-  uint64_t* empty = cols + ST;     // [ST] Q tile read by its products, its columns by 8 warps
-  uint64_t* sfull = empty + ST;    // [4] a product and its note are there,
+  uint64_t* empty = full + ST;     // [ST] Q tile read by its products, its columns by 8 warps
+  uint64_t* sfull = empty + ST;    // [4] a product, its columns (2 warps) and its note are there,
   uint64_t* sempty = sfull + 4;    // [4] and have been read
   uint64_t* sums = sempty + 4;     // [2][4] three warps' sums are there
   uint64_t* taken = sums + 8;      // [2][4] and have been added
@@ -593,11 +688,10 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     }
     for (int s = 0; s < ST; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&cols[s], 2);
       mbar_init(&empty[s], 9);
     }
     for (int s = 0; s < 4; ++s) {
-      mbar_init(&sfull[s], 2);
+      mbar_init(&sfull[s], 3);
       mbar_init(&sempty[s], 8);
     }
     for (int s = 0; s < 8; ++s) {
@@ -722,117 +816,159 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     }
   } else if (warp == 17) {
     // ---------------- products ----------------
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16(128, kTile, false, false);
-      int ki = 0, u = 0;
-      auto note = [&](int w, const Note& n) {
-        notes[w] = n;
-        mbar_arrive(&sfull[w]);
-      };
-      bool more = it.next();
-      while (ok && more) {
-        const int steps = it.steps, per = it.per, first = it.first, off = it.off, n = it.q.n, keys = it.q.keys;
-        const int key0 = it.kt * kTile;
-        const int64_t row = (int64_t)it.q.k0 * a.h_kv + it.kv;
-        more = it.next();
-        if (steps == 0) continue;
-        const bool leave = !more || it.fresh;  // resident: the Q tiles' last use
-        const int ks = ki % KS;
-        ok = mbar_wait_short(&kfull[ks], (ki / KS) & 1);
-        ++ki;
-        const uint32_t ka = smem_u32(sm + ks * SM::kTileBytes);
-        int hb = rank / per, i0 = first + rank % per * a.R;  // step v's head block and first query
-        for (int v = rank; ok && v < steps; v += split, ++u) {
-          const int s = stage_of(v, u), w = u & 3;
-          const uint32_t ph = phase_of(v, u);
-          if (!mbar_wait_short(&full[s], ph) || !mbar_wait_short(&cols[s], ph) ||
-              !mbar_wait_short(&sempty[w], ((u >> 2) & 1) ^ 1)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t qa = smem_u32(sm + SM::kRing + s * SM::kTileBytes);
+    constexpr uint32_t idesc = idesc_bf16(128, kTile, false, false);
+    const bool lead = elected();
+    const uint64_t kd = make_sdesc(smem_u32(sm), 16, 1024, 2), qd = make_sdesc(smem_u32(sm + SM::kRing), 16, 1024, 2);
+    int u = 0, ks = 0, st = 0;  // steps so far, the K ring's next tile, the Q ring's (streamed)
+    uint32_t kph = 0, sph = 0;
+    bool more = it.next();
+    while (ok && more) {
+      const int steps = it.steps;
+      more = it.next();
+      if (steps == 0) continue;
+      const bool free_q = !resident || !more || it.fresh;  // resident: the Q tiles' last use
+      ok = __all_sync(0xffffffffu, mbar_wait_short(&kfull[ks], kph));
+      const uint64_t k0 = desc_at(kd, ks * SM::kTileBytes);
+      int v = rank;
+      for (; ok && v < steps; v += split, ++u) {
+        const int s = resident ? v : st, w = u & 3;
+        const uint32_t ph = resident ? (flips >> v) & 1u : sph;
+        ok = __all_sync(0xffffffffu, mbar_wait_short(&full[s], ph) && mbar_wait_short(&sempty[w], ((u >> 2) & 1) ^ 1));
+        if (!ok) break;
+        tc_fence_after();
+        if (lead) {
+          const uint64_t q0 = desc_at(qd, s * SM::kTileBytes);
 #pragma unroll
           for (int e = 0; e < D / 16; ++e) {
             const uint32_t o = (e >> 2) * kSub + (e & 3) * 32;
-            mma_f16(tmem + w * kTile, make_sdesc(ka + o, 16, 1024, 2), make_sdesc(qa + o, 16, 1024, 2), idesc, e > 0);
+            mma_f16(tmem + w * kTile, desc_at(k0, o), desc_at(q0, o), idesc, e > 0);
           }
           mma_commit(&sfull[w]);
-          const bool free_q = !resident || leave;
           if (free_q) mma_commit(&empty[s]);
-          // a column is masked for some key of the tile in the first tiles only
-          const bool whole = off + i0 >= key0 + kTile - 1 && (hb + 1) * a.gb <= a.group;
-          note(w, Note{(whole ? kWhole : 0) | (v + 2 * split >= steps ? kLast : 0) | (free_q ? kLeave : 0), s,
-                       min(a.R, n - i0) * a.gb, key0, keys, 0, row});
-          i0 += split * a.R;
-          while (i0 >= first + per * a.R) {
-            i0 -= per * a.R;
-            ++hb;
-          }
         }
-        if (ok && rank < steps && rank + split >= steps) {  // one step: the other warps end the item too
-          const int w = u & 3;
-          ok = mbar_wait_short(&sempty[w], ((u >> 2) & 1) ^ 1);
-          mbar_arrive(&sfull[w]);
-          note(w, Note{kLast, 0, 0, key0, keys, 0, row});
-          ++u;
+        __syncwarp();
+        if (++st == ST) {
+          st = 0;
+          sph ^= 1;
         }
-        mma_commit(&kempty[ks]);
-        if (leave) flips ^= (1u << min(steps, ST)) - 1;
       }
-      for (int e = 0; ok && e < 2; ++e, ++u) {  // nothing more
+      if (ok && v == rank + split) {  // one step: a note without a product ends the item for the other warps
         const int w = u & 3;
-        ok = mbar_wait_short(&sempty[w], ((u >> 2) & 1) ^ 1);
-        mbar_arrive(&sfull[w]);
-        note(w, Note{kStop, 0, 0, 0, 0, 0, 0});
+        ok = __all_sync(0xffffffffu, mbar_wait_short(&sempty[w], ((u >> 2) & 1) ^ 1));
+        if (lane == 0) mbar_arrive(&sfull[w]);
+        ++u;
       }
-      mma_commit(done);
-      mbar_wait(done, 0, ok ? 2000000000ull : 100000000ull);
+      if (lead) mma_commit(&kempty[ks]);
+      __syncwarp();
+      if (++ks == KS) {
+        ks = 0;
+        kph ^= 1;
+      }
+      if (!resident || free_q) flips ^= (1u << min(steps, ST)) - 1;
     }
+    for (int e = 0; ok && e < 2; ++e, ++u) {  // nothing more: two notes without products
+      const int w = u & 3;
+      ok = __all_sync(0xffffffffu, mbar_wait_short(&sempty[w], ((u >> 2) & 1) ^ 1));
+      if (lane == 0) mbar_arrive(&sfull[w]);
+    }
+    if (lead) mma_commit(done);
+    __syncwarp();
+    mbar_wait(done, 0, ok ? 2000000000ull : 100000000ull);
   } else if (warp >= 18) {
-    // ---------------- columns (and the zeros of keys that no counting query sees) ----------------
-    int u = 0;
-    while (ok && it.next()) {
-      if (it.steps == 0) {
-        for (int r = tid - 18 * 32; r < min(kTile, it.q.keys - it.kt * kTile); r += 64)
-          a.weights[((int64_t)it.q.k0 + it.kt * kTile + r) * a.h_kv + it.kv] = 0.f;
+    // ---------------- columns and notes (and the zeros of keys that no counting query sees) ----------------
+    int u = 0, st = 0;
+    uint32_t sph = 0;
+    int col_r[2], col_h[2];  // the lane's columns: query within the tile, head within the block
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int c = (warp - 18) * 64 + e * 32 + lane;
+      col_r[e] = c / a.gb;
+      col_h[e] = c % a.gb;
+    }
+    auto note = [&](const Note& n) {  // for the u-th product, whose buffer must be free
+      const int w = u & 3;
+      if (!__all_sync(0xffffffffu, mbar_wait_short(&sempty[w], ((u >> 2) & 1) ^ 1))) return false;
+      if (lane == 0) {
+        if (warp == 18) notes[w] = n;
+        mbar_arrive(&sfull[w]);
+      }
+      ++u;
+      return true;
+    };
+    bool more = it.next();
+    while (ok && more) {
+      const int steps = it.steps, per = it.per, first = it.first, off = it.off, n = it.q.n, keys = it.q.keys, kv = it.kv;
+      const int q0 = it.q.q0, key0 = it.kt * kTile;
+      const int64_t row = (int64_t)it.q.k0 * a.h_kv + kv;
+      const bool fresh = it.fresh;
+      more = it.next();
+      if (steps == 0) {
+        for (int r = key0 + tid - 18 * 32; r < min(key0 + kTile, keys); r += 64) a.weights[row + (int64_t)r * a.h_kv] = 0.f;
         continue;
       }
-      if (resident && !it.fresh) continue;
-      for (int v = rank; v < it.steps; v += split, ++u) {
-        const int s = stage_of(v, u);
-        const uint32_t ph = phase_of(v, u);
-        const int hb = v / it.per, i0 = it.first + (v % it.per) * a.R;
-        const int heads = min(a.gb, a.group - hb * a.gb);
-        float x[2];
-        int k[2];
+      const bool lay = !resident || fresh, leave = !resident || !more || it.fresh;
+      // the next step's log-sum-exps are asked for before this step's stage is free
+      float x[2], next_x[2];
+      int k[2], next_k[2];
+      int hb = rank / per, i0 = first + rank % per * a.R;  // the step's head block and first query
+      auto fetch = [&](int v, int hb, int i0) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int c = (warp - 18) * 64 + e * 32 + lane;
-          const int i = i0 + c / a.gb, hh = c % a.gb;
-          const bool live = c < a.R * a.gb && i < it.q.n && hh < heads;
-          x[e] = 0.f;
-          k[e] = kColNone;
+          const int i = i0 + col_r[e], h = hb * a.gb + col_h[e];
+          const bool live = v < steps && col_r[e] < a.R && i < n && h < a.group;
+          next_x[e] = 0.f;
+          next_k[e] = kColNone;
           if (live) {
-            x[e] = a.lse_in[(int64_t)(it.q.q0 + i) * a.H + it.kv * a.group + hb * a.gb + hh] * kLog2e;
-            k[e] = it.off + i;
+            next_x[e] = a.lse_in[(int64_t)(q0 + i) * a.H + kv * a.group + h];
+            next_k[e] = off + i;
           }
         }
-        if (!__all_sync(0xffffffffu, mbar_wait_short(&empty[s], ph ^ 1))) {
+      };
+      if (lay) fetch(rank, hb, i0);
+      for (int v = rank; v < steps; v += split) {
+        const int s = resident ? v : st;
+        const uint32_t ph = resident ? (flips >> v) & 1u : sph;
+        if (++st == ST) {
+          st = 0;
+          sph ^= 1;
+        }
+        // a column is masked for some key of the tile in the first tiles only
+        const bool whole = off + i0 >= key0 + kTile - 1 && (hb + 1) * a.gb <= a.group;
+        const Note told{(whole ? kWhole : 0) | (v + 2 * split >= steps ? kLast : 0) | (leave ? kLeave : 0), s,
+                        min(a.R, n - i0) * a.gb, key0, keys, 0, row};
+        i0 += split * a.R;
+        while (i0 >= first + per * a.R) {
+          i0 -= per * a.R;
+          ++hb;
+        }
+        if (lay) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            x[e] = next_x[e];
+            k[e] = next_k[e];
+          }
+          fetch(v + split, hb, i0);
+          if (!__all_sync(0xffffffffu, mbar_wait_short(&empty[s], ph ^ 1))) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int c = (warp - 18) * 64 + e * 32 + lane;
+            lse2[s * kTile + c] = x[e] * -kLog2e;
+            last[s * kTile + c] = k[e];
+          }
+          __syncwarp();
+        }
+        if (!note(told)) {
           ok = false;
           break;
         }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int c = (warp - 18) * 64 + e * 32 + lane;
-          lse2[s * kTile + c] = x[e];
-          last[s * kTile + c] = k[e];
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&cols[s]);
       }
-      flips ^= (1u << min(it.steps, ST)) - 1;
+      if (ok && rank < steps && rank + split >= steps) ok = note(Note{kLast, 0, 0, key0, keys, 0, row});
+      if (lay) flips ^= (1u << min(steps, ST)) - 1;
     }
+    for (int e = 0; ok && e < 2; ++e) ok = note(Note{kStop, 0, 0, 0, 0, 0, 0});
   } else {
     // ---------------- sums: one key per thread ----------------
     const int g = warp >> 2, half = g & 1, row = (warp & 3) * 32 + lane;
@@ -860,14 +996,18 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sempty[w]);
+        f32x2 two[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+        const f32x2 scale = pair(a.scale_log2, a.scale_log2);
 #pragma unroll
         for (int e = 0; e < 64; e += 4) {
           const float4 z = *reinterpret_cast<const float4*>(x + e);
-          sum[0] += ex2(fmaf(__uint_as_float(y[e]), a.scale_log2, -z.x));
-          sum[1] += ex2(fmaf(__uint_as_float(y[e + 1]), a.scale_log2, -z.y));
-          sum[2] += ex2(fmaf(__uint_as_float(y[e + 2]), a.scale_log2, -z.z));
-          sum[3] += ex2(fmaf(__uint_as_float(y[e + 3]), a.scale_log2, -z.w));
+          const f32x2 t0 = fma2(pair(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), scale, pair(z.x, z.y));
+          const f32x2 t1 = fma2(pair(__uint_as_float(y[e + 2]), __uint_as_float(y[e + 3])), scale, pair(z.z, z.w));
+          two[0] = add2(two[0], ex2_sfu(t0));
+          two[1] = add2(two[1], e % (4 * kFmaEvery) == 0 ? ex2_fma(t1) : ex2_sfu(t1));
         }
+        const float2 a0 = unpair(two[0]), a1 = unpair(two[1]);
+        sum[0] = a0.x, sum[1] = a0.y, sum[2] = a1.x, sum[3] = a1.y;
       } else {
 #pragma unroll 1
         for (int c = 0; c < 64 && c < live; c += 32) {
@@ -876,7 +1016,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
           tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float p = ex2(fmaf(__uint_as_float(y[e]), a.scale_log2, -x[c + e]));
+            const float p = ex2(fmaf(__uint_as_float(y[e]), a.scale_log2, x[c + e]));
             sum[e & 3] += key <= k[c + e] ? p : 0.f;
           }
         }
