@@ -54,6 +54,11 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -64,10 +69,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // takes 16 a cycle and SM, half as long again as the products of the same tile): x = n + f with
 // n = rint(x), 2^f by the polynomial of degree 5 of least relative error on [-1/2, 1/2] (Remez
 // exchange; 7.5e-8, in fp32 2.2e-7, as much as ex2.approx is off), 2^n from the bits of the sum
-// that rounds x.  Below -125 it stays at 2^-125; NaN passes through.
+// that rounds x.  Below -126.5 the bits of 2^n are those of
+// 0; NaN passes through.
 __device__ __forceinline__ f32x2 ex2_fma(f32x2 x) {
   float2 y = unpair(x);
-  x = pair(max_nan(y.x, -125.f), max_nan(y.y, -125.f));
+  x = pair(max_nan(y.x, -127.f), max_nan(y.y, -127.f));
   const float kRound = 12582912.f + 127.f;  // 1.5 2^23, and the bias of an exponent
   const f32x2 r = add2(x, pair(kRound, kRound));
   const f32x2 f = add2(x, mul2(add2(r, pair(-kRound, -kRound)), pair(-1.f, -1.f)));
@@ -174,6 +180,9 @@ __device__ __forceinline__ SeqSpan span_of(const PromptKArgs& a, int b) {
 //   than 2^8 only, and then the row's O is rescaled in place; S_t (j) complete implies
 //   that P_t V_(j-1) is, so no further barrier guards that.
 constexpr int kAttnThreads = 384;
+#ifndef FMA_PAIR
+#define FMA_PAIR(u) ((u) % 8 == 7)
+#endif
 
 template <int D>
 struct AttnSmem {
@@ -196,11 +205,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + SM::kBar);
   uint64_t* qfull = bar;              // both Q tiles landed
   uint64_t* sfull = bar + 1;          // [2] S_t ready
-  uint64_t* pfull = bar + 3;          // [2] P_t written
-  uint64_t* look = bar + 5;           // one phase per masked V tile: it is there,
-  uint64_t* clean = bar + 6;          // and it has been looked over
-  uint64_t* odone = bar + 7;          // every product done
-  uint64_t* full = bar + 8;           // [ST]
+  uint64_t* pfull = bar + 3;          // [2][2] P_t written: its first 64 keys, the others
+  uint64_t* look = bar + 7;           // one phase per masked V tile: it is there,
+  uint64_t* clean = bar + 8;          // and it has been looked over
+  uint64_t* odone = bar + 9;          // every product done
+  uint64_t* full = bar + 10;          // [ST]
   uint64_t* empty = full + ST;        // [ST]
   uint32_t* tslot = reinterpret_cast<uint32_t*>(empty + ST);
   int* dirty = reinterpret_cast<int*>(tslot + 1);  // a masked V tile held a value that is not finite
@@ -238,8 +247,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     mbar_init(qfull, 1);
     mbar_init(&sfull[0], 1);
     mbar_init(&sfull[1], 1);
-    mbar_init(&pfull[0], 4);
-    mbar_init(&pfull[1], 4);
+    for (int s = 0; s < 4; ++s) mbar_init(&pfull[s], 4);
     mbar_init(look, 1);
     mbar_init(clean, 2);
     mbar_init(odone, 1);
@@ -336,17 +344,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (!ok || j >= ntile[t]) continue;
-          if (!all(mbar_wait_short(&pfull[t], j & 1))) {
-            ok = false;
-            continue;
-          }
-          tc_fence_after();
-          if (lead) {
-            const uint64_t v0 = desc_at(vd, vst * SM::kTileBytes);
+          const uint64_t v0 = desc_at(vd, vst * SM::kTileBytes);
 #pragma unroll
-            for (int ks = 0; ks < kTile / 16; ++ks)
-              mma_f16_ts(tmem + 256 + t * kTile, tmem + t * kTile + ks * 8, desc_at(v0, ks * 2048), idesc_o,
-                         j > 0 || ks > 0);
+          for (int h = 0; h < 2; ++h) {
+            if (!all(ok && mbar_wait_short(&pfull[t * 2 + h], j & 1))) {
+              ok = false;
+              continue;
+            }
+            tc_fence_after();
+            if (lead) {
+#pragma unroll
+              for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+                mma_f16_ts(tmem + 256 + t * kTile, tmem + t * kTile + ks * 8, desc_at(v0, ks * 2048), idesc_o,
+                           j > 0 || ks > 0);
+            }
+            __syncwarp();
+          }
+          if (!ok) continue;
+          if (lead) {
             if (t == 1 || j >= ntile[1]) mma_commit(&empty[vst]);
             if (j + 1 < ntile[t]) issue_s(t, kst);
           }
@@ -431,47 +446,57 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
-      for (int c = 4; c < kTile; c += 4)
+      for (int c = 4; c < kTile - 4; c += 8)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], sv[c + u]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], sv[c + u], sv[c + 4 + u]);
+      const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], sv[kTile - 4], sv[kTile - 3]),
+                             fmaxf(sv[kTile - 2], sv[kTile - 1]));
       const bool move = live && (top - m) * a.scale_log2 > kMoveMax;  // m = -inf: true but for a row without scores
       if (__any_sync(0xffffffffu, move)) {
         if (j > 0) {
           const float f = move ? ex2((m - top) * a.scale_log2) : 1.f;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(to + c * 32, o);
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(to + c * 16, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
-            tmem_st32(to + c * 32, o);
+            for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+            tmem_st16(to + c * 16, o);
           }
           l *= f;
         }
         if (move) m = top;
       }
-      const float base = m == -INFINITY ? 0.f : m * a.scale_log2;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const float base = m == -INFINITY ? 0.f : -m * a.scale_log2;
+      const f32x2 scale2 = pair(a.scale_log2, a.scale_log2), base2 = pair(base, base);
+      f32x2 sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+      // four quarters; the first half of P goes on its way while the third quarter is computed
 #pragma unroll
-      for (int c = 0; c < kTile / 64; ++c) {
-        uint32_t w[32];
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[16];
 #pragma unroll
-        for (int u = 0; u < 32; ++u) {
-          const float p0 = ex2(fmaf(sv[c * 64 + 2 * u], a.scale_log2, -base));
-          const float p1 = ex2(fmaf(sv[c * 64 + 2 * u + 1], a.scale_log2, -base));
-          sum[(2 * u) & 3] += p0;
-          sum[(2 * u + 1) & 3] += p1;
-          w[u] = pack_bf2(p0, p1);
+        for (int u = 0; u < 16; ++u) {
+          const f32x2 x = fma2(pair(sv[c * 32 + 2 * u], sv[c * 32 + 2 * u + 1]), scale2, base2);
+          const f32x2 p = FMA_PAIR(u) ? ex2_fma(x) : ex2_sfu(x);
+          sum[u & 1] = add2(sum[u & 1], p);
+          const float2 y = unpair(p);
+          w[u] = pack_bf2(y.x, y.y);
         }
-        tmem_st32(ts + c * 32, w);
+        if (c == 2) {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&pfull[t * 2]);
+        }
+        tmem_st16(ts + c * 16, w);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      const float2 s0 = unpair(sum[0]), s1 = unpair(sum[1]);
+      l += (s0.x + s0.y) + (s1.x + s1.y);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&pfull[t]);
+      if (lane == 0) mbar_arrive(&pfull[t * 2 + 1]);
     }
     // ---- O / l, and lse
     if (ntile[t] > 0 && ok && !__all_sync(0xffffffffu, mbar_wait_short(odone, 0))) ok = false;
@@ -540,10 +565,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 //   split     where there are few items, a cluster shares one item's steps out and adds the
 //             sums through distributed shared memory, in rank order.
 constexpr int kWeightThreads = 640;
-#ifndef FMA_EVERY
-#define FMA_EVERY 100
-#endif
-constexpr int kFmaEvery = FMA_EVERY;  // of 4 columns, two go to the FMA pipe in every kFmaEvery-th turn
 constexpr int kColNone = -(1 << 30);  // a column that sees no key
 enum { kResident = 0, kStreamed = 1 };  // > 1: split over so many CTAs
 
@@ -1004,7 +1025,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
           const f32x2 t0 = fma2(pair(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), scale, pair(z.x, z.y));
           const f32x2 t1 = fma2(pair(__uint_as_float(y[e + 2]), __uint_as_float(y[e + 3])), scale, pair(z.z, z.w));
           two[0] = add2(two[0], ex2_sfu(t0));
-          two[1] = add2(two[1], e % (4 * kFmaEvery) == 0 ? ex2_fma(t1) : ex2_sfu(t1));
+          two[1] = add2(two[1], ex2_sfu(t1));
         }
         const float2 a0 = unpair(two[0]), a1 = unpair(two[1]);
         sum[0] = a0.x, sum[1] = a0.y, sum[2] = a1.x, sum[3] = a1.y;
