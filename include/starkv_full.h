@@ -143,13 +143,21 @@ STARKV_API starkv_status starkv_kv4_evict(starkv_ctx* ctx, const starkv_kv4_cach
  * out: device bf16 [total_q][num_q_heads][head_dim] (dense); lse: device fp32
  * [total_q][num_q_heads], ln sum_j exp(score), or NULL.  A query that sees no key has a
  * zero row and lse -inf.
- * Errors: INVALID_ARG, UNSUPPORTED_SHAPE (more than 65535 sequences, or 2^31 blocks); device
+ * workspace: >= starkv_prompt_workspace_bytes, 256-byte aligned (may be NULL where that is
+ * 0); it must not be used by another call at the same time.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE (more than 65535 sequences, or 2^31 blocks),
+ * WORKSPACE_TOO_SMALL; device
  * bit BAD_QUERY_SPAN (cu_q, cu_k or max_q_len; the sequence's rows are left as they were). */
 STARKV_API starkv_status starkv_prompt_attn(starkv_ctx* ctx, const void* q, const void* k, const void* v,
                                             int64_t q_stride, int64_t k_stride, int64_t v_stride,
                                             const int32_t* cu_q, const int32_t* cu_k, int32_t batch, int64_t total_q,
                                             int64_t total_k, int32_t max_q_len, void* out, float* lse,
-                                            starkv_stream_t stream);
+                                            void* workspace, size_t workspace_bytes, starkv_stream_t stream);
+
+/* Workspace bytes of starkv_prompt_attn for packed rows of these sizes (40 MB at most, where
+ * units of its work are shared between SMs).  out: host.  Errors: INVALID_ARG. */
+STARKV_API starkv_status starkv_prompt_workspace_bytes(const starkv_ctx* ctx, int32_t batch, int64_t total_q,
+                                                       int64_t total_k, size_t* out);
 
 /* The attention weight that the last `window` queries of each packed sequence give to
  * its keys: weights[j][kv] = sum over the query heads of KV head kv and over those

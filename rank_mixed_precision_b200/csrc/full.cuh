@@ -69,10 +69,15 @@ struct PromptArgs {
   int batch;
   int64_t total_q, total_k;
 };
-int64_t prompt_blocks(const Ctx& c, int batch, int max_q_len);
+struct PromptPlan {
+  int ctas;             // CTAs that share the key tiles (0: one per pair of query tiles)
+  int64_t blocks;
+  size_t off_ml, off_cuts, ws_bytes;
+};
+PromptPlan plan_prompt(const Ctx& c, int batch, int64_t total_q, int64_t total_k, int max_q_len);
 int64_t weights_items(const Ctx& c, int batch, int max_k_len);
 cudaError_t launch_prompt_attn(const Ctx& c, const PromptArgs& a, int max_q_len, __nv_bfloat16* out, float* lse,
-                               cudaStream_t s);
+                               void* ws, const PromptPlan& plan, cudaStream_t s);
 cudaError_t launch_prompt_weights(const Ctx& c, const PromptArgs& a, const float* lse, int max_k_len, int window,
                                   float* weights, cudaStream_t s);
 

@@ -177,7 +177,7 @@ starkv_status starkv_kv4_evict(starkv_ctx* ctx, const starkv_kv4_cache* cache, c
 starkv_status starkv_prompt_attn(starkv_ctx* ctx, const void* q, const void* k, const void* v, int64_t q_stride,
                                  int64_t k_stride, int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k,
                                  int32_t batch, int64_t total_q, int64_t total_k, int32_t max_q_len, void* out,
-                                 float* lse, starkv_stream_t stream) {
+                                 float* lse, void* workspace, size_t workspace_bytes, starkv_stream_t stream) {
   starkv_status st = check_ctx(ctx);
   if (st) return st;
   const Ctx* c = reinterpret_cast<const Ctx*>(ctx);
@@ -191,10 +191,16 @@ starkv_status starkv_prompt_attn(starkv_ctx* ctx, const void* q, const void* k, 
   if (st) return st;
   if (!out || !aligned(out, 16) || !aligned(lse, 4))
     return fail(STARKV_ERR_INVALID_ARG, "out must be given and 16-byte aligned, lse 4-byte");
-  if (prompt_blocks(*c, batch, max_q_len) > kMaxBlocks) return fail(STARKV_ERR_UNSUPPORTED_SHAPE, "too many blocks");
+  const PromptPlan plan = plan_prompt(*c, batch, total_q, total_k, max_q_len);
+  if (plan.blocks > kMaxBlocks) return fail(STARKV_ERR_UNSUPPORTED_SHAPE, "too many blocks");
+  if (plan.ws_bytes > 0 && (!workspace || workspace_bytes < plan.ws_bytes))
+    return fail(STARKV_ERR_WORKSPACE_TOO_SMALL, "prompt attention needs %zu workspace bytes, got %zu", plan.ws_bytes,
+                workspace ? workspace_bytes : (size_t)0);
+  if (!aligned(workspace, 256)) return fail(STARKV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   PromptArgs a{(const __nv_bfloat16*)q, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, q_stride, k_stride, v_stride,
                cu_q, cu_k, batch, total_q, total_k};
-  const cudaError_t e = launch_prompt_attn(*c, a, max_q_len, (__nv_bfloat16*)out, lse, (cudaStream_t)stream);
+  const cudaError_t e = launch_prompt_attn(*c, a, max_q_len, (__nv_bfloat16*)out, lse, workspace, plan,
+                                           (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");
   return ok();
 }
@@ -221,6 +227,14 @@ starkv_status starkv_prompt_weights(starkv_ctx* ctx, const void* q, const void* 
                total_q, total_k};
   const cudaError_t e = launch_prompt_weights(*c, a, lse, max_k_len, window, weights, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "prompt weights launch");
+  return ok();
+}
+
+starkv_status starkv_prompt_workspace_bytes(const starkv_ctx* ctx, int32_t batch, int64_t total_q, int64_t total_k,
+                                            size_t* out) {
+  if (!ctx || !out) return fail(STARKV_ERR_INVALID_ARG, "NULL argument");
+  if (batch < 0 || total_q < 0 || total_k < 0) return fail(STARKV_ERR_INVALID_ARG, "negative size");
+  *out = batch == 0 || total_q == 0 ? 0 : plan_prompt(*reinterpret_cast<const Ctx*>(ctx), batch, total_q, total_k, 1).ws_bytes;
   return ok();
 }
 

@@ -108,9 +108,15 @@ __device__ __forceinline__ uint32_t movm_trans(uint32_t x) {
 // halves of the 32 banks, and so do V's four rows of a load (t = 0..3).
 __device__ __forceinline__ int token_of(int t, int e, int f) { return 8 * f + 4 * e + ((t + e) & 3); }
 
-// Position of the first page of CTA c's stretch, and the CTA whose stretch holds position x.
-__device__ __forceinline__ int64_t cut(int64_t c, int64_t total, int ctas) { return c * total / ctas; }
-__device__ __forceinline__ int64_t cta_of(int64_t x, int64_t total, int ctas) { return ((x + 1) * ctas - 1) / total; }
+// Position of the first page of CTA c's stretch, and the CTA whose stretch holds position x < total.
+// Where there are fewer pages than CTAs, the last CTAs have none: no stretch between two others
+// is empty.
+__device__ __forceinline__ int64_t cut(int64_t c, int64_t total, int ctas) {
+  return total <= ctas ? min(c, total) : c * total / ctas;
+}
+__device__ __forceinline__ int64_t cta_of(int64_t x, int64_t total, int ctas) {
+  return total <= ctas ? x : ((x + 1) * ctas - 1) / total;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, kCtas) kv4_decode_kernel(const DecodeArgs a) {

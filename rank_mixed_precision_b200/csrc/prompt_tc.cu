@@ -138,7 +138,13 @@ struct SeqSpan {
   bool ok;
 };
 
+struct Cut;
+
 struct PromptKArgs {
+  int ctas;             // CTAs that share the units' key tiles (0: one per unit)
+  float* part_o;        // [ctas][2][256][D], relative to the part's maximum: [0] of a unit that began before the
+  float2* part_ml;      // [ctas][2][256] (maximum, sum)                     CTA's stretch, [1] of one that goes on behind
+  Cut* cuts;            // [ctas]
   int H, h_kv, group, gb, head_blocks, R, batch, max_q, max_k, qtiles, ktiles, window, mode;
   int64_t total_q, total_k;
   const __nv_bfloat16* v;
@@ -166,23 +172,41 @@ __device__ __forceinline__ SeqSpan span_of(const PromptKArgs& a, int b) {
   return s;
 }
 
+// Position at which CTA c's stretch begins, and the CTA whose stretch holds position x < total.
+// Where there are fewer positions than CTAs, the last CTAs have none: no stretch between two
+// others is empty.
+__device__ __forceinline__ int64_t cut(int64_t c, int64_t total, int ctas) {
+  return total <= ctas ? min(c, total) : c * total / ctas;
+}
+__device__ __forceinline__ int64_t cta_of(int64_t x, int64_t total, int ctas) {
+  return total <= ctas ? x : ((x + 1) * ctas - 1) / total;
+}
+
 // ===========================================================================
 // Attention
 // ===========================================================================
-// A CTA takes two query tiles (2 R queries) of one (sequence, KV head, head block) and
-// walks the keys once for both.  Warps 0..3 and 4..7 each hold one tile's softmax (one
-// row per thread), warp 8 copies, warp 9 issues the products, warps 10 and 11 look the V
-// tiles of masked keys over.
+// A unit is two query tiles (2 R queries) of one (sequence, KV head, head block) with all the
+// key tiles that they see.  One CTA an SM takes an equal stretch of the units' key tiles, laid
+// end to end (each unit one position longer, for its start and its end), so that neither few
+// long units nor many of unequal lengths leave SMs idle; a unit that a cut goes through leaves
+// partial results, which a second kernel joins.  Where there are few keys, a CTA takes a whole
+// unit and there is no second kernel.
+//
+// Warps 0..3 and 4..7 each hold one tile's softmax (one row per thread), warp 8 copies, warp 9
+// issues the products, warps 10 and 11 look the V tiles of masked keys over.
 //   S_t = Q_t K_j^T into TMEM; the softmax warps replace it by P_t in bf16 (the same
 //   columns, half as many), which is the A operand of O_t += P_t V_j from TMEM.  In issue
 //   order P_0 V_j, S_0 (j + 1), P_1 V_j, S_1 (j + 1): one tile's products run while the
 //   other tile's softmax does.  The running maximum moves when a score passes it by more
 //   than 2^8 only, and then the row's O is rescaled in place; S_t (j) complete implies
-//   that P_t V_(j-1) is, so no further barrier guards that.
+//   that P_t V_(j-1) is, so no further barrier guards that.  The next unit's Q and first
+//   products run while the softmax warps write the last unit out.
 constexpr int kAttnThreads = 384;
-#ifndef FMA_PAIR
-#define FMA_PAIR(u) ((u) % 8 == 7)
-#endif
+constexpr int kFewKeys = 1024;    // at most this many keys in all: a CTA takes a whole unit
+constexpr int kLeastTiles = 2;    // key tiles of a stretch, where there are few
+// Pairs of exponentials that go to the FMA pipe: one of eight.  (2048 queries over 32768 keys: none
+// 914 us, one of eight 894, one of four 982, half 1070: the softmax warps' issue slots bound them too.)
+__device__ constexpr bool on_fma_pipe(int pair) { return pair % 8 == 7; }
 
 template <int D>
 struct AttnSmem {
@@ -193,6 +217,113 @@ struct AttnSmem {
   static constexpr uint32_t kBytes = kBar + 256 + 1024;
 };
 
+// sum over i < n of floor((a i + b) / m), a, b >= 0, by the Euclidean steps of (a, m).
+__device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+  int64_t sum = 0;
+  while (n > 0) {
+    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const int64_t top = a * n + b;
+    if (top < m) break;
+    n = top / m;
+    b = top % m;
+    const int64_t t = m;
+    m = a;
+    a = t;
+  }
+  return sum;
+}
+
+// Units of a sequence: pairs of query tiles, each with its key tiles.
+struct Pairs {
+  int n, off, M, count;  // queries; query i sees keys 0 .. off + i; queries of a pair
+  __device__ Pairs() {}
+  __device__ Pairs(const SeqSpan& q, int R) : n(q.ok ? q.n : 0), off(q.keys - q.n), M(2 * R) { count = (n + M - 1) / M; }
+  // key tiles of pair i
+  __device__ int tiles(int i) const {
+    const int64_t seen = (int64_t)off + min((int64_t)n, (int64_t)(i + 1) * M);
+    return seen > 0 ? (int)((seen + kTile - 1) / kTile) : 0;
+  }
+  // positions (key tiles, and one a pair) of the pairs before pair x
+  __device__ int64_t before(int x) const {
+    const int64_t whole = min(x, count - 1);                               // pairs of M queries
+    const int64_t first = off >= 0 ? 0 : ((int64_t)M - off) / M - 1;       // the first that sees a key
+    int64_t sum = x;
+    if (whole > first) sum += floor_sum(whole - first, kTile, M, off + (first + 1) * M + kTile - 1);
+    if (x == count && x > 0) sum += tiles(count - 1);
+    return sum;
+  }
+};
+
+// The pieces of a CTA, in order; every role walks its own copy.
+struct Pieces {
+  const PromptKArgs& a;
+  int64_t pos, end;   // positions left
+  int b, u, i, p;     // the next piece's sequence, KV head and head block, pair, and position in the unit
+  SeqSpan q;
+  Pairs pairs;
+  // the present piece: key tiles j0 .. j1 - 1 of nt
+  int j0, j1, nt, kv, hb, pair;
+  bool fresh;         // the next piece is another unit's
+
+  __device__ Pieces(const PromptKArgs& args, int64_t first, int64_t stop, int b_, int u_, int i_, int p_)
+      : a(args), pos(first), end(stop), b(b_), u(u_), i(i_), p(p_), fresh(false) {
+    if (pos < end) {
+      q = span_of(a, b);
+      pairs = Pairs(q, a.R);
+    }
+  }
+  __device__ bool next() {
+    while (pos < end) {
+      if (fresh) {
+        fresh = false;
+        p = 0;
+        if (++i == pairs.count) {
+          i = 0;
+          if (++u == a.h_kv * a.head_blocks) {
+            u = 0;
+            do {  // (a position behind this one is some sequence's)
+              q = span_of(a, ++b);
+              pairs = Pairs(q, a.R);
+            } while (pairs.count == 0);
+          }
+        }
+      }
+      nt = pairs.tiles(i);
+      const int take = (int)min((int64_t)(nt + 1 - p), end - pos);
+      j0 = max(0, p - 1);
+      j1 = p + take - 1;
+      kv = u / a.head_blocks;
+      hb = u % a.head_blocks;
+      pair = i;
+      pos += take;
+      p += take;
+      fresh = p > nt;
+      if (j1 > j0 || nt == 0) return true;
+    }
+    return false;
+  }
+  __device__ bool whole() const { return j0 == 0 && j1 == nt; }
+  __device__ int qbase() const { return pair * pairs.M; }
+  // key tiles of query tile t
+  __device__ int tiles_of(int t) const {
+    const int rows = min(a.R, pairs.n - qbase() - t * a.R);
+    const int keys = rows > 0 ? pairs.off + qbase() + t * a.R + rows : 0;
+    return keys > 0 ? (keys + kTile - 1) / kTile : 0;
+  }
+  // the end of query tile t's key tiles in this piece (j0: none)
+  __device__ int stop_of(int t) const { return max(j0, min(j1, tiles_of(t))); }
+  // the first key tile that some row does not see whole
+  __device__ int first_masked() const { return max(0, pairs.off + qbase() + 1) / kTile; }
+};
+
+// What the join goes by: a unit that begins in this CTA and goes on behind its stretch.
+struct Cut {
+  int there, last;        // 0: none; the CTA that ends the unit
+  int b, kv, hb, pair;
+};
+
 template <int D>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     prompt_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
@@ -201,56 +332,37 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   constexpr int NSUB = D / 64;
   constexpr int ST = SM::kStages;
   extern __shared__ uint8_t smem_raw[];
+  __shared__ int64_t part[kAttnThreads / 32];
+  __shared__ int64_t begin[2];        // the stretch's first sequence, and the positions before it
+  __shared__ int start[3];            // and its unit: u, pair, position
   uint8_t* sm = align1024(smem_raw);
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + SM::kBar);
   uint64_t* qfull = bar;              // both Q tiles landed
-  uint64_t* sfull = bar + 1;          // [2] S_t ready
-  uint64_t* pfull = bar + 3;          // [2][2] P_t written: its first 64 keys, the others
-  uint64_t* look = bar + 7;           // one phase per masked V tile: it is there,
-  uint64_t* clean = bar + 8;          // and it has been looked over
-  uint64_t* odone = bar + 9;          // every product done
-  uint64_t* full = bar + 10;          // [ST]
+  uint64_t* qempty = bar + 1;         // and have been read
+  uint64_t* sfull = bar + 2;          // [2] S_t ready
+  uint64_t* pfull = bar + 4;          // [2][2] P_t written: its first 64 keys, the others
+  uint64_t* odone = bar + 8;          // [2] a piece's products into O_t done
+  uint64_t* oempty = bar + 10;        // [2] O_t read
+  uint64_t* look = bar + 12;          // one phase per masked V tile: it is there,
+  uint64_t* clean = bar + 13;         // and it has been looked over
+  uint64_t* full = bar + 14;          // [ST]
   uint64_t* empty = full + ST;        // [ST]
   uint32_t* tslot = reinterpret_cast<uint32_t*>(empty + ST);
   int* dirty = reinterpret_cast<int*>(tslot + 1);  // a masked V tile held a value that is not finite
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  const int units = a.h_kv * a.head_blocks * a.batch;
-  const int unit = blockIdx.x % units;
-  const int qt = a.qtiles - 1 - (int)(blockIdx.x / units);  // the tiles with the most keys first
-  const int hb = unit % a.head_blocks, kv = unit / a.head_blocks % a.h_kv, b = unit / a.head_blocks / a.h_kv;
-  pdl_wait();
-  pdl_launch_dependents();
-  const SeqSpan q = span_of(a, b);
-  if (!q.ok) {
-    if (tid == 0) set_status(a.status, STARKV_DEV_BAD_QUERY_SPAN);
-    return;
-  }
-  const int qbase = qt * 2 * a.R;
-  if (qbase >= q.n) return;
-  const int off = q.keys - q.n;  // query i sees keys 0 .. off + i
-  const int heads = min(a.gb, a.group - hb * a.gb);
-  const int h0 = kv * a.group + hb * a.gb;
-  int ntile[2];  // key tiles of the two query tiles
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int rows = min(a.R, q.n - qbase - t * a.R);
-    const int keys = rows > 0 ? off + qbase + t * a.R + rows : 0;  // keys that its last query sees
-    ntile[t] = keys > 0 ? (keys + kTile - 1) / kTile : 0;
-  }
-  const int nt = max(ntile[0], ntile[1]);
-  // the first key tile that some row does not see whole
-  const int first_masked = max(0, off + qbase + 1) / kTile;
-
   if (warp == 9) tmem_alloc(tslot, 512);
   if (tid == 0) {
     mbar_init(qfull, 1);
-    mbar_init(&sfull[0], 1);
-    mbar_init(&sfull[1], 1);
+    mbar_init(qempty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sfull[s], 1);
+      mbar_init(&odone[s], 1);
+      mbar_init(&oempty[s], 4);
+    }
     for (int s = 0; s < 4; ++s) mbar_init(&pfull[s], 4);
     mbar_init(look, 1);
     mbar_init(clean, 2);
-    mbar_init(odone, 1);
     for (int s = 0; s < ST; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -258,96 +370,192 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     *dirty = 0;
     fence_mbar_init();
   }
-  tc_fence_before();
-  __syncthreads();
+  pdl_wait();
+  pdl_launch_dependents();
+  // ---- the CTA's stretch
+  const int units = a.h_kv * a.head_blocks;
+  int64_t pos = 0, end = 0, total = 0;
+  if (a.ctas == 0) {
+    const int each = units * a.batch, unit = blockIdx.x % each;
+    if (tid == 0) {
+      const int i = a.qtiles - 1 - (int)(blockIdx.x / each);  // the pairs with the most keys first
+      begin[0] = unit / units;
+      start[0] = unit % units;
+      start[1] = i;
+      start[2] = 0;
+      const SeqSpan q = span_of(a, unit / units);
+      if (!q.ok) set_status(a.status, STARKV_DEV_BAD_QUERY_SPAN);
+      const Pairs pairs(q, a.R);
+      begin[1] = i < pairs.count ? pairs.tiles(i) + 1 : 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    end = begin[1];
+  } else {
+    int64_t mine = 0;
+    for (int i = tid; i < a.batch; i += kAttnThreads) {
+      const SeqSpan q = span_of(a, i);
+      if (!q.ok && blockIdx.x == 0) set_status(a.status, STARKV_DEV_BAD_QUERY_SPAN);
+      const Pairs pairs(q, a.R);
+      mine += pairs.before(pairs.count);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) part[warp] = mine;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kAttnThreads / 32; ++w) total += part[w];
+    total *= units;
+    pos = cut(blockIdx.x, total, a.ctas);
+    end = cut(blockIdx.x + 1, total, a.ctas);
+    if (warp == 0 && pos < end) {
+      // the sequence that holds pos, 32 at a time
+      int64_t carry = 0;
+      for (int i0 = 0; i0 < a.batch; i0 += 32) {
+        int64_t w = 0;
+        if (i0 + lane < a.batch) {
+          const Pairs pairs(span_of(a, i0 + lane), a.R);
+          w = pairs.before(pairs.count) * units;
+        }
+        int64_t inc = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += v;
+        }
+        if (carry + inc - w <= pos && pos < carry + inc) {
+          begin[0] = i0 + lane;
+          begin[1] = carry + inc - w;
+        }
+        carry += __shfl_sync(0xffffffffu, inc, 31);
+      }
+      __syncwarp();
+      // its unit: the last pair that begins at or before the position, in 32 parts at a time
+      const Pairs pairs(span_of(a, (int)begin[0]), a.R);
+      const int64_t each = pairs.before(pairs.count), in = pos - begin[1], rest = in % each;
+      int lo = 0, hi = pairs.count;
+      while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const uint32_t yes = __ballot_sync(0xffffffffu, at < hi && pairs.before(at) <= rest);
+        lo += (31 - __clz(yes)) * step;  // (lane 0's is always one)
+        hi = min(hi, lo + step);
+      }
+      if (lane == 0) {
+        start[0] = (int)(in / each);
+        start[1] = lo;
+        start[2] = (int)(rest - pairs.before(lo));
+      }
+    }
+    tc_fence_before();
+    __syncthreads();
+  }
   tc_fence_after();
   const uint32_t tmem = *tslot;
   bool ok = true;
+  Pieces it(a, pos, end, pos < end ? (int)begin[0] : 0, start[0], start[1], start[2]);
 
   if (warp == 8) {
     // ---------------- copies ----------------
-    if (lane == 0 && nt > 0) {
-      mbar_arrive_expect_tx(qfull, 2u * NSUB * a.R * a.gb * 128);
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < NSUB; ++i)
-          tma_load_3d(sm + t * SM::kTileBytes + i * kSub, &q_map, i * 64, h0, q.q0 + qbase + t * a.R, qfull);
-      int issued = 0;
-      for (; issued < 2 * nt; ++issued) {
-        const int s = issued % ST, j = issued >> 1;
-        if (!mbar_wait_short(&empty[s], ((issued / ST) & 1) ^ 1)) {
+    if (lane == 0) {
+      int r = 0, pieces = 0;  // ring positions and pieces with keys so far
+      while (ok && it.next()) {
+        if (it.nt == 0) continue;
+        if (!mbar_wait_short(qempty, (pieces & 1) ^ 1)) {
           ok = false;
           break;
         }
-        mbar_arrive_expect_tx(&full[s], SM::kTileBytes);
+        mbar_arrive_expect_tx(qfull, 2u * NSUB * a.R * a.gb * 128);
 #pragma unroll
-        for (int i = 0; i < NSUB; ++i)
-          tma_load_2d(sm + SM::kRing + s * SM::kTileBytes + i * kSub, issued & 1 ? &v_map : &k_map, kv * D + i * 64,
-                      q.k0 + j * kTile, &full[s]);
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < NSUB; ++i)
+            tma_load_3d(sm + t * SM::kTileBytes + i * kSub, &q_map, i * 64, it.kv * a.group + it.hb * a.gb,
+                        it.q.q0 + it.qbase() + t * a.R, qfull);
+        ++pieces;
+        for (int e = 2 * it.j0; e < 2 * it.j1; ++e, ++r) {
+          const int s = r % ST;
+          if (!mbar_wait_short(&empty[s], ((r / ST) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[s], SM::kTileBytes);
+#pragma unroll
+          for (int i = 0; i < NSUB; ++i)
+            tma_load_2d(sm + SM::kRing + s * SM::kTileBytes + i * kSub, e & 1 ? &v_map : &k_map, it.kv * D + i * 64,
+                        it.q.k0 + (e >> 1) * kTile, &full[s]);
+        }
       }
       if (!ok) {  // wait (with a limit) for the copies in flight
-        mbar_wait(qfull, 0, 100000000ull);
-        for (int i = max(0, issued - ST); i < issued; ++i) mbar_wait(&full[i % ST], (i / ST) & 1, 100000000ull);
+        if (pieces > 0) mbar_wait(qfull, (pieces - 1) & 1, 100000000ull);
+        for (int i = max(0, r - ST); i < r; ++i) mbar_wait(&full[i % ST], (i / ST) & 1, 100000000ull);
       }
     }
   } else if (warp == 9) {
     // ---------------- products ----------------
-    if (nt > 0) {
-      constexpr uint32_t idesc_s = idesc_bf16(128, kTile, false, false);
-      constexpr uint32_t idesc_o = idesc_bf16(128, D, false, true);
-      const bool lead = elected();
-      const uint64_t qd = make_sdesc(smem_u32(sm), 16, 1024, 2);
-      const uint64_t kd = make_sdesc(smem_u32(sm + SM::kRing), 16, 1024, 2);
-      const uint64_t vd = make_sdesc(smem_u32(sm + SM::kRing), kSub, 1024, 2);
-      auto issue_s = [&](int t, int stage) {
-        const uint64_t q0 = desc_at(qd, t * SM::kTileBytes), k0 = desc_at(kd, stage * SM::kTileBytes);
+    constexpr uint32_t idesc_s = idesc_bf16(128, kTile, false, false);
+    constexpr uint32_t idesc_o = idesc_bf16(128, D, false, true);
+    const bool lead = elected();
+    const uint64_t qd = make_sdesc(smem_u32(sm), 16, 1024, 2);
+    const uint64_t kd = make_sdesc(smem_u32(sm + SM::kRing), 16, 1024, 2);
+    const uint64_t vd = make_sdesc(smem_u32(sm + SM::kRing), kSub, 1024, 2);
+    auto issue_s = [&](int t, int stage) {
+      const uint64_t q0 = desc_at(qd, t * SM::kTileBytes), k0 = desc_at(kd, stage * SM::kTileBytes);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t o = (ks >> 2) * kSub + (ks & 3) * 32;
-          mma_f16(tmem + t * kTile, desc_at(q0, o), desc_at(k0, o), idesc_s, ks > 0);
-        }
-        mma_commit(&sfull[t]);
-      };
-      auto all = [&](bool got) { return __all_sync(0xffffffffu, got) != 0; };
-      // the ring's positions: K_j at kst, V_j at vst, each with its phase
-      int kst = 0, vst = 1;
-      uint32_t kph = 0, vph = 0;
-      auto on = [&](int& st, uint32_t& ph) {
-        st += 2;
-        if (st >= ST) {
-          st -= ST;
-          ph ^= 1;
-        }
-      };
-      ok = all(mbar_wait_short(qfull, 0) && mbar_wait_short(&full[0], 0));
-      if (ok) {
-        tc_fence_after();
-        if (lead) {
-          if (ntile[0] > 0) issue_s(0, 0);
-          if (ntile[1] > 0) issue_s(1, 0);
-          mma_commit(&empty[0]);
-        }
-        __syncwarp();
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t o = (ks >> 2) * kSub + (ks & 3) * 32;
+        mma_f16(tmem + t * kTile, desc_at(q0, o), desc_at(k0, o), idesc_s, ks > 0);
       }
-      uint32_t looked = 0;
-      for (int j = 0; ok && j < nt; ++j) {
-        on(kst, kph);
+      mma_commit(&sfull[t]);
+    };
+    auto all = [&](bool got) { return __all_sync(0xffffffffu, got) != 0; };
+    // the ring's positions: a piece's next K and V tiles, each with its phase
+    int kst = 0, vst = 1;
+    uint32_t kph = 0, vph = 0;
+    auto on = [&](int& st, uint32_t& ph) {
+      st += 2;
+      if (st >= ST) {
+        st -= ST;
+        ph ^= 1;
+      }
+    };
+    uint32_t qph = 0, looked = 0, pph[2] = {0, 0}, oph[2] = {0, 0};
+    while (ok && it.next()) {
+      if (it.nt == 0) continue;
+      const int j0 = it.j0, j1 = it.j1, first_masked = it.first_masked();
+      const int stop[2] = {it.stop_of(0), it.stop_of(1)};
+      ok = all(mbar_wait_short(qfull, qph) && mbar_wait_short(&full[kst], kph));
+      qph ^= 1;
+      if (!ok) break;
+      tc_fence_after();
+      if (lead) {
+        if (stop[0] > j0) issue_s(0, kst);
+        if (stop[1] > j0) issue_s(1, kst);
+        mma_commit(&empty[kst]);
+        if (j1 - j0 == 1) mma_commit(qempty);
+      }
+      __syncwarp();
+      on(kst, kph);
+      for (int j = j0; ok && j < j1; ++j) {
+        const bool more = j + 1 < j1;
         bool got = mbar_wait_short(&full[vst], vph);
         if (got && j >= first_masked) {
           if (lane == 0) mbar_arrive(look);
           got = mbar_wait_short(clean, looked);
           looked ^= 1;
         }
-        if (got && j + 1 < nt) got = mbar_wait_short(&full[kst], kph);
+        if (got && more) got = mbar_wait_short(&full[kst], kph);
         ok = all(got);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (!ok || j >= ntile[t]) continue;
+          if (!ok || j >= stop[t]) continue;
+          if (j == j0) {  // the piece before has been read out of O_t
+            ok = all(mbar_wait_short(&oempty[t], oph[t] ^ 1));
+            oph[t] ^= 1;
+          }
           const uint64_t v0 = desc_at(vd, vst * SM::kTileBytes);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (!all(ok && mbar_wait_short(&pfull[t * 2 + h], j & 1))) {
+            if (!all(ok && mbar_wait_short(&pfull[t * 2 + h], pph[t]))) {
               ok = false;
               continue;
             }
@@ -356,186 +564,232 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
               for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
                 mma_f16_ts(tmem + 256 + t * kTile, tmem + t * kTile + ks * 8, desc_at(v0, ks * 2048), idesc_o,
-                           j > 0 || ks > 0);
+                           j > j0 || ks > 0);
             }
             __syncwarp();
           }
+          pph[t] ^= 1;
           if (!ok) continue;
           if (lead) {
-            if (t == 1 || j >= ntile[1]) mma_commit(&empty[vst]);
-            if (j + 1 < ntile[t]) issue_s(t, kst);
+            if (j + 1 < stop[t]) issue_s(t, kst);
+            else mma_commit(&odone[t]);
           }
           __syncwarp();
         }
-        if (ok && j + 1 < nt && lead) mma_commit(&empty[kst]);
+        if (ok && lead) {
+          mma_commit(&empty[vst]);
+          if (more) mma_commit(&empty[kst]);
+          if (j + 2 == j1) mma_commit(qempty);
+        }
+        __syncwarp();
         on(vst, vph);
+        if (more) on(kst, kph);
       }
-      if (lead) mma_commit(odone);  // completes once every product issued above has
+      // (K_(j1) of the next piece follows V_(j1 - 1): kst already stands there)
+    }
+    if (!ok) {  // the products in flight still read shared memory and TMEM: wait (with a limit)
+      if (lead) mma_commit(&odone[0]);
       __syncwarp();
-      if (!ok) mbar_wait(odone, 0, 100000000ull);
+      const uint64_t t0 = global_ns();
+      while (global_ns() - t0 < 100000000ull) {
+      }
     }
   } else if (warp >= 10) {
     // ---------------- V tiles with masked keys ----------------
     // A key that some row does not see has p = 0 there, but 0 * inf and 0 * NaN are not 0, and the
     // rows behind the sequence are another's.  So values that are not finite are cleared (rows
     // behind the sequence, whatever they hold) and, where a row does see them, added at the end.
-    for (int j = first_masked; ok && j < nt; ++j) {
-      const int i = 2 * j + 1;
-      const bool got = mbar_wait_short(look, (j - first_masked) & 1) && mbar_wait_short(&full[i % ST], (i / ST) & 1);
-      if (!__all_sync(0xffffffffu, got)) {
-        ok = false;
-        break;
-      }
-      uint8_t* tile = sm + SM::kRing + (i % ST) * SM::kTileBytes;
-      bool mine = false;
-      for (int e = (warp - 10) * 32 + lane; e < kTile * D / 8; e += 64) {
-        uint4* p = reinterpret_cast<uint4*>(tile) + e;
-        uint4 x = *p;
-        uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-        bool hit = false;
+    int r = 0;
+    uint32_t looked = 0;
+    while (ok && it.next()) {
+      if (it.nt == 0) continue;
+      for (int j = max(it.j0, it.first_masked()); j < it.j1; ++j) {
+        const int i = r + 2 * (j - it.j0) + 1;
+        const bool got = mbar_wait_short(look, looked) && mbar_wait_short(&full[i % ST], (i / ST) & 1);
+        looked ^= 1;
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        uint8_t* tile = sm + SM::kRing + (i % ST) * SM::kTileBytes;
+        bool mine = false;
+        for (int e = (warp - 10) * 32 + lane; e < kTile * D / 8; e += 64) {
+          uint4* p = reinterpret_cast<uint4*>(tile) + e;
+          uint4 x = *p;
+          uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+          bool hit = false;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if ((w[u] & 0x7f80u) == 0x7f80u) {
-            w[u] &= 0xffff0000u;
-            hit = true;
+          for (int u = 0; u < 4; ++u) {
+            if ((w[u] & 0x7f80u) == 0x7f80u) {
+              w[u] &= 0xffff0000u;
+              hit = true;
+            }
+            if ((w[u] & 0x7f800000u) == 0x7f800000u) {
+              w[u] &= 0x0000ffffu;
+              hit = true;
+            }
           }
-          if ((w[u] & 0x7f800000u) == 0x7f800000u) {
-            w[u] &= 0x0000ffffu;
-            hit = true;
+          if (hit) {
+            *p = x;
+            mine = true;
           }
         }
-        if (hit) {
-          *p = x;
-          mine = true;
-        }
+        if (mine) *reinterpret_cast<volatile int*>(dirty) = 1;
+        __threadfence_block();
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(clean);
       }
-      if (mine) *reinterpret_cast<volatile int*>(dirty) = 1;
-      __threadfence_block();
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(clean);
+      r += 2 * (it.j1 - it.j0);
     }
   } else {
     // ---------------- softmax: one row per thread ----------------
     const int t = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
-    const int qi = qbase + t * a.R + r / a.gb;  // query of the row
-    const int hh = r % a.gb;
-    const bool live = r < a.R * a.gb && qi < q.n && hh < heads;
-    const int seen = live ? off + qi + 1 : 1 << 30;  // keys the row sees (may be <= 0); a row of nothing masks nothing
+    const int row_q = t * a.R + r / a.gb, hh = r % a.gb;  // the row's query within the pair, and head within the block
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ts = trow + t * kTile, to = trow + 256 + t * kTile;
-    float m = -INFINITY, l = 0.f;
-    for (int j = 0; j < ntile[t]; ++j) {
-      if (!__all_sync(0xffffffffu, mbar_wait_short(&sfull[t], j & 1))) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      float sv[kTile];
-      {
-        uint32_t(&raw)[kTile] = *reinterpret_cast<uint32_t(*)[kTile]>(sv);
+    uint32_t sph = 0, oph = 0;
+    while (ok && it.next()) {
+      const int qi = it.qbase() + row_q;
+      const int heads = min(a.gb, a.group - it.hb * a.gb);
+      const bool live = r < a.R * a.gb && qi < it.pairs.n && hh < heads;
+      const int seen = live ? it.pairs.off + qi + 1 : 1 << 30;  // keys the row sees (may be <= 0); a row of nothing masks nothing
+      const int j0 = it.j0, stop = it.nt > 0 ? it.stop_of(t) : j0;
+      float m = -INFINITY, l = 0.f;
+      for (int j = j0; j < stop; ++j) {
+        if (!__all_sync(0xffffffffu, mbar_wait_short(&sfull[t], sph))) {
+          ok = false;
+          break;
+        }
+        sph ^= 1;
+        tc_fence_after();
+        float sv[kTile];
+        {
+          uint32_t(&raw)[kTile] = *reinterpret_cast<uint32_t(*)[kTile]>(sv);
 #pragma unroll
-        for (int c = 0; c < kTile / 32; ++c) tmem_ld32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&raw[c * 32]));
-        tmem_ld_wait();
-      }
-      const int lim = seen - j * kTile;
-      if (__any_sync(0xffffffffu, lim < kTile)) {
+          for (int c = 0; c < kTile / 32; ++c) tmem_ld32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&raw[c * 32]));
+          tmem_ld_wait();
+        }
+        const int lim = seen - j * kTile;
+        if (__any_sync(0xffffffffu, lim < kTile)) {
 #pragma unroll
-        for (int c = 0; c < kTile; ++c) sv[c] = c < lim ? sv[c] : -INFINITY;
-      }
-      float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
+          for (int c = 0; c < kTile; ++c) sv[c] = c < lim ? sv[c] : -INFINITY;
+        }
+        float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
-      for (int c = 4; c < kTile - 4; c += 8)
+        for (int c = 4; c < kTile - 4; c += 8)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], sv[c + u], sv[c + 4 + u]);
-      const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], sv[kTile - 4], sv[kTile - 3]),
-                             fmaxf(sv[kTile - 2], sv[kTile - 1]));
-      const bool move = live && (top - m) * a.scale_log2 > kMoveMax;  // m = -inf: true but for a row without scores
-      if (__any_sync(0xffffffffu, move)) {
-        if (j > 0) {
-          const float f = move ? ex2((m - top) * a.scale_log2) : 1.f;
+          for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], sv[c + u], sv[c + 4 + u]);
+        const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], sv[kTile - 4], sv[kTile - 3]),
+                               fmaxf(sv[kTile - 2], sv[kTile - 1]));
+        const bool move = live && (top - m) * a.scale_log2 > kMoveMax;  // m = -inf: true but for a row without scores
+        if (__any_sync(0xffffffffu, move)) {
+          if (j > j0) {
+            const float f = move ? ex2((m - top) * a.scale_log2) : 1.f;
 #pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t o[16];
-            tmem_ld16(to + c * 16, o);
-            tmem_ld_wait();
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(to + c * 16, o);
+              tmem_ld_wait();
 #pragma unroll
-            for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
-            tmem_st16(to + c * 16, o);
+              for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+              tmem_st16(to + c * 16, o);
+            }
+            l *= f;
           }
-          l *= f;
+          if (move) m = top;
         }
-        if (move) m = top;
-      }
-      const float base = m == -INFINITY ? 0.f : -m * a.scale_log2;
-      const f32x2 scale2 = pair(a.scale_log2, a.scale_log2), base2 = pair(base, base);
-      f32x2 sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-      // four quarters; the first half of P goes on its way while the third quarter is computed
+        const float base = m == -INFINITY ? 0.f : -m * a.scale_log2;
+        const f32x2 scale2 = pair(a.scale_log2, a.scale_log2), base2 = pair(base, base);
+        f32x2 sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+        // four quarters; the first half of P goes on its way while the third quarter is computed
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t w[16];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
 #pragma unroll
-        for (int u = 0; u < 16; ++u) {
-          const f32x2 x = fma2(pair(sv[c * 32 + 2 * u], sv[c * 32 + 2 * u + 1]), scale2, base2);
-          const f32x2 p = FMA_PAIR(u) ? ex2_fma(x) : ex2_sfu(x);
-          sum[u & 1] = add2(sum[u & 1], p);
-          const float2 y = unpair(p);
-          w[u] = pack_bf2(y.x, y.y);
+          for (int u = 0; u < 16; ++u) {
+            const f32x2 x = fma2(pair(sv[c * 32 + 2 * u], sv[c * 32 + 2 * u + 1]), scale2, base2);
+            const f32x2 p = on_fma_pipe(u) ? ex2_fma(x) : ex2_sfu(x);
+            sum[u & 1] = add2(sum[u & 1], p);
+            const float2 y = unpair(p);
+            w[u] = pack_bf2(y.x, y.y);
+          }
+          if (c == 2) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pfull[t * 2]);
+          }
+          tmem_st16(ts + c * 16, w);
         }
-        if (c == 2) {
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&pfull[t * 2]);
-        }
-        tmem_st16(ts + c * 16, w);
+        const float2 s0 = unpair(sum[0]), s1 = unpair(sum[1]);
+        l += (s0.x + s0.y) + (s1.x + s1.y);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[t * 2 + 1]);
       }
-      const float2 s0 = unpair(sum[0]), s1 = unpair(sum[1]);
-      l += (s0.x + s0.y) + (s1.x + s1.y);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pfull[t * 2 + 1]);
-    }
-    // ---- O / l, and lse
-    if (ntile[t] > 0 && ok && !__all_sync(0xffffffffu, mbar_wait_short(odone, 0))) ok = false;
-    if (ok) {
-      tc_fence_after();
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int64_t row = (int64_t)(q.q0 + qi) * a.H + h0 + hh;
-      const bool fix = ntile[t] > 0 && *reinterpret_cast<volatile int*>(dirty) != 0;
+      if (!ok) break;
+      // ---- O / l and lse, or the part: O, m, l
+      const bool any = stop > j0;
+      if (any) {
+        if (!__all_sync(0xffffffffu, mbar_wait_short(&odone[t], oph))) {
+          ok = false;
+          break;
+        }
+        oph ^= 1;
+        tc_fence_after();
+      }
+      const bool whole = it.whole();
+      const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      const int64_t row = (int64_t)(it.q.q0 + qi) * a.H + it.kv * a.group + it.hb * a.gb + hh;
+      const int64_t slot = ((int64_t)blockIdx.x * 2 + (j0 == 0)) * 2 * kTile + t * kTile + r;
+      const bool fix = any && *reinterpret_cast<volatile int*>(dirty) != 0;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
-        if (ntile[t] > 0) {
+        __syncwarp();
+        if (any) {
           tmem_ld32(to + c * 32, o);
           tmem_ld_wait();
+          if (c == D / 32 - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&oempty[t]);
+          }
         } else {
 #pragma unroll
           for (int u = 0; u < 32; ++u) o[u] = 0u;
         }
         if (!live) continue;
         if (fix)
-          for (int j = first_masked * kTile; j < seen; ++j) {
-            const __nv_bfloat16* vr = a.v + (int64_t)(q.k0 + j) * a.v_stride + kv * D + c * 32;
+          for (int j = max(it.first_masked(), j0) * kTile; j < min(seen, stop * kTile); ++j) {
+            const __nv_bfloat16* vr = a.v + (int64_t)(it.q.k0 + j) * a.v_stride + it.kv * D + c * 32;
 #pragma unroll
             for (int u = 0; u < 32; ++u) {
               const float x = __bfloat162float(vr[u]);
               if (!isfinite(x)) o[u] = __float_as_uint(__uint_as_float(o[u]) + x);
             }
           }
-        uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + c * 32);
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + c * 32);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          uint32_t w[4];
+          for (int u = 0; u < 4; ++u) {
+            uint32_t w[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            w[x] = pack_bf2(__uint_as_float(o[8 * u + 2 * x]) * inv, __uint_as_float(o[8 * u + 2 * x + 1]) * inv);
-          dst[u] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int x = 0; x < 4; ++x)
+              w[x] = pack_bf2(__uint_as_float(o[8 * u + 2 * x]) * inv, __uint_as_float(o[8 * u + 2 * x + 1]) * inv);
+            dst[u] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(a.part_o + slot * D + c * 32);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) dst[u] = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
         }
       }
-      if (live && a.lse) a.lse[row] = l == 0.f ? -INFINITY : fmaf(m, a.scale, logf(l));
+      if (live && whole && a.lse) a.lse[row] = l == 0.f ? -INFINITY : fmaf(m, a.scale, logf(l));
+      if (live && !whole) a.part_ml[slot] = make_float2(m, l);
     }
   }
   if (!ok && lane == 0) set_status(a.status, kDevWaitTimeout);
@@ -544,6 +798,65 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+  if (a.ctas > 0 && tid == 0) {
+    // the unit that goes on behind the stretch, if its first key tiles are here: the last piece's
+    Cut c = {0, 0, 0, 0, 0, 0};
+    if (pos < end) {
+      Pieces last(a, pos, end, (int)begin[0], start[0], start[1], start[2]);
+      bool any = false;
+      int64_t unit_end = 0;
+      while (last.next()) {
+        any = last.j0 == 0 && last.j1 < last.nt;
+        unit_end = last.pos + (last.nt - last.j1);
+      }
+      if (any) c = Cut{1, (int)cta_of(unit_end - 1, total, a.ctas), last.b, last.kv, last.hb, last.pair};
+    }
+    a.cuts[blockIdx.x] = c;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Join of the units that a cut went through: block (c, y) takes 32 rows of the unit that
+// begins in CTA c's stretch and goes on behind it.
+// ---------------------------------------------------------------------------
+constexpr int kMergeThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) prompt_join_kernel(const PromptKArgs a) {
+  constexpr int kRow = D / 4;  // threads of a row
+  pdl_wait();
+  pdl_launch_dependents();
+  const int first = blockIdx.x;
+  const Cut c = a.cuts[first];
+  if (!c.there) return;
+  const SeqSpan q = span_of(a, c.b);
+  const int c4 = threadIdx.x % kRow * 4;
+  for (int e = threadIdx.x / kRow; e < 32; e += kMergeThreads / kRow) {
+    const int r2 = blockIdx.y * 32 + e, t = r2 / kTile, r = r2 % kTile;  // row of the unit; its tile, and row there
+    const int qi = c.pair * 2 * a.R + t * a.R + r / a.gb, hh = r % a.gb;
+    if (r >= a.R * a.gb || qi >= q.n || hh >= min(a.gb, a.group - c.hb * a.gb)) continue;
+    auto slot = [&](int k) { return ((int64_t)k * 2 + (k == first)) * 2 * kTile + r2; };
+    float m = -INFINITY;
+    for (int k = first; k <= c.last; ++k) m = fmaxf(m, a.part_ml[slot(k)].x);
+    float l = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = first; k <= c.last; ++k) {
+      const float2 ml = a.part_ml[slot(k)];
+      if (ml.y == 0.f) continue;  // no scores of the row there
+      const float f = m == -INFINITY ? 1.f : ex2((ml.x - m) * a.scale_log2);
+      const float4 x = *reinterpret_cast<const float4*>(a.part_o + slot(k) * D + c4);
+      l = fmaf(ml.y, f, l);
+      v.x = fmaf(x.x, f, v.x);
+      v.y = fmaf(x.y, f, v.y);
+      v.z = fmaf(x.z, f, v.z);
+      v.w = fmaf(x.w, f, v.w);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t row = (int64_t)(q.q0 + qi) * a.H + c.kv * a.group + c.hb * a.gb + hh;
+    *reinterpret_cast<uint2*>(a.out + row * D + c4) =
+        make_uint2(pack_bf2(v.x * inv, v.y * inv), pack_bf2(v.z * inv, v.w * inv));
+    if (c4 == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : fmaf(m, a.scale, logf(l));
   }
 }
 
@@ -1141,8 +1454,10 @@ cudaError_t launch_attn_d(const CUtensorMap& qm, const CUtensorMap& km, const CU
   const size_t smem = AttnSmem<D>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(prompt_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const unsigned blocks = (unsigned)a.qtiles * a.h_kv * a.head_blocks * a.batch;
-  return launch_chained(prompt_attn_kernel<D>, dim3(blocks), dim3(kAttnThreads), smem, s, 1u, qm, km, vm, a);
+  const unsigned blocks = a.ctas > 0 ? (unsigned)a.ctas : (unsigned)a.qtiles * a.h_kv * a.head_blocks * a.batch;
+  e = launch_chained(prompt_attn_kernel<D>, dim3(blocks), dim3(kAttnThreads), smem, s, 1u, qm, km, vm, a);
+  if (e != cudaSuccess || a.ctas == 0) return e;
+  return launch_chained(prompt_join_kernel<D>, dim3(a.ctas, 2 * kTile / 32), dim3(kMergeThreads), 0, s, 1u, a);
 }
 
 template <int D>
@@ -1172,19 +1487,38 @@ int64_t weights_items(const Ctx& c, int batch, int max_k_len) {
   return ((int64_t)max_k_len + kTile - 1) / kTile * c.cfg.num_kv_heads * batch;
 }
 
-int64_t prompt_blocks(const Ctx& c, int batch, int max_q_len) {
-  PromptArgs p = {};
-  const PromptKArgs a = args_of(c, p);
-  return ((int64_t)max_q_len + 2 * a.R - 1) / (2 * a.R) * a.h_kv * a.head_blocks * batch;
+PromptPlan plan_prompt(const Ctx& c, int batch, int64_t total_q, int64_t total_k, int max_q_len) {
+  PromptPlan p = {};
+  const PromptKArgs a = args_of(c, PromptArgs{});
+  const int64_t units = (int64_t)a.h_kv * a.head_blocks;
+  p.blocks = ((int64_t)max_q_len + 2 * a.R - 1) / (2 * a.R) * units * batch;
+  if (total_k <= kFewKeys) return p;
+  int sms = 148;
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c.device);
+  // at most so many pairs of query tiles, and key tiles of one
+  const int64_t pairs = total_q / (2 * a.R) + batch, tiles = (total_k + kTile - 1) / kTile;
+  const int64_t most = pairs * units >= sms ? sms : pairs * units * ((tiles + kLeastTiles - 1) / kLeastTiles);
+  p.ctas = (int)(most < sms ? most : sms);
+  p.blocks = p.ctas;
+  auto al = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t rows = (size_t)p.ctas * 2 * 2 * kTile;
+  p.off_ml = al(rows * c.cfg.head_dim * 4);
+  p.off_cuts = p.off_ml + al(rows * 8);
+  p.ws_bytes = p.off_cuts + al((size_t)p.ctas * sizeof(Cut));
+  return p;
 }
 
 cudaError_t launch_prompt_attn(const Ctx& c, const PromptArgs& p, int max_q_len, __nv_bfloat16* out, float* lse,
-                               cudaStream_t s) {
+                               void* ws, const PromptPlan& plan, cudaStream_t s) {
   PromptKArgs a = args_of(c, p);
   a.max_q = max_q_len;
   a.qtiles = (max_q_len + 2 * a.R - 1) / (2 * a.R);
   a.out = out;
   a.lse = lse;
+  a.ctas = plan.ctas;
+  a.part_o = (float*)ws;
+  a.part_ml = (float2*)((char*)ws + plan.off_ml);
+  a.cuts = (Cut*)((char*)ws + plan.off_cuts);
   CUtensorMap qm, km, vm;
   if (!map_q(c, p, a, &qm)) return cudaErrorInvalidValue;
   km = vm = qm;  // no keys at all: nothing is copied

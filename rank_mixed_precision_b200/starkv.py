@@ -35,7 +35,7 @@ EXPORTS = [
 # every function include/starkv_full.h declares
 EXPORTS_FULL = [
     "starkv_kv4_layout", "starkv_kv4_append", "starkv_kv4_read", "starkv_kv4_decode_attn", "starkv_kv4_evict",
-    "starkv_prompt_attn", "starkv_prompt_weights",
+    "starkv_prompt_attn", "starkv_prompt_workspace_bytes", "starkv_prompt_weights",
 ]
 
 
@@ -111,8 +111,9 @@ _SIGS = {
                                 _vp], _i32),
     "starkv_kv4_evict": ([_vp, ctypes.POINTER(starkv_kv4_cache), _vp, _vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp,
                           _vp], _i32),
-    "starkv_prompt_attn": ([_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp],
-                           _i32),
+    "starkv_prompt_attn": ([_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp, _sz,
+                            _vp], _i32),
+    "starkv_prompt_workspace_bytes": ([_vp, _i32, _i64, _i64, ctypes.POINTER(_sz)], _i32),
     "starkv_prompt_weights": ([_vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i32, _i64, _i64, _i32, _i32, _vp, _vp], _i32),
 }
 
@@ -495,7 +496,13 @@ def _packed(cfg, q, k, cu_q, cu_k):
     return qs, ks
 
 
-def starkv_prompt_attn(ctx, cfg, q, k, v, cu_q, cu_k, max_q_len, out, lse=None, stream=None):
+def starkv_prompt_workspace_bytes(ctx, batch: int, total_q: int, total_k: int) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().starkv_prompt_workspace_bytes(ctx, batch, total_q, total_k, ctypes.byref(out)))
+    return out.value
+
+
+def starkv_prompt_attn(ctx, cfg, q, k, v, cu_q, cu_k, max_q_len, out, lse=None, workspace=None, stream=None):
     """Causal attention of packed sequences over their own keys and values."""
     qs, ks = _packed(cfg, q, k, cu_q, cu_k)
     vs = _rows(v, cfg.num_kv_heads, cfg.head_dim, "v")
@@ -506,9 +513,12 @@ def starkv_prompt_attn(ctx, cfg, q, k, v, cu_q, cu_k, max_q_len, out, lse=None, 
         _need(lse, torch.float32, "lse", 2)
         if tuple(lse.shape) != tuple(q.shape[:2]):
             raise ValueError("lse must be [total_q, num_q_heads]")
-    _one_device(q, k, v, cu_q, cu_k, out, lse)
+    if workspace is not None:
+        _need(workspace, torch.uint8, "workspace", 1)
+    _one_device(q, k, v, cu_q, cu_k, out, lse, workspace)
     _check(lib().starkv_prompt_attn(ctx, _at(q), _at(k), _at(v), qs, ks, vs, _at(cu_q), _at(cu_k), cu_q.shape[0] - 1,
-                                    q.shape[0], k.shape[0], int(max_q_len), _at(out), _at(lse), _on(stream)))
+                                    q.shape[0], k.shape[0], int(max_q_len), _at(out), _at(lse), _at(workspace),
+                                    0 if workspace is None else workspace.numel(), _on(stream)))
 
 
 def starkv_prompt_weights(ctx, cfg, q, k, lse, cu_q, cu_k, max_k_len, window, weights, stream=None):
@@ -672,7 +682,9 @@ class StarKV:
         """Causal attention of packed prompts: (out [total_q, H, d], lse [total_q, H])."""
         out = _new(q, q.shape, q.dtype, stream) if out is None else out
         lse = _new(q, q.shape[:2], torch.float32, stream)
-        starkv_prompt_attn(self.ctx, self.cfg, q, k, v, cu_q, cu_k, max_q_len, out, lse, stream)
+        n = starkv_prompt_workspace_bytes(self.ctx, cu_q.shape[0] - 1, q.shape[0], k.shape[0])
+        ws = _new(q, n, torch.uint8, stream) if n else None
+        starkv_prompt_attn(self.ctx, self.cfg, q, k, v, cu_q, cu_k, max_q_len, out, lse, ws, stream)
         return out, lse
 
     def prompt_weights(self, q, k, lse, cu_q, cu_k, max_k_len: int, window: int, stream=None):

@@ -56,7 +56,8 @@ def test_a_null_context_is_refused_before_any_device_work(S):
              lambda: L.starkv_kv4_read(None, None, None, None, None, 1, 1, 1, None, None, None),
              lambda: L.starkv_kv4_decode_attn(None, None, None, None, None, 1, 1, 0, None, None, 0, None),
              lambda: L.starkv_kv4_evict(None, None, None, None, None, 0, 1, 1, None, 1, None, None, None),
-             lambda: L.starkv_prompt_attn(None, None, None, None, 0, 0, 0, None, None, 1, 1, 1, 1, None, None, None),
+             lambda: L.starkv_prompt_attn(None, None, None, None, 0, 0, 0, None, None, 1, 1, 1, 1, None, None, None, 0, None),
+             lambda: L.starkv_prompt_workspace_bytes(None, 1, 1, 1, None),
              lambda: L.starkv_prompt_weights(None, None, None, 0, 0, None, None, None, 1, 1, 1, 1, 1, None, None),
              lambda: L.starkv_kv4_layout(None, 1, None)]
     for call in calls:

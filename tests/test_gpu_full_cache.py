@@ -177,6 +177,29 @@ def test_decode_of_several_splits(shape, lens):
     check_decode(shape, lens, True, seed=len(lens))
 
 
+def test_decode_of_short_sequences_in_wide_tables():
+    """A table with room for far more pages than its sequences hold: fewer pages than the work is cut into."""
+    S = skv()
+    shape = H, h, d = 8, 2, 64
+    for lens in ([40, 3, 0, 100], [17], [0, 1]):
+        rng = np.random.default_rng(sum(lens))
+        kv = context(*shape)
+        pages, t, _ = fill(rng, lens, h, d)
+        wide = np.full((len(lens), 700), 1 << 30, np.int32)  # what lies behind a sequence's pages is not read
+        wide[:, :t.shape[1]] = t
+        qd, q = bf16(rng, len(lens), H, d)
+        cache = S.KV4Cache(kv.cfg, pages=torch.from_numpy(pages).cuda(), weights=torch.zeros((len(pages), h, 16), device="cuda"))
+        for accumulate in (False, True):
+            out = kv.kv4_decode(cache, qd, i32(wide), i32(lens), accumulate=accumulate).double().cpu().numpy()
+            assert kv.status() == 0
+            for b, n in enumerate(lens):
+                k, v = F.values(pages, F.slots_of(t[b], n), d)
+                o, _, _, mag = F.attend(q[b:b + 1].astype(np.float64), k, v, [n])
+                assert (np.abs(out[b] - o[0]) <= 2.0**-8 * np.abs(o[0]) + 2.0**-10 * (mag[0] + np.abs(v).max(initial=0))).all()
+        w = cache.weights.double().cpu().numpy()
+        assert abs(w.sum() - H * sum(n > 0 for n in lens)) < 1e-4
+
+
 def test_decode_with_scores_far_apart():
     check_decode((8, 2, 128), [400, 90], True, seed=2, q_scale=30.0)
     check_decode((8, 2, 128), [400, 90], True, seed=2, q_scale=1e-3)

@@ -95,6 +95,28 @@ def test_weights_of_a_window(window):
     run((14, 2, 64), [200, 0, 33], [260, 0, 33], window=window, seed=window)
 
 
+@pytest.mark.parametrize("shape", [(4, 4, 64), (12, 4, 128), (20, 1, 128)])
+@pytest.mark.parametrize("n_q,n_k", [([1], [3000]), ([7, 0, 1], [1500, 700, 40]), ([1100], [1100]), ([300, 20, 5], [200, 900, 600])])
+def test_prompt_whose_units_are_shared(shape, n_q, n_k):
+    """More than 1024 keys in all: key tiles of one unit on several SMs, their parts joined."""
+    run(shape, n_q, n_k, window=3, seed=n_k[0])
+
+
+def test_values_that_are_not_finite_in_a_shared_unit():
+    shape = H, h, d = 4, 2, 64
+    rng = np.random.default_rng(14)
+    kv = context(*shape)
+    q, k, v = inputs(rng, shape, [40], [1500])
+    cq, ck = i32([0, 40]), i32([0, 1500])
+    clean, lse0 = kv.prompt(q, k, v, cq, ck, 40)
+    v2 = v.clone()
+    v2[1480, 1, 9] = float("inf")  # seen from query 20 on
+    out, lse = kv.prompt(q, k, v2, cq, ck, 40)
+    assert (out[20:, 2:, 9] == float("inf")).all() and torch.equal(lse, lse0)
+    out[20:, 2:, 9], clean[20:, 2:, 9] = 0, 0
+    assert torch.equal(out, clean) and kv.status() == 0
+
+
 def test_prompt_with_scores_far_apart():
     run((8, 2, 128), [200], [200], window=200, q_scale=30.0)   # the running maximum moves often
     run((8, 2, 128), [200], [200], window=200, q_scale=1e-4)
