@@ -110,6 +110,10 @@ __device__ __forceinline__ bool elected() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
   return p != 0;
 }
+// A value that is the same in every lane, said so that the compiler knows it: loops that
+// issue products go by such values only, or their descriptors leave the uniform registers.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // D[tmem] (+)= A[tmem] * B[smem]; issued by one thread.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                            uint32_t accumulate) {
@@ -213,8 +217,9 @@ struct AttnSmem {
   static constexpr uint32_t kTileBytes = kTile * D * 2;
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr uint32_t kRing = 2 * kTileBytes;  // behind the two Q tiles: K_0, V_0, K_1, V_1, ...
-  static constexpr uint32_t kBar = kRing + kStages * kTileBytes;
-  static constexpr uint32_t kBytes = kBar + 256 + 1024;
+  static constexpr uint32_t kTold = kRing + kStages * kTileBytes;
+  static constexpr uint32_t kBar = kTold + 2 * 64;
+  static constexpr uint32_t kBytes = kBar + 384 + 1024;
 };
 
 // sum over i < n of floor((a i + b) / m), a, b >= 0, by the Euclidean steps of (a, m).
@@ -267,10 +272,10 @@ struct Pieces {
   int j0, j1, nt, kv, hb, pair;
   bool fresh;         // the next piece is another unit's
 
-  __device__ Pieces(const PromptKArgs& args, int64_t first, int64_t stop, int b_, int u_, int i_, int p_)
-      : a(args), pos(first), end(stop), b(b_), u(u_), i(i_), p(p_), fresh(false) {
+  __device__ Pieces(const PromptKArgs& args, int64_t first, int64_t stop, int b_, const int (&start)[3], const SeqSpan& span)
+      : a(args), pos(first), end(stop), b(b_), u(start[0]), i(start[1]), p(start[2]), fresh(false) {
     if (pos < end) {
-      q = span_of(a, b);
+      q = span;
       pairs = Pairs(q, a.R);
     }
   }
@@ -318,6 +323,21 @@ struct Pieces {
   __device__ int first_masked() const { return max(0, pairs.off + qbase() + 1) / kTile; }
 };
 
+// A piece as the softmax warps need it (warp 8 lays it out; two of them, in turn).
+struct __align__(16) Told {
+  int j0, stop[2];        // key tiles j0 .. stop[t] - 1 of query tile t
+  int flags;              // kTold...
+  int n, off, qbase;      // queries; query i sees keys 0 .. off + i; the pair's first query
+  int heads;              // of the head block
+  int first_masked;
+  int k0, kv_at;          // the sequence's first key row, and the KV head's first channel
+  int q_row;              // the pair's first query row
+  int head0;              // the block's first head
+  int pad[3];
+};
+static_assert(sizeof(Told) == 64, "");
+enum { kToldWhole = 1, kToldLater = 2, kToldStop = 4 };  // all of the unit; not its first tiles; no more pieces
+
 // What the join goes by: a unit that begins in this CTA and goes on behind its stretch.
 struct Cut {
   int there, last;        // 0: none; the CTA that ends the unit
@@ -335,6 +355,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   __shared__ int64_t part[kAttnThreads / 32];
   __shared__ int64_t begin[2];        // the stretch's first sequence, and the positions before it
   __shared__ int start[3];            // and its unit: u, pair, position
+  __shared__ SeqSpan first_span;
   uint8_t* sm = align1024(smem_raw);
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + SM::kBar);
   uint64_t* qfull = bar;              // both Q tiles landed
@@ -343,13 +364,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint64_t* pfull = bar + 4;          // [2][2] P_t written: its first 64 keys, the others
   uint64_t* odone = bar + 8;          // [2] a piece's products into O_t done
   uint64_t* oempty = bar + 10;        // [2] O_t read
-  uint64_t* look = bar + 12;          // one phase per masked V tile: it is there,
-  uint64_t* clean = bar + 13;         // and it has been looked over
-  uint64_t* full = bar + 14;          // [ST]
+  uint64_t* look = bar + 12;          // [4] masked V tiles, in turn: one has been asked for
+  uint64_t* clean = bar + 16;         // [4] and it has been looked over
+  uint64_t* told = bar + 20;          // [2] a piece is laid out,
+  uint64_t* heard = bar + 22;         // [2] and done with
+  uint64_t* full = bar + 24;          // [ST]
   uint64_t* empty = full + ST;        // [ST]
   uint32_t* tslot = reinterpret_cast<uint32_t*>(empty + ST);
+  Told* piece = reinterpret_cast<Told*>(sm + SM::kTold);
   int* dirty = reinterpret_cast<int*>(tslot + 1);  // a masked V tile held a value that is not finite
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
   if (warp == 9) tmem_alloc(tslot, 512);
   if (tid == 0) {
@@ -361,8 +385,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(&oempty[s], 4);
     }
     for (int s = 0; s < 4; ++s) mbar_init(&pfull[s], 4);
-    mbar_init(look, 1);
-    mbar_init(clean, 2);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&look[s], 1);
+      mbar_init(&clean[s], 2);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&told[s], 1);
+      mbar_init(&heard[s], 8);
+    }
     for (int s = 0; s < ST; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -384,6 +414,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       start[1] = i;
       start[2] = 0;
       const SeqSpan q = span_of(a, unit / units);
+      first_span = q;
       if (!q.ok) set_status(a.status, STARKV_DEV_BAD_QUERY_SPAN);
       const Pairs pairs(q, a.R);
       begin[1] = i < pairs.count ? pairs.tiles(i) + 1 : 0;
@@ -431,7 +462,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       __syncwarp();
       // its unit: the last pair that begins at or before the position, in 32 parts at a time
-      const Pairs pairs(span_of(a, (int)begin[0]), a.R);
+      const SeqSpan span = span_of(a, (int)begin[0]);
+      const Pairs pairs(span, a.R);
+      if (lane == 0) first_span = span;
       const int64_t each = pairs.before(pairs.count), in = pos - begin[1], rest = in % each;
       int lo = 0, hi = pairs.count;
       while (hi - lo > 1) {
@@ -450,15 +483,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncthreads();
   }
   tc_fence_after();
-  const uint32_t tmem = *tslot;
+  const uint32_t tmem = (uint32_t)uniform((int)*tslot);
   bool ok = true;
-  Pieces it(a, pos, end, pos < end ? (int)begin[0] : 0, start[0], start[1], start[2]);
+  Pieces it(a, pos, end, (int)begin[0], start, first_span);
 
   if (warp == 8) {
     // ---------------- copies ----------------
     if (lane == 0) {
-      int r = 0, pieces = 0;  // ring positions and pieces with keys so far
+      int r = 0, pieces = 0, all = 0, masked = 0;  // ring positions, pieces with keys, pieces, masked V tiles so far
+      auto tell = [&](const Told& x) {
+        if (!mbar_wait_short(&heard[all & 1], ((all >> 1) & 1) ^ 1)) return false;
+        piece[all & 1] = x;
+        mbar_arrive(&told[all & 1]);
+        ++all;
+        return true;
+      };
       while (ok && it.next()) {
+        ok = tell(Told{it.j0, {it.nt > 0 ? it.stop_of(0) : it.j0, it.nt > 0 ? it.stop_of(1) : it.j0},
+                       (it.whole() ? kToldWhole : 0) | (it.j0 > 0 ? kToldLater : 0), it.pairs.n, it.pairs.off, it.qbase(),
+                       min(a.gb, a.group - it.hb * a.gb), it.first_masked(), it.q.k0, it.kv * D, it.q.q0 + it.qbase(),
+                       it.kv * a.group + it.hb * a.gb, {0, 0, 0}});
+        if (!ok) break;
         if (it.nt == 0) continue;
         if (!mbar_wait_short(qempty, (pieces & 1) ^ 1)) {
           ok = false;
@@ -472,6 +517,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             tma_load_3d(sm + t * SM::kTileBytes + i * kSub, &q_map, i * 64, it.kv * a.group + it.hb * a.gb,
                         it.q.q0 + it.qbase() + t * a.R, qfull);
         ++pieces;
+        const int first_masked = it.first_masked();
         for (int e = 2 * it.j0; e < 2 * it.j1; ++e, ++r) {
           const int s = r % ST;
           if (!mbar_wait_short(&empty[s], ((r / ST) & 1) ^ 1)) {
@@ -483,8 +529,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           for (int i = 0; i < NSUB; ++i)
             tma_load_2d(sm + SM::kRing + s * SM::kTileBytes + i * kSub, e & 1 ? &v_map : &k_map, it.kv * D + i * 64,
                         it.q.k0 + (e >> 1) * kTile, &full[s]);
+          // (the ring holds four V tiles at most, so none of the four barriers is two phases ahead)
+          if ((e & 1) && (e >> 1) >= first_masked) mbar_arrive(&look[masked++ & 3]);
         }
       }
+      if (ok) ok = tell(Told{0, {0, 0}, kToldStop, 0, 0, 0, 0, 0, 0, 0, 0, 0, {0, 0, 0}});
       if (!ok) {  // wait (with a limit) for the copies in flight
         if (pieces > 0) mbar_wait(qfull, (pieces - 1) & 1, 100000000ull);
         for (int i = max(0, r - ST); i < r; ++i) mbar_wait(&full[i % ST], (i / ST) & 1, 100000000ull);
@@ -507,7 +556,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       mma_commit(&sfull[t]);
     };
-    auto all = [&](bool got) { return __all_sync(0xffffffffu, got) != 0; };
+    auto all = [&](bool got) { return uniform(__all_sync(0xffffffffu, got)) != 0; };
     // the ring's positions: a piece's next K and V tiles, each with its phase
     int kst = 0, vst = 1;
     uint32_t kph = 0, vph = 0;
@@ -518,11 +567,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ph ^= 1;
       }
     };
-    uint32_t qph = 0, looked = 0, pph[2] = {0, 0}, oph[2] = {0, 0};
-    while (ok && it.next()) {
-      if (it.nt == 0) continue;
-      const int j0 = it.j0, j1 = it.j1, first_masked = it.first_masked();
-      const int stop[2] = {it.stop_of(0), it.stop_of(1)};
+    int looked = 0;
+    uint32_t qph = 0, pph[2] = {0, 0}, oph[2] = {0, 0};
+    while (ok && uniform(it.next())) {
+      if (uniform(it.nt) == 0) continue;
+      const int j0 = uniform(it.j0), j1 = uniform(it.j1), first_masked = uniform(it.first_masked());
+      const int stop[2] = {uniform(it.stop_of(0)), uniform(it.stop_of(1))};
       ok = all(mbar_wait_short(qfull, qph) && mbar_wait_short(&full[kst], kph));
       qph ^= 1;
       if (!ok) break;
@@ -539,9 +589,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const bool more = j + 1 < j1;
         bool got = mbar_wait_short(&full[vst], vph);
         if (got && j >= first_masked) {
-          if (lane == 0) mbar_arrive(look);
-          got = mbar_wait_short(clean, looked);
-          looked ^= 1;
+          got = mbar_wait_short(&clean[looked & 3], (looked >> 2) & 1);
+          ++looked;
         }
         if (got && more) got = mbar_wait_short(&full[kst], kph);
         ok = all(got);
@@ -599,46 +648,43 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // A key that some row does not see has p = 0 there, but 0 * inf and 0 * NaN are not 0, and the
     // rows behind the sequence are another's.  So values that are not finite are cleared (rows
     // behind the sequence, whatever they hold) and, where a row does see them, added at the end.
-    int r = 0;
-    uint32_t looked = 0;
+    int r = 0, looked = 0;
     while (ok && it.next()) {
       if (it.nt == 0) continue;
-      for (int j = max(it.j0, it.first_masked()); j < it.j1; ++j) {
+      for (int j = max(it.j0, it.first_masked()); j < it.j1; ++j, ++looked) {
         const int i = r + 2 * (j - it.j0) + 1;
-        const bool got = mbar_wait_short(look, looked) && mbar_wait_short(&full[i % ST], (i / ST) & 1);
-        looked ^= 1;
+        const bool got =
+            mbar_wait_short(&look[looked & 3], (looked >> 2) & 1) && mbar_wait_short(&full[i % ST], (i / ST) & 1);
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
         }
-        uint8_t* tile = sm + SM::kRing + (i % ST) * SM::kTileBytes;
-        bool mine = false;
-        for (int e = (warp - 10) * 32 + lane; e < kTile * D / 8; e += 64) {
-          uint4* p = reinterpret_cast<uint4*>(tile) + e;
-          uint4 x = *p;
-          uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-          bool hit = false;
+        uint4* tile = reinterpret_cast<uint4*>(sm + SM::kRing + (i % ST) * SM::kTileBytes) + (warp - 10) * 32 + lane;
+        __nv_bfloat162 top = __halves2bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0));  // largest magnitude, NaN if any
+#pragma unroll 8
+        for (int e = 0; e < kTile * D / 8 / 64; ++e) {
+          const uint4 x = tile[e * 64];
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            if ((w[u] & 0x7f80u) == 0x7f80u) {
-              w[u] &= 0xffff0000u;
-              hit = true;
-            }
-            if ((w[u] & 0x7f800000u) == 0x7f800000u) {
-              w[u] &= 0x0000ffffu;
-              hit = true;
-            }
-          }
-          if (hit) {
-            *p = x;
-            mine = true;
-          }
+          for (int u = 0; u < 4; ++u) top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[u])));
         }
-        if (mine) *reinterpret_cast<volatile int*>(dirty) = 1;
+        if (!isfinite(__low2float(top)) || !isfinite(__high2float(top))) {
+          for (int e = 0; e < kTile * D / 8 / 64; ++e) {
+            uint4 x = tile[e * 64];
+            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              if ((w[u] & 0x7f80u) == 0x7f80u) w[u] &= 0xffff0000u;
+              if ((w[u] & 0x7f800000u) == 0x7f800000u) w[u] &= 0x0000ffffu;
+            }
+            tile[e * 64] = x;
+          }
+          *reinterpret_cast<volatile int*>(dirty) = 1;
+        }
         __threadfence_block();
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(clean);
+        if (lane == 0) mbar_arrive(&clean[looked & 3]);
       }
       r += 2 * (it.j1 - it.j0);
     }
@@ -650,12 +696,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ts = trow + t * kTile, to = trow + 256 + t * kTile;
     uint32_t sph = 0, oph = 0;
-    while (ok && it.next()) {
-      const int qi = it.qbase() + row_q;
-      const int heads = min(a.gb, a.group - it.hb * a.gb);
-      const bool live = r < a.R * a.gb && qi < it.pairs.n && hh < heads;
-      const int seen = live ? it.pairs.off + qi + 1 : 1 << 30;  // keys the row sees (may be <= 0); a row of nothing masks nothing
-      const int j0 = it.j0, stop = it.nt > 0 ? it.stop_of(t) : j0;
+    const bool in_tile = r < a.R * a.gb;
+    for (int n = 0;; ++n) {
+      if (!__all_sync(0xffffffffu, mbar_wait_short(&told[n & 1], (n >> 1) & 1))) {
+        ok = false;
+        break;
+      }
+      const Told& x = piece[n & 1];
+      if (x.flags & kToldStop) break;
+      const bool live = in_tile && x.qbase + row_q < x.n && hh < x.heads;
+      // keys the row sees (may be <= 0); a row of nothing masks nothing
+      const int seen = live ? x.off + x.qbase + row_q + 1 : 1 << 30;
+      const int j0 = x.j0, stop = x.stop[t];
       float m = -INFINITY, l = 0.f;
       for (int j = j0; j < stop; ++j) {
         if (!__all_sync(0xffffffffu, mbar_wait_short(&sfull[t], sph))) {
@@ -664,25 +716,36 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         sph ^= 1;
         tc_fence_after();
-        float sv[kTile];
-        {
-          uint32_t(&raw)[kTile] = *reinterpret_cast<uint32_t(*)[kTile]>(sv);
+        // four quarters of the row's scores; the last is let go after the maximum and loaded again when the
+        // first has been used up (all four beside P's words are more registers than a thread has)
+        uint32_t sv[4][32];
 #pragma unroll
-          for (int c = 0; c < kTile / 32; ++c) tmem_ld32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&raw[c * 32]));
-          tmem_ld_wait();
-        }
+        for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, sv[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_wait32(sv[c]);
         const int lim = seen - j * kTile;
-        if (__any_sync(0xffffffffu, lim < kTile)) {
+        // the quarters from this one on hold keys that some row of the warp does not see
+        const int whole_quarters = (int)__reduce_min_sync(0xffffffffu, (uint32_t)min(max(lim, 0), kTile)) >> 5;
+        auto mask = [&](uint32_t (&y)[32], int c) {
 #pragma unroll
-          for (int c = 0; c < kTile; ++c) sv[c] = c < lim ? sv[c] : -INFINITY;
+          for (int u = 0; u < 32; ++u) y[u] = c * 32 + u < lim ? y[u] : 0xff800000u;
+        };
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c >= whole_quarters) mask(sv[c], c);
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          auto at = [&](int u) { return __uint_as_float(sv[c][u]); };
+          float y[2] = {max3(at(0), at(1), at(2)), max3(at(3), at(4), at(5))};
+#pragma unroll
+          for (int u = 6; u < 30; u += 4) {
+            y[0] = max3(y[0], at(u), at(u + 1));
+            y[1] = max3(y[1], at(u + 2), at(u + 3));
+          }
+          mx[c] = max3(fmaxf(at(30), at(31)), y[0], y[1]);
         }
-        float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
-#pragma unroll
-        for (int c = 4; c < kTile - 4; c += 8)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], sv[c + u], sv[c + 4 + u]);
-        const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], sv[kTile - 4], sv[kTile - 3]),
-                               fmaxf(sv[kTile - 2], sv[kTile - 1]));
+        const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
         const bool move = live && (top - m) * a.scale_log2 > kMoveMax;  // m = -inf: true but for a row without scores
         if (__any_sync(0xffffffffu, move)) {
           if (j > j0) {
@@ -703,14 +766,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const float base = m == -INFINITY ? 0.f : -m * a.scale_log2;
         const f32x2 scale2 = pair(a.scale_log2, a.scale_log2), base2 = pair(base, base);
         f32x2 sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-        // four quarters; the first half of P goes on its way while the third quarter is computed
+        // the first half of P goes on its way while the third quarter is computed
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t w[16];
+          if (c == 1) tmem_ld32(ts + 96, sv[3]);
+          if (c == 3) {
+            tmem_ld_wait32(sv[3]);
+            if (whole_quarters < 4) mask(sv[3], 3);
+          }
 #pragma unroll
           for (int u = 0; u < 16; ++u) {
-            const f32x2 x = fma2(pair(sv[c * 32 + 2 * u], sv[c * 32 + 2 * u + 1]), scale2, base2);
-            const f32x2 p = on_fma_pipe(u) ? ex2_fma(x) : ex2_sfu(x);
+            const f32x2 z = fma2(pair(__uint_as_float(sv[c][2 * u]), __uint_as_float(sv[c][2 * u + 1])), scale2, base2);
+            const f32x2 p = on_fma_pipe(u) ? ex2_fma(z) : ex2_sfu(z);
             sum[u & 1] = add2(sum[u & 1], p);
             const float2 y = unpair(p);
             w[u] = pack_bf2(y.x, y.y);
@@ -741,10 +809,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         oph ^= 1;
         tc_fence_after();
       }
-      const bool whole = it.whole();
+      const bool whole = x.flags & kToldWhole;
       const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-      const int64_t row = (int64_t)(it.q.q0 + qi) * a.H + it.kv * a.group + it.hb * a.gb + hh;
-      const int64_t slot = ((int64_t)blockIdx.x * 2 + (j0 == 0)) * 2 * kTile + t * kTile + r;
+      const int64_t row = (int64_t)(x.q_row + row_q) * a.H + x.head0 + hh;
+      const int64_t slot = ((int64_t)blockIdx.x * 2 + (x.flags & kToldLater ? 0 : 1)) * 2 * kTile + t * kTile + r;
       const bool fix = any && *reinterpret_cast<volatile int*>(dirty) != 0;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -764,12 +832,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         if (!live) continue;
         if (fix)
-          for (int j = max(it.first_masked(), j0) * kTile; j < min(seen, stop * kTile); ++j) {
-            const __nv_bfloat16* vr = a.v + (int64_t)(it.q.k0 + j) * a.v_stride + it.kv * D + c * 32;
+          for (int j = max(x.first_masked, j0) * kTile; j < min(seen, stop * kTile); ++j) {
+            const __nv_bfloat16* vr = a.v + (int64_t)(x.k0 + j) * a.v_stride + x.kv_at + c * 32;
 #pragma unroll
             for (int u = 0; u < 32; ++u) {
-              const float x = __bfloat162float(vr[u]);
-              if (!isfinite(x)) o[u] = __float_as_uint(__uint_as_float(o[u]) + x);
+              const float y = __bfloat162float(vr[u]);
+              if (!isfinite(y)) o[u] = __float_as_uint(__uint_as_float(o[u]) + y);
             }
           }
         if (whole) {
@@ -778,8 +846,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           for (int u = 0; u < 4; ++u) {
             uint32_t w[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              w[x] = pack_bf2(__uint_as_float(o[8 * u + 2 * x]) * inv, __uint_as_float(o[8 * u + 2 * x + 1]) * inv);
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack_bf2(__uint_as_float(o[8 * u + 2 * e]) * inv, __uint_as_float(o[8 * u + 2 * e + 1]) * inv);
             dst[u] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
@@ -790,6 +858,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       if (live && whole && a.lse) a.lse[row] = l == 0.f ? -INFINITY : fmaf(m, a.scale, logf(l));
       if (live && !whole) a.part_ml[slot] = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&heard[n & 1]);
     }
   }
   if (!ok && lane == 0) set_status(a.status, kDevWaitTimeout);
@@ -803,7 +873,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // the unit that goes on behind the stretch, if its first key tiles are here: the last piece's
     Cut c = {0, 0, 0, 0, 0, 0};
     if (pos < end) {
-      Pieces last(a, pos, end, (int)begin[0], start[0], start[1], start[2]);
+      Pieces last(a, pos, end, (int)begin[0], start, first_span);
       bool any = false;
       int64_t unit_end = 0;
       while (last.next()) {
@@ -1002,7 +1072,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   int* last = reinterpret_cast<int*>(sm + SM::kCols + ST * kTile * 4);
   float* other = reinterpret_cast<float*>(sm + SM::kSums);
   Note* notes = reinterpret_cast<Note*>(sm + SM::kNotes);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int split = a.mode > 1 ? a.mode : 1;
   const int rank = a.mode > 1 ? blockIdx.x % a.mode : 0;  // (clusters are consecutive blocks)
 
@@ -1095,7 +1165,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     seq = (int)begin[0];
     before = begin[1];
   }
-  const uint32_t tmem = *tslot;
+  const uint32_t tmem = (uint32_t)uniform((int)*tslot);
   const bool resident = a.mode == kResident;
   bool ok = true;
   Items it(a, pos, end, seq, before);
@@ -1155,19 +1225,19 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     const uint64_t kd = make_sdesc(smem_u32(sm), 16, 1024, 2), qd = make_sdesc(smem_u32(sm + SM::kRing), 16, 1024, 2);
     int u = 0, ks = 0, st = 0;  // steps so far, the K ring's next tile, the Q ring's (streamed)
     uint32_t kph = 0, sph = 0;
-    bool more = it.next();
+    bool more = uniform(it.next());
     while (ok && more) {
-      const int steps = it.steps;
-      more = it.next();
+      const int steps = uniform(it.steps);
+      more = uniform(it.next());
       if (steps == 0) continue;
-      const bool free_q = !resident || !more || it.fresh;  // resident: the Q tiles' last use
-      ok = __all_sync(0xffffffffu, mbar_wait_short(&kfull[ks], kph));
+      const bool free_q = uniform(!resident || !more || it.fresh);  // resident: the Q tiles' last use
+      ok = uniform(__all_sync(0xffffffffu, mbar_wait_short(&kfull[ks], kph)));
       const uint64_t k0 = desc_at(kd, ks * SM::kTileBytes);
       int v = rank;
       for (; ok && v < steps; v += split, ++u) {
         const int s = resident ? v : st, w = u & 3;
         const uint32_t ph = resident ? (flips >> v) & 1u : sph;
-        ok = __all_sync(0xffffffffu, mbar_wait_short(&full[s], ph) && mbar_wait_short(&sempty[w], ((u >> 2) & 1) ^ 1));
+        ok = uniform(__all_sync(0xffffffffu, mbar_wait_short(&full[s], ph) && mbar_wait_short(&sempty[w], ((u >> 2) & 1) ^ 1)));
         if (!ok) break;
         tc_fence_after();
         if (lead) {
