@@ -716,6 +716,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         sph ^= 1;
         tc_fence_after();
+        // masked keys (last tiles only): -inf takes their scores' place in TMEM, a quarter at a time in one
+        // rolled loop, so that the code of the other tiles stays short (it is bound by its fetch, too)
+        const int lim = seen - j * kTile;
+        if (__any_sync(0xffffffffu, lim < kTile)) {
+#pragma unroll 1
+          for (int c = 0; c < kTile; c += 32) {
+            if (!__any_sync(0xffffffffu, lim < c + 32)) continue;
+            uint32_t y[32];
+            tmem_ld32(ts + c, y);
+            tmem_ld_wait32(y);
+#pragma unroll
+            for (int u = 0; u < 32; ++u) y[u] = u < lim - c ? y[u] : 0xff800000u;
+            tmem_st32(ts + c, y);
+          }
+          tmem_st_wait();
+        }
         // four quarters of the row's scores; the last is let go after the maximum and loaded again when the
         // first has been used up (all four beside P's words are more registers than a thread has)
         uint32_t sv[4][32];
@@ -723,16 +739,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, sv[c]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_wait32(sv[c]);
-        const int lim = seen - j * kTile;
-        // the quarters from this one on hold keys that some row of the warp does not see
-        const int whole_quarters = (int)__reduce_min_sync(0xffffffffu, (uint32_t)min(max(lim, 0), kTile)) >> 5;
-        auto mask = [&](uint32_t (&y)[32], int c) {
-#pragma unroll
-          for (int u = 0; u < 32; ++u) y[u] = c * 32 + u < lim ? y[u] : 0xff800000u;
-        };
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (c >= whole_quarters) mask(sv[c], c);
         float mx[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -771,10 +777,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int c = 0; c < 4; ++c) {
           uint32_t w[16];
           if (c == 1) tmem_ld32(ts + 96, sv[3]);
-          if (c == 3) {
-            tmem_ld_wait32(sv[3]);
-            if (whole_quarters < 4) mask(sv[3], 3);
-          }
+          if (c == 3) tmem_ld_wait32(sv[3]);
 #pragma unroll
           for (int u = 0; u < 16; ++u) {
             const f32x2 z = fma2(pair(__uint_as_float(sv[c][2 * u]), __uint_as_float(sv[c][2 * u + 1])), scale2, base2);
