@@ -238,12 +238,13 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadArgs a)
 //
 // Each token that may go gets a 32-bit key that orders like its weight (NaN below all).
 // The threads hold the keys in registers (eight tokens of each stretch of 8192 a thread,
-// four stretches; keys of tokens beyond 32768 are read again each time) and find the
-// largest threshold that `need` keys reach bit by bit, from the first bit in which the
-// keys differ: a count in registers, a warp's and a block's sum, one barrier a bit, and
-// an early end where exactly `need` reach it.  (A histogram of digits took three passes,
-// but weights share few leading digits: its atomics on few counters cost 3 times as much.)
-// One ordered pass then lists the tokens above the threshold and the first equal to it.
+// four stretches; keys of tokens beyond 32768 are read again each time).  The threshold,
+// the need-th largest key, is found by counts in 2048 equal bins of the range that is left:
+// all of [least, largest] first, then the bin that holds it, until a bin is one key or
+// ends exactly at the need-th (three passes at most, two for most weights).  Bins of the
+// range, not leading digits: weights share their exponents' digits, and counts of few bins
+// queue up.  (A search bit by bit took 33 us for 256 lists of 4096 .. 8192.)
+// One ordered pass then lists the keys above the threshold and the first equal to it.
 // ---------------------------------------------------------------------------
 struct EvictArgs {
   const int32_t* block_table;
@@ -260,6 +261,7 @@ struct EvictArgs {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelEach = 8;                            // tokens of a thread in a stretch
+constexpr int kBins = 2048;                            // two a thread
 constexpr int kStretch = kSelThreads * kSelEach;
 constexpr int kHeld = 4;                               // stretches whose keys stay in registers
 
@@ -271,11 +273,15 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 __global__ void __launch_bounds__(kSelThreads, 1) kv4_select_kernel(const EvictArgs a) {
+  __shared__ uint32_t bins[kBins];
   __shared__ uint32_t wsum[2][32];
   __shared__ uint32_t ends[2][32];
+  __shared__ uint32_t found[3];  // bin of the threshold, keys above the bin, keys in it
   __shared__ unsigned bad;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int head = blockIdx.x, b = blockIdx.y;
+  if (tid == 0) bad = 0;
+  __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
   const int n = a.seq_lens[b];
@@ -283,20 +289,43 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv4_select_kernel(const EvictA
   const int cap = a.dst_max_pages * kPage;
   int32_t* kept = a.kept + ((int64_t)b * a.pool.h_kv + head) * cap;
   const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
-  if (tid == 0) bad = 0;
-  __syncthreads();
   const int keep = min(n, want);
-  if (n < 0 || want < 0 || n > a.max_pages * kPage || keep > cap) {
+  const bool sane = n >= 0 && want >= 0 && n <= a.max_pages * kPage && keep <= cap;
+  const int recent = min(a.recent, keep);
+  const int old = sane ? n - recent : 0;     // tokens that may go
+  const int need = keep - recent;            // how many of them stay
+  auto check = [&](int64_t p) {
+    if (p >= 0 && p < a.pool.n_pages) return true;
+    atomicOr(&bad, STARKV_DEV_BAD_PAGE);
+    return false;
+  };
+  // keys of tokens i0 .. i0 + 7 (one page's half: 32 contiguous bytes); the page is the caller's to check
+  auto keys_of = [&](int64_t p, int i0, uint32_t (&k)[kSelEach]) {
+    const float4* w = reinterpret_cast<const float4*>(a.pool.weights + (p * a.pool.h_kv + head) * kPage + i0 % kPage);
+    const float4 x = w[0], y = w[1];
+    const float v[kSelEach] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int e = 0; e < kSelEach; ++e) k[e] = i0 + e < old ? weight_key(v[e]) : 0u;
+  };
+  uint32_t held[kHeld][kSelEach];
+#pragma unroll
+  for (int g = 0; g < kHeld; ++g) {
+#pragma unroll
+    for (int e = 0; e < kSelEach; ++e) held[g][e] = 0;
+  }
+  if (!sane) {
     if (tid == 0) bad = STARKV_DEV_BAD_SEQ_LEN;
   } else {
-    for (int i = tid; i < (n + kPage - 1) / kPage; i += kSelThreads) {
-      const int64_t p = table[i];
-      if (p < 0 || p >= a.pool.n_pages) atomicOr(&bad, STARKV_DEV_BAD_PAGE);
+    for (int i = tid; i < (keep + kPage - 1) / kPage; i += kSelThreads)
+      check(a.dst_table[(int64_t)b * a.dst_max_pages + i]);
+#pragma unroll
+    for (int g = 0; g < kHeld; ++g) {
+      const int i0 = g * kStretch + tid * kSelEach;
+      if (i0 >= n) continue;
+      const int64_t p = table[i0 / kPage];
+      if (check(p) && need > 0 && keep < n && i0 < old) keys_of(p, i0, held[g]);
     }
-    for (int i = tid; i < (keep + kPage - 1) / kPage; i += kSelThreads) {
-      const int64_t p = a.dst_table[(int64_t)b * a.dst_max_pages + i];
-      if (p < 0 || p >= a.pool.n_pages) atomicOr(&bad, STARKV_DEV_BAD_PAGE);
-    }
+    for (int i0 = kHeld * kStretch + tid * kSelEach; i0 < n; i0 += kStretch) check(table[i0 / kPage]);
   }
   __syncthreads();
   if (bad || keep <= 0) {
@@ -309,44 +338,30 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv4_select_kernel(const EvictA
     for (int i = tid; i < n; i += kSelThreads) kept[i] = i;
     return;
   }
-  const int recent = min(a.recent, keep);
-  const int old = n - recent;                // tokens that may go
-  uint32_t need = (uint32_t)(keep - recent); // how many of them stay
   for (int i = tid; i < recent; i += kSelThreads) kept[need + i] = old + i;
   if (need == 0) return;
-  // keys of tokens i0 .. i0 + 7 (one page's half: 32 contiguous bytes)
-  auto keys_at = [&](int i0, uint32_t (&k)[kSelEach]) {
+  // f(key) of every key that may go
+  auto each = [&](auto&& f) {
 #pragma unroll
-    for (int e = 0; e < kSelEach; ++e) k[e] = 0;
-    if (i0 >= old) return;
-    const int64_t p = table[i0 / kPage];
-    const float4* w = reinterpret_cast<const float4*>(a.pool.weights + (p * a.pool.h_kv + head) * kPage + i0 % kPage);
-    const float4 x = w[0], y = w[1];
-    const float v[kSelEach] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    for (int g = 0; g < kHeld; ++g)
+      if (g * kStretch < old) {
 #pragma unroll
-    for (int e = 0; e < kSelEach; ++e)
-      if (i0 + e < old) k[e] = weight_key(v[e]);
-  };
-  uint32_t held[kHeld][kSelEach];
-#pragma unroll
-  for (int g = 0; g < kHeld; ++g) keys_at(g * kStretch + tid * kSelEach, held[g]);
-  // smallest and largest key: their common leading bits are the threshold's
-  uint32_t lo = 0xffffffffu, hi = 0;
-  auto span = [&](int i0, const uint32_t (&k)[kSelEach]) {
-#pragma unroll
-    for (int e = 0; e < kSelEach; ++e)
-      if (i0 + e < old) {
-        lo = min(lo, k[e]);
-        hi = max(hi, k[e]);
+        for (int e = 0; e < kSelEach; ++e)
+          if (g * kStretch + tid * kSelEach + e < old) f(held[g][e]);
       }
-  };
+    for (int i0 = kHeld * kStretch + tid * kSelEach; i0 < old; i0 += kStretch) {
+      uint32_t k[kSelEach];
+      keys_of(table[i0 / kPage], i0, k);
 #pragma unroll
-  for (int g = 0; g < kHeld; ++g) span(g * kStretch + tid * kSelEach, held[g]);
-  for (int i0 = kHeld * kStretch + tid * kSelEach; i0 < old; i0 += kStretch) {
-    uint32_t k[kSelEach];
-    keys_at(i0, k);
-    span(i0, k);
-  }
+      for (int e = 0; e < kSelEach; ++e)
+        if (i0 + e < old) f(k[e]);
+    }
+  };
+  uint32_t lo = 0xffffffffu, hi = 0;
+  each([&](uint32_t k) {
+    lo = min(lo, k);
+    hi = max(hi, k);
+  });
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
   if (lane == 0) {
@@ -356,42 +371,52 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv4_select_kernel(const EvictA
   __syncthreads();
   lo = __reduce_min_sync(0xffffffffu, ends[0][lane]);
   hi = __reduce_max_sync(0xffffffffu, ends[1][lane]);
-  const int bits = lo == hi ? 0 : 32 - __clz(lo ^ hi);
-  uint32_t threshold = bits == 32 ? 0u : hi >> bits << bits;  // at least `need` keys reach it
-  uint32_t above_all = 0;  // keys above the threshold, once it is found
-  bool exact = false;
-#pragma unroll 1
-  for (int bit = bits - 1; bit >= 0; --bit) {
-    const uint32_t t = threshold | (1u << bit);
-    uint32_t c = 0;
+  // keys above the range [lo, hi] stay; `left` of the keys in it do
+  uint32_t left = (uint32_t)need;
+  uint32_t threshold;
+  while (true) {
+    const uint32_t width = hi - lo;
+    const int shift = max(0, 32 - __clz(width) - 11);  // width >> shift < 2048
+    bins[tid] = 0;
+    bins[tid + kSelThreads] = 0;
+    __syncthreads();
+    each([&](uint32_t k) {
+      if (k - lo <= width) atomicAdd(&bins[(k - lo) >> shift], 1u);
+    });
+    __syncthreads();
+    // thread i owns the two bins 2 i, 2 i + 1 counted from the top: find the one that holds the left-th key
+    const uint32_t top = kBins - 1 - 2 * tid;
+    const uint32_t c0 = bins[top], c1 = bins[top - 1];
+    uint32_t inc = c0 + c1;
 #pragma unroll
-    for (int g = 0; g < kHeld; ++g)
-      if (g * kStretch < old) {
-#pragma unroll
-        for (int e = 0; e < kSelEach; ++e) c += held[g][e] >= t;
-      }
-    for (int i0 = kHeld * kStretch + tid * kSelEach; i0 < old; i0 += kStretch) {
-      uint32_t k[kSelEach];
-      keys_at(i0, k);
-#pragma unroll
-      for (int e = 0; e < kSelEach; ++e) c += k[e] >= t;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
     }
-    c = __reduce_add_sync(0xffffffffu, c);
-    if (lane == 0) wsum[bit & 1][warp] = c;
-    __syncthreads();  // (the other buffer was read before the last barrier)
-    c = __reduce_add_sync(0xffffffffu, wsum[bit & 1][lane]);
-    if (c >= need) threshold = t;
-    else above_all = c;
-    if (c == need) {
-      exact = true;  // exactly the keys that reach it stay
+    if (lane == 31) wsum[0][warp] = inc;
+    __syncthreads();
+    const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[0][lane] : 0u) + inc - c0 - c1;
+    if (before < left && left <= before + c0 + c1) {
+      const bool upper = left <= before + c0;
+      found[0] = upper ? top : top - 1;
+      found[1] = upper ? before : before + c0;
+      found[2] = upper ? c0 : c1;
+    }
+    __syncthreads();
+    left -= found[1];
+    lo += found[0] << shift;
+    if (left == found[2]) {  // all of the bin's keys stay
+      threshold = lo - 1;    // (lo > 0: fewer than all keys stay)
+      left = 0;
       break;
     }
+    if (shift == 0) {
+      threshold = lo;
+      break;
+    }
+    hi = lo + ((1u << shift) - 1);
   }
-  if (exact) {
-    threshold -= 1;
-    above_all = need;
-  }
-  const uint32_t equals = need - above_all;  // of the keys equal to the threshold, the first so many stay
+  const uint32_t equals = left;  // of the keys equal to the threshold, the first so many stay
   // the ordered list: a stretch at a time, each thread behind the threads before it
   uint32_t base = 0, base_eq = 0;
   auto list = [&](int i0, const uint32_t (&k)[kSelEach], int turn) {
@@ -430,26 +455,84 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv4_select_kernel(const EvictA
   for (int g = 0; g < kHeld; ++g)
     if (g * kStretch < old) list(g * kStretch + tid * kSelEach, held[g], g);
   for (int g = kHeld; g * kStretch < old; ++g) {
-    uint32_t k[kSelEach];
-    keys_at(g * kStretch + tid * kSelEach, k);
+    uint32_t k[kSelEach] = {};
+    const int i0 = g * kStretch + tid * kSelEach;
+    if (i0 < old) keys_of(table[i0 / kPage], i0, k);
     list(g * kStretch + tid * kSelEach, k, g);
   }
 }
 
 // ---------------------------------------------------------------------------
-// Eviction, step 2: gather the kept tokens' rows.  One warp fills one (destination
-// page, KV head): all its loads are issued before the first store.
+// Eviction, step 2: gather the kept tokens' rows.  A warp fills kMovePages (destination
+// page, KV head)s: all their source slots are looked up first, and a page's rows are asked
+// for before the page before it is stored, so that the chain of dependent loads (kept index,
+// page, rows) is waited for once in four pages.
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 128;
+constexpr int kMovePages = 4;
+
+template <int D>
+struct MoveRows {
+  using P = Kv4<D>;
+  static constexpr int kChunks = P::kRow / 16;       // 16-byte pieces of a token's codes: 4 or 2
+  static constexpr int kPer = kPage * kChunks / 32;  // pieces a lane moves, K or V: 2 or 1
+  uint4 codes[2][kPer];
+  uint32_t meta[P::kGroups];
+  float w;
+  uint32_t have;  // tokens of the page that are there
+
+  // from: lane t's source slot of token t (-1: none)
+  __device__ __forceinline__ void load(const Kv4Pool& pool, int head, int64_t from, int lane) {
+    have = __ballot_sync(0xffffffffu, from >= 0) & 0xffffu;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int64_t src = __shfl_sync(0xffffffffu, from, (i * 32 + lane) / kChunks);
+      if (src < 0) continue;
+      const uint8_t* base = pool.pages + (src / kPage * pool.h_kv + head) * (int64_t)P::kBytes +
+                            (src % kPage) * P::kRow + (lane % kChunks) * 16;
+      codes[0][i] = *reinterpret_cast<const uint4*>(base);
+      codes[1][i] = *reinterpret_cast<const uint4*>(base + P::kV);
+    }
+    // lanes 0..15 move the K metadata, 16..31 the V metadata of token lane % 16
+    const int64_t src = __shfl_sync(0xffffffffu, from, lane & 15);
+    if (src < 0) return;
+    const int64_t ph = src / kPage * pool.h_kv + head;
+    const uint8_t* m = pool.pages + ph * (int64_t)P::kBytes + (lane < 16 ? P::kKMeta : P::kVMeta) + (src % kPage) * P::kMetaRow;
+    if constexpr (P::kGroups == 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(m);
+      meta[0] = x.x, meta[1] = x.y, meta[2] = x.z, meta[3] = x.w;
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(m);
+      meta[0] = x.x, meta[1] = x.y;
+    }
+    if (lane < 16) w = pool.weights[ph * kPage + src % kPage];
+  }
+
+  __device__ __forceinline__ void store(const Kv4Pool& pool, int head, int64_t page, int lane) const {
+    uint8_t* to = pool.pages + (page * pool.h_kv + head) * (int64_t)P::kBytes;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int t = (i * 32 + lane) / kChunks;
+      if (!(have >> t & 1)) continue;
+      uint8_t* base = to + t * P::kRow + (lane % kChunks) * 16;
+      *reinterpret_cast<uint4*>(base) = codes[0][i];
+      *reinterpret_cast<uint4*>(base + P::kV) = codes[1][i];
+    }
+    if (!(have >> (lane & 15) & 1)) return;
+    uint8_t* m = to + (lane < 16 ? P::kKMeta : P::kVMeta) + (lane & 15) * P::kMetaRow;
+    if constexpr (P::kGroups == 4)
+      *reinterpret_cast<uint4*>(m) = make_uint4(meta[0], meta[1], meta[2], meta[3]);
+    else
+      *reinterpret_cast<uint2*>(m) = make_uint2(meta[0], meta[1]);
+    if (lane < 16) pool.weights[(page * pool.h_kv + head) * kPage + lane] = w;
+  }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) kv4_move_kernel(const EvictArgs a) {
-  using P = Kv4<D>;
-  constexpr int kChunks = P::kRow / 16;             // 16-byte pieces of a token's codes: 4 or 2
-  constexpr int kPer = kPage * kChunks / 32;        // pieces a lane moves, K or V: 2 or 1
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.z, head = blockIdx.y;
-  const int page = blockIdx.x * (kMoveThreads / 32) + warp;
+  const int page0 = (blockIdx.x * (kMoveThreads / 32) + warp) * kMovePages;
   pdl_wait();
   pdl_launch_dependents();
   const int cap = a.dst_max_pages * kPage;
@@ -463,52 +546,25 @@ __global__ void __launch_bounds__(kMoveThreads) kv4_move_kernel(const EvictArgs 
     }
     a.new_lens[b] = lo;
   }
-  if (page >= a.dst_max_pages) return;
-  const int mine = lane < kPage ? kept[page * kPage + lane] : -1;
-  if (!__any_sync(0xffffffffu, mine >= 0)) return;
-  int64_t from = -1;  // lane t: source of token t as page * 16 + offset
-  if (mine >= 0) from = (int64_t)a.block_table[(int64_t)b * a.max_pages + mine / kPage] * kPage + mine % kPage;
-  uint8_t* to = a.pool.pages +
-                ((int64_t)a.dst_table[(int64_t)b * a.dst_max_pages + page] * a.pool.h_kv + head) * (int64_t)P::kBytes;
-  uint4 codes[2][kPer];
-  int64_t src[kPer];
+  // lane 16 h + t: source slots of tokens t of pages page0 + h and page0 + 2 + h
+  int64_t from[kMovePages / 2];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int t = (i * 32 + lane) / kChunks;
-    src[i] = __shfl_sync(0xffffffffu, from, t);
-    if (src[i] < 0) continue;
-    const uint8_t* base = a.pool.pages + (src[i] / kPage * a.pool.h_kv + head) * (int64_t)P::kBytes +
-                          (src[i] % kPage) * P::kRow + (lane % kChunks) * 16;
-    codes[0][i] = *reinterpret_cast<const uint4*>(base);
-    codes[1][i] = *reinterpret_cast<const uint4*>(base + P::kV);
+  for (int i = 0; i < kMovePages / 2; ++i) {
+    const int at = (page0 + 2 * i) * kPage + lane;
+    const int mine = at < cap ? kept[at] : -1;
+    from[i] = mine < 0 ? -1 : (int64_t)a.block_table[(int64_t)b * a.max_pages + mine / kPage] * kPage + mine % kPage;
   }
-  // lanes 0..15 move the K metadata, 16..31 the V metadata of token lane % 16
-  const int64_t msrc = __shfl_sync(0xffffffffu, from, lane & 15);
-  const int moff = lane < 16 ? P::kKMeta : P::kVMeta;
-  uint32_t meta[P::kGroups];
-  float w = 0.f;
-  if (msrc >= 0) {
-    const int64_t ph = msrc / kPage * a.pool.h_kv + head;
-    const uint32_t* m = reinterpret_cast<const uint32_t*>(a.pool.pages + ph * (int64_t)P::kBytes + moff +
-                                                          (msrc % kPage) * P::kMetaRow);
+  int64_t to = -1;  // lane i: destination page page0 + i
+  if (lane < kMovePages && page0 + lane < a.dst_max_pages && kept[(page0 + lane) * kPage] >= 0)
+    to = a.dst_table[(int64_t)b * a.dst_max_pages + page0 + lane];
+  MoveRows<D> rows[2];
+  auto of_page = [&](int i) { return __shfl_sync(0xffffffffu, from[i >> 1], (i & 1) * 16 + (lane & 15)); };
+  rows[0].load(a.pool, head, of_page(0), lane);
 #pragma unroll
-    for (int i = 0; i < P::kGroups; ++i) meta[i] = m[i];
-    if (lane < 16) w = a.pool.weights[ph * kPage + msrc % kPage];
-  }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (src[i] < 0) continue;
-    const int e = i * 32 + lane;
-    uint8_t* base = to + (e / kChunks) * P::kRow + (lane % kChunks) * 16;
-    *reinterpret_cast<uint4*>(base) = codes[0][i];
-    *reinterpret_cast<uint4*>(base + P::kV) = codes[1][i];
-  }
-  if (msrc >= 0) {
-    uint32_t* m = reinterpret_cast<uint32_t*>(to + moff + (lane & 15) * P::kMetaRow);
-#pragma unroll
-    for (int i = 0; i < P::kGroups; ++i) m[i] = meta[i];
-    if (lane < 16)
-      a.pool.weights[((int64_t)a.dst_table[(int64_t)b * a.dst_max_pages + page] * a.pool.h_kv + head) * kPage + lane] = w;
+  for (int i = 0; i < kMovePages; ++i) {
+    if (i + 1 < kMovePages) rows[(i + 1) & 1].load(a.pool, head, of_page(i + 1), lane);
+    const int64_t page = __shfl_sync(0xffffffffu, to, i);
+    if (page >= 0) rows[i & 1].store(a.pool, head, page, lane);
   }
 }
 
@@ -562,7 +618,7 @@ cudaError_t launch_kv4_evict(const Ctx& c, const starkv_kv4_cache& cache, const 
               pool_of(c, cache), c.status};
   cudaError_t e = launch_chained(kv4_select_kernel, dim3(c.cfg.num_kv_heads, batch), dim3(kSelThreads), 0, s, 1u, a);
   if (e != cudaSuccess) return e;
-  const int per = kMoveThreads / 32;
+  const int per = kMoveThreads / 32 * kMovePages;
   return launch_chained(c.cfg.head_dim == 64 ? kv4_move_kernel<64> : kv4_move_kernel<128>,
                         dim3((dst_max_pages + per - 1) / per, c.cfg.num_kv_heads, batch), dim3(kMoveThreads), 0, s, 1u,
                         a);

@@ -206,7 +206,12 @@ __device__ __forceinline__ int64_t cta_of(int64_t x, int64_t total, int ctas) {
 //   that P_t V_(j-1) is, so no further barrier guards that.  The next unit's Q and first
 //   products run while the softmax warps write the last unit out.
 constexpr int kAttnThreads = 384;
-constexpr int kFewKeys = 1024;    // at most this many keys in all: a CTA takes a whole unit
+// A CTA takes a whole unit where there are at most kFewKeys keys in all (256 tokens: 10.1 us, 13.4 us cut
+// and joined), and where there are units for all SMs and the keys and values do not stay in L2: units
+// that start together then read the same tiles together, stretches do not (32768 keys of 32 heads: 1060 us
+// and 1178 us, for 65% and 26% of hits in L2; sixteen prompts that fit: 298 us and 291 us).
+constexpr int kFewKeys = 1024;
+constexpr int64_t kMostCached = (int64_t)96 << 20;  // bytes of keys and values
 constexpr int kLeastTiles = 2;    // key tiles of a stretch, where there are few
 // Pairs of exponentials that go to the FMA pipe: one of eight.  (2048 queries over 32768 keys: none
 // 914 us, one of eight 894, one of four 982, half 1070: the softmax warps' issue slots bound them too.)
@@ -1570,6 +1575,7 @@ PromptPlan plan_prompt(const Ctx& c, int batch, int64_t total_q, int64_t total_k
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c.device);
   // at most so many pairs of query tiles, and key tiles of one
   const int64_t pairs = total_q / (2 * a.R) + batch, tiles = (total_k + kTile - 1) / kTile;
+  if (total_k * a.h_kv * c.cfg.head_dim * 4 > kMostCached && total_q / (2 * a.R) * units >= sms) return p;
   const int64_t most = pairs * units >= sms ? sms : pairs * units * ((tiles + kLeastTiles - 1) / kLeastTiles);
   p.ctas = (int)(most < sms ? most : sms);
   p.blocks = p.ctas;
