@@ -50,7 +50,7 @@ struct Kv4DecodePlan {
   int head_blocks;      // blocks of at most 8 query heads of a KV head
   int units;            // num_kv_heads * head_blocks
   int score_heads;      // floats of a token's scores in the workspace (0: not kept)
-  size_t off_ml, off_unit, off_scores, ws_bytes;
+  size_t off_ml, off_unit, off_before, off_scores, ws_bytes;
 };
 Kv4DecodePlan plan_kv4_decode(const Ctx& c, int batch, int max_pages, bool accumulate);
 cudaError_t launch_kv4_decode(const Ctx& c, const starkv_kv4_cache& cache, const __nv_bfloat16* q,

@@ -237,14 +237,13 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadArgs a)
 // Eviction, step 1: the kept tokens of one (sequence, KV head).
 //
 // Each token that may go gets a 32-bit key that orders like its weight (NaN below all).
-// The threads hold the keys in registers (eight tokens of each stretch of 8192 a thread,
-// four stretches; keys of tokens beyond 32768 are read again each time).  The threshold,
-// the need-th largest key, is found by counts in 2048 equal bins of the range that is left:
-// all of [least, largest] first, then the bin that holds it, until a bin is one key or
-// ends exactly at the need-th (three passes at most, two for most weights).  Bins of the
-// range, not leading digits: weights share their exponents' digits, and counts of few bins
-// queue up.  (A search bit by bit took 33 us for 256 lists of 4096 .. 8192.)
-// One ordered pass then lists the keys above the threshold and the first equal to it.
+// A cluster of CTAs shares a long sequence out; the threads hold the keys in registers (eight
+// tokens of each stretch of 4096 a thread, four stretches; keys beyond are read again each
+// time).  The threshold, the need-th largest key, is found by counts in 2048 equal bins of the
+// range that is left: all of [least, largest] first, then the bin that holds it, until a bin is
+// one key or ends exactly at the need-th (three passes at most, two for most weights).  Bins of
+// the range, not leading digits: weights share their exponents' digits, and counts of few bins
+// queue up.  One ordered pass then lists the keys above the threshold and the first equal to it.
 // ---------------------------------------------------------------------------
 struct EvictArgs {
   const int32_t* block_table;
@@ -257,11 +256,16 @@ struct EvictArgs {
   int32_t* kept;
   Kv4Pool pool;
   unsigned int* status;
+  int cluster;  // CTAs that share a (sequence, KV head) in the selection
 };
 
-constexpr int kSelThreads = 1024;
+// CTAs of a cluster at most: 32 lists of 32768 tokens take 49 us (with the move: 71) on one CTA each,
+// 35 on two, 32 on four, 40 on eight.
+constexpr int kMostCluster = 4;
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelEach = 8;                            // tokens of a thread in a stretch
-constexpr int kBins = 2048;                            // two a thread
+constexpr int kBins = 2048;                            // four a thread
 constexpr int kStretch = kSelThreads * kSelEach;
 constexpr int kHeld = 4;                               // stretches whose keys stay in registers
 
@@ -272,14 +276,40 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return ((u & 0x80000000u) ? ~u : (u | 0x80000000u)) + 1u;
 }
 
-__global__ void __launch_bounds__(kSelThreads, 1) kv4_select_kernel(const EvictArgs a) {
-  __shared__ uint32_t bins[kBins];
-  __shared__ uint32_t wsum[2][32];
-  __shared__ uint32_t ends[2][32];
-  __shared__ uint32_t found[3];  // bin of the threshold, keys above the bin, keys in it
+// Sum (and the sum before) of a value over the block's warps' lanes; sum: scratch, free again behind the next barrier.
+__device__ __forceinline__ uint32_t block_scan(uint32_t mine, uint32_t* sum, uint32_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) sum[warp] = inc;
+  __syncthreads();
+  const uint32_t w = lane < kSelWarps ? sum[lane] : 0u;
+  total = __reduce_add_sync(0xffffffffu, w);
+  return __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u) + inc - mine;
+}
+
+// grid (num_kv_heads * cluster, batch)
+__global__ void __launch_bounds__(kSelThreads, 2) kv4_select_kernel(const EvictArgs a) {
+  __shared__ __align__(16) uint32_t bins[kBins];
+  __shared__ uint32_t scan[2][kSelWarps];
+  __shared__ uint32_t ends[2][kSelWarps];
+  __shared__ uint32_t shared[4];  // for the cluster: a bad length or page, least and largest key; the counts of the list
+  __shared__ uint32_t found[3];   // bin of the threshold, keys above the bin, keys in it
   __shared__ unsigned bad;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int head = blockIdx.x, b = blockIdx.y;
+  const int C = a.cluster, rank = C > 1 ? (int)cluster_rank() : 0;
+  const int head = blockIdx.x / C, b = blockIdx.y;
+  auto sync = [&]() {
+    if (C > 1) cluster_sync();
+    else __syncthreads();
+  };
+  auto of_rank = [&](const uint32_t* p, int r) -> uint32_t {
+    return C > 1 ? __float_as_uint(dsmem_ld_f32(dsmem_addr(p, (uint32_t)r))) : *p;
+  };
   if (tid == 0) bad = 0;
   __syncthreads();
   pdl_wait();
@@ -292,8 +322,10 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv4_select_kernel(const EvictA
   const int keep = min(n, want);
   const bool sane = n >= 0 && want >= 0 && n <= a.max_pages * kPage && keep <= cap;
   const int recent = min(a.recent, keep);
-  const int old = sane ? n - recent : 0;     // tokens that may go
-  const int need = keep - recent;            // how many of them stay
+  const int need = keep - recent;            // how many of the others stay
+  // the CTA's tokens: t0 .. t1 - 1, of which those below old may go
+  const int per = sane ? (int)(((int64_t)n + C * kPage - 1) / (C * kPage)) * kPage : 0;
+  const int t0 = min((int64_t)n, (int64_t)rank * per), t1 = min((int64_t)n, (int64_t)t0 + per), old = min(t1, n - recent);
   auto check = [&](int64_t p) {
     if (p >= 0 && p < a.pool.n_pages) return true;
     atomicOr(&bad, STARKV_DEV_BAD_PAGE);
@@ -316,40 +348,28 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv4_select_kernel(const EvictA
   if (!sane) {
     if (tid == 0) bad = STARKV_DEV_BAD_SEQ_LEN;
   } else {
-    for (int i = tid; i < (keep + kPage - 1) / kPage; i += kSelThreads)
+    for (int i = rank * kSelThreads + tid; i < (keep + kPage - 1) / kPage; i += C * kSelThreads)
       check(a.dst_table[(int64_t)b * a.dst_max_pages + i]);
 #pragma unroll
     for (int g = 0; g < kHeld; ++g) {
-      const int i0 = g * kStretch + tid * kSelEach;
-      if (i0 >= n) continue;
+      const int i0 = t0 + g * kStretch + tid * kSelEach;
+      if (i0 >= t1) continue;
       const int64_t p = table[i0 / kPage];
       if (check(p) && need > 0 && keep < n && i0 < old) keys_of(p, i0, held[g]);
     }
-    for (int i0 = kHeld * kStretch + tid * kSelEach; i0 < n; i0 += kStretch) check(table[i0 / kPage]);
+    for (int i0 = t0 + kHeld * kStretch + tid * kSelEach; i0 < t1; i0 += kStretch) check(table[i0 / kPage]);
   }
   __syncthreads();
-  if (bad || keep <= 0) {
-    if (bad && tid == 0) set_status(a.status, bad);
-    for (int i = tid; i < cap; i += kSelThreads) kept[i] = -1;
-    return;
-  }
-  for (int i = keep + tid; i < cap; i += kSelThreads) kept[i] = -1;
-  if (keep == n) {
-    for (int i = tid; i < n; i += kSelThreads) kept[i] = i;
-    return;
-  }
-  for (int i = tid; i < recent; i += kSelThreads) kept[need + i] = old + i;
-  if (need == 0) return;
-  // f(key) of every key that may go
+  // f(key) of every key of the CTA that may go
   auto each = [&](auto&& f) {
 #pragma unroll
     for (int g = 0; g < kHeld; ++g)
-      if (g * kStretch < old) {
+      if (t0 + g * kStretch < old) {
 #pragma unroll
         for (int e = 0; e < kSelEach; ++e)
-          if (g * kStretch + tid * kSelEach + e < old) f(held[g][e]);
+          if (t0 + g * kStretch + tid * kSelEach + e < old) f(held[g][e]);
       }
-    for (int i0 = kHeld * kStretch + tid * kSelEach; i0 < old; i0 += kStretch) {
+    for (int i0 = t0 + kHeld * kStretch + tid * kSelEach; i0 < old; i0 += kStretch) {
       uint32_t k[kSelEach];
       keys_of(table[i0 / kPage], i0, k);
 #pragma unroll
@@ -358,10 +378,11 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv4_select_kernel(const EvictA
     }
   };
   uint32_t lo = 0xffffffffu, hi = 0;
-  each([&](uint32_t k) {
-    lo = min(lo, k);
-    hi = max(hi, k);
-  });
+  if (!bad && need > 0 && keep < n)
+    each([&](uint32_t k) {
+      lo = min(lo, k);
+      hi = max(hi, k);
+    });
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
   if (lane == 0) {
@@ -369,44 +390,77 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv4_select_kernel(const EvictA
     ends[1][warp] = hi;
   }
   __syncthreads();
-  lo = __reduce_min_sync(0xffffffffu, ends[0][lane]);
-  hi = __reduce_max_sync(0xffffffffu, ends[1][lane]);
+  if (warp == 0) {
+    lo = __reduce_min_sync(0xffffffffu, lane < kSelWarps ? ends[0][lane] : 0xffffffffu);
+    hi = __reduce_max_sync(0xffffffffu, lane < kSelWarps ? ends[1][lane] : 0u);
+    if (lane == 0) {
+      shared[0] = bad;
+      shared[1] = lo;
+      shared[2] = hi;
+    }
+  }
+  sync();
+  unsigned wrong = 0;
+  lo = 0xffffffffu;
+  hi = 0;
+  for (int r = 0; r < C; ++r) {
+    wrong |= of_rank(&shared[0], r);
+    lo = min(lo, of_rank(&shared[1], r));
+    hi = max(hi, of_rank(&shared[2], r));
+  }
+  // what needs no search; the CTAs share the writing out
+  const int step = C * kSelThreads, at0 = rank * kSelThreads + tid;
+  const int kept_now = wrong || keep < 0 ? 0 : keep;
+  if (wrong && rank == 0 && tid == 0) set_status(a.status, wrong);
+  for (int i = kept_now + at0; i < cap; i += step) kept[i] = -1;
+  if (kept_now == n) {
+    for (int i = at0; i < n; i += step) kept[i] = i;
+  } else if (kept_now > 0) {
+    for (int i = at0; i < recent; i += step) kept[need + i] = n - recent + i;
+  }
+  if (kept_now == 0 || kept_now == n || need == 0) {
+    if (C > 1) cluster_sync();  // (its shared memory has been read)
+    return;
+  }
   // keys above the range [lo, hi] stay; `left` of the keys in it do
   uint32_t left = (uint32_t)need;
   uint32_t threshold;
   while (true) {
     const uint32_t width = hi - lo;
     const int shift = max(0, 32 - __clz(width) - 11);  // width >> shift < 2048
-    bins[tid] = 0;
-    bins[tid + kSelThreads] = 0;
+    uint4* mine = reinterpret_cast<uint4*>(bins) + (kBins / 4 - 1 - tid);  // thread i: the i-th four bins from the top
+    *mine = make_uint4(0, 0, 0, 0);
     __syncthreads();
     each([&](uint32_t k) {
       if (k - lo <= width) atomicAdd(&bins[(k - lo) >> shift], 1u);
     });
-    __syncthreads();
-    // thread i owns the two bins 2 i, 2 i + 1 counted from the top: find the one that holds the left-th key
-    const uint32_t top = kBins - 1 - 2 * tid;
-    const uint32_t c0 = bins[top], c1 = bins[top - 1];
-    uint32_t inc = c0 + c1;
+    sync();
+    uint32_t c[4] = {0, 0, 0, 0};  // from the top
+    if (C == 1) {
+      const uint4 x = *mine;
+      c[0] = x.w, c[1] = x.z, c[2] = x.y, c[3] = x.x;
+    } else {
+      for (int r = 0; r < C; ++r) {
+        const float4 x = dsmem_ld_f4(dsmem_addr(mine, (uint32_t)r));
+        c[0] += __float_as_uint(x.w), c[1] += __float_as_uint(x.z), c[2] += __float_as_uint(x.y), c[3] += __float_as_uint(x.x);
+      }
+    }
+    uint32_t all, before = block_scan(c[0] + c[1] + c[2] + c[3], scan[0], all);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
+    for (int e = 0; e < 4; ++e) {
+      if (before < left && left <= before + c[e]) {
+        found[0] = (kBins / 4 - 1 - tid) * 4 + 3 - e;
+        found[1] = before;
+        found[2] = c[e];
+      }
+      before += c[e];
     }
-    if (lane == 31) wsum[0][warp] = inc;
-    __syncthreads();
-    const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[0][lane] : 0u) + inc - c0 - c1;
-    if (before < left && left <= before + c0 + c1) {
-      const bool upper = left <= before + c0;
-      found[0] = upper ? top : top - 1;
-      found[1] = upper ? before : before + c0;
-      found[2] = upper ? c0 : c1;
-    }
-    __syncthreads();
+    sync();  // (and the bins have been read)
     left -= found[1];
     lo += found[0] << shift;
-    if (left == found[2]) {  // all of the bin's keys stay
-      threshold = lo - 1;    // (lo > 0: fewer than all keys stay)
+    const uint32_t in_bin = found[2];
+    if (left == in_bin) {  // all of the bin's keys stay
+      threshold = lo - 1;  // (lo > 0: fewer than all keys stay)
       left = 0;
       break;
     }
@@ -417,25 +471,35 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv4_select_kernel(const EvictA
     hi = lo + ((1u << shift) - 1);
   }
   const uint32_t equals = left;  // of the keys equal to the threshold, the first so many stay
-  // the ordered list: a stretch at a time, each thread behind the threads before it
+  // the ordered list, behind the CTAs before this one: a stretch at a time, each thread behind the threads before it
   uint32_t base = 0, base_eq = 0;
-  auto list = [&](int i0, const uint32_t (&k)[kSelEach], int turn) {
-    uint32_t mine = 0;  // above in the low half, equal in the high half: at most 8192 each in a stretch
+  if (C > 1) {
+    uint32_t up = 0, eq = 0;
+    each([&](uint32_t k) {
+      up += k > threshold;
+      eq += k == threshold;
+    });
+    uint32_t total;
+    block_scan(up, scan[0], total);
+    if (tid == 0) shared[0] = total;
+    block_scan(eq, scan[1], total);
+    if (tid == 0) shared[3] = total;
+    sync();
+    for (int r = 0; r < rank; ++r) {
+      base += of_rank(&shared[0], r);
+      base_eq += of_rank(&shared[3], r);
+    }
+    sync();
+  }
+  int turn = 0;
+  auto list = [&](int i0, const uint32_t (&k)[kSelEach]) {
+    uint32_t mine = 0;  // above in the low half, equal in the high half: at most 4096 each in a stretch
 #pragma unroll
     for (int e = 0; e < kSelEach; ++e)
       if (i0 + e < old) mine += k[e] > threshold ? 1u : k[e] == threshold ? 0x10000u : 0u;
-    uint32_t inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    __syncthreads();
-    if (lane == 31) wsum[turn & 1][warp] = inc;
-    __syncthreads();
-    const uint32_t w = wsum[turn & 1][lane];
-    const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u) + inc - mine;
-    const uint32_t total = __reduce_add_sync(0xffffffffu, w);
+    uint32_t total;
+    const uint32_t before = block_scan(mine, scan[turn & 1], total);  // (two scratches: one barrier a stretch)
+    ++turn;
     uint32_t up = base + (before & 0xffffu), eq = base_eq + (before >> 16);
 #pragma unroll
     for (int e = 0; e < kSelEach; ++e)
@@ -451,14 +515,15 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv4_select_kernel(const EvictA
     base += total & 0xffffu;
     base_eq += total >> 16;
   };
+  __syncthreads();
 #pragma unroll
   for (int g = 0; g < kHeld; ++g)
-    if (g * kStretch < old) list(g * kStretch + tid * kSelEach, held[g], g);
-  for (int g = kHeld; g * kStretch < old; ++g) {
+    if (t0 + g * kStretch < old) list(t0 + g * kStretch + tid * kSelEach, held[g]);
+  for (int i = t0 + kHeld * kStretch; i < old; i += kStretch) {
     uint32_t k[kSelEach] = {};
-    const int i0 = g * kStretch + tid * kSelEach;
+    const int i0 = i + tid * kSelEach;
     if (i0 < old) keys_of(table[i0 / kPage], i0, k);
-    list(g * kStretch + tid * kSelEach, k, g);
+    list(i0, k);
   }
 }
 
@@ -615,8 +680,12 @@ cudaError_t launch_kv4_evict(const Ctx& c, const starkv_kv4_cache& cache, const 
                              const int32_t* dst_table, int dst_max_pages, int32_t* new_lens, int32_t* kept,
                              cudaStream_t s) {
   EvictArgs a{block_table, seq_lens, keep_lens, recent, max_pages, dst_table, dst_max_pages, new_lens, kept,
-              pool_of(c, cache), c.status};
-  cudaError_t e = launch_chained(kv4_select_kernel, dim3(c.cfg.num_kv_heads, batch), dim3(kSelThreads), 0, s, 1u, a);
+              pool_of(c, cache), c.status, 1};
+  // clusters where a list is long and there are few: two CTAs run on an SM
+  const int64_t most = (int64_t)max_pages * kPage, lists = (int64_t)c.cfg.num_kv_heads * batch;
+  while (a.cluster < kMostCluster && most / a.cluster > kStretch && lists * a.cluster * 2 <= 2 * 148) a.cluster *= 2;
+  cudaError_t e = launch_chained(kv4_select_kernel, dim3(c.cfg.num_kv_heads * a.cluster, batch), dim3(kSelThreads), 0, s,
+                                 (unsigned)a.cluster, a);
   if (e != cudaSuccess) return e;
   const int per = kMoveThreads / 32 * kMovePages;
   return launch_chained(c.cfg.head_dim == 64 ? kv4_move_kernel<64> : kv4_move_kernel<128>,

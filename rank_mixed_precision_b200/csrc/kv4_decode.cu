@@ -53,6 +53,7 @@ struct DecodeArgs {
   float* part_o;           // [ctas][2][8][D], relative to the part's maximum: [0] of a unit that began before the
   float2* part_ml;         // [ctas][2][8] (maximum, sum)                     CTA's stretch, [1] of one that goes on behind
   float2* unit_ml;         // [B][units][8], of units within one CTA (NULL: not asked for)
+  int64_t* before;         // [B + 1] pages before each sequence, and of all (ctas > 0)
   float* scores;           // [B][h_kv][max_pages * 16][score_heads], log2 units (NULL: not asked for)
   unsigned int* status;
 };
@@ -115,7 +116,10 @@ __device__ __forceinline__ int64_t cut(int64_t c, int64_t total, int ctas) {
   return total <= ctas ? min(c, total) : c * total / ctas;
 }
 __device__ __forceinline__ int64_t cta_of(int64_t x, int64_t total, int ctas) {
-  return total <= ctas ? x : ((x + 1) * ctas - 1) / total;
+  if (total <= ctas) return x;
+  const int64_t y = (x + 1) * ctas - 1;
+  // (a division in 64 bits is hundreds of cycles of the join's short life)
+  return (y | total) >> 32 == 0 ? (int64_t)((uint32_t)y / (uint32_t)total) : y / total;
 }
 
 template <int D>
@@ -164,6 +168,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_decode_kernel(const Decod
     const int64_t total = block_sum<kThreads>(mine, sums) * a.units;
     pos = cut(blockIdx.x, total, a.ctas);
     end = cut(blockIdx.x + 1, total, a.ctas);
+    if (blockIdx.x == 0 && tid == 0) a.before[a.batch] = total / a.units;
     if (pos == end) return;
     // the last sequence that starts at or before pos, among those that have pages
     int64_t carry = 0;
@@ -180,6 +185,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_decode_kernel(const Decod
       __syncthreads();
       int64_t first = carry + inc - pages;
       for (int w = 0; w < warp; ++w) first += sums[w];
+      if (blockIdx.x == 0 && i0 + tid < a.batch) a.before[i0 + tid] = first;
       if (pages > 0 && first * a.units <= pos && pos < (first + pages) * a.units) {
         begin[0] = i0 + tid;
         begin[1] = first;
@@ -361,9 +367,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_decode_kernel(const Decod
       float sa[2] = {0.f, 0.f}, sb[2] = {0.f, 0.f};
 #pragma unroll
       for (int kp = 0; kp < NG; ++kp) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        float d[4];
         const uint32_t wa = ka[kp], wb = kb[kp], va = wa >> 8, vb = wb >> 8;
-        mma16816(d, wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u, qb[kp][0], qb[kp][1]);
+        mma16816_zero(d, wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u, qb[kp][0], qb[kp][1]);
         mma16816(d, va & 0x000f000fu, vb & 0x000f000fu, va & 0x00f000f0u, vb & 0x00f000f0u, qb[kp][2], qb[kp][3]);
         const float2 sza = unpack_meta(ma[kp]), szb = unpack_meta(mb[kp]);
 #pragma unroll
@@ -562,7 +568,6 @@ constexpr int kJoinHeads = 32;  // heads whose maximum and 1 / sum a pass holds
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const DecodeArgs a) {
   __shared__ float2 norm[kJoinHeads];  // maximum, 1 / sum
-  __shared__ int64_t sums[kJoinThreads / 32];
   __shared__ float4 acc[kJoinThreads];
   const int tid = threadIdx.x;
   const int kv = blockIdx.y, b = blockIdx.z;
@@ -578,15 +583,12 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const DecodeArgs
       for (int i = tid; i < a.group * (D / 2); i += kJoinThreads) out[i] = 0u;
     return;
   }
-  int64_t before = 0, total = 0;
-  if (a.ctas > 0) {
-    for (int i = tid; i < a.batch; i += kJoinThreads) {
-      const int p = pages_of(a, i);
-      total += p;
-      if (i < b) before += p;
-    }
-    total = block_sum<kJoinThreads>(total, sums) * a.units;
-    before = block_sum<kJoinThreads>(before, sums) * a.units;
+  const int64_t before = a.ctas > 0 ? a.before[b] * a.units : 0, total = a.ctas > 0 ? a.before[a.batch] * a.units : 0;
+  int64_t page_of[kJoinTokens / kJoinThreads];  // asked for before the sums are
+#pragma unroll
+  for (int i = 0; i < kJoinTokens / kJoinThreads; ++i) {
+    const int tok = token0 + i * kJoinThreads + tid;
+    page_of[i] = blockIdx.x > 0 && tok < len ? a.block_table[(int64_t)b * a.max_pages + tok / kPage] : -1;
   }
   // the CTAs whose stretches hold unit u's first and last page
   auto ctas_of = [&](int u, int64_t& c0, int64_t& c1) {
@@ -678,11 +680,16 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const DecodeArgs
         const float* row = rows + (int64_t)tok * a.score_heads;
         if (a.score_heads == 1) {
           add[i] = ex2(row[0] - norm[0].x) * norm[0].y;
+        } else if (a.score_heads == 2) {
+          const float2 x = *reinterpret_cast<const float2*>(row);
+          add[i] = fmaf(ex2(x.x - norm[0].x), norm[0].y, ex2(x.y - norm[1].x) * norm[1].y);
         } else {
-          for (int h = 0; h < heads; h += 2) {
-            const float2 x = *reinterpret_cast<const float2*>(row + h);
-            add[i] = fmaf(ex2(x.x - norm[h].x), norm[h].y, add[i]);
-            if (h + 1 < heads) add[i] = fmaf(ex2(x.y - norm[h + 1].x), norm[h + 1].y, add[i]);
+          for (int h = 0; h < heads; h += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(row + h);
+            const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (h + e < heads) add[i] = fmaf(ex2(y[e] - norm[h + e].x), norm[h + e].y, add[i]);
           }
         }
       }
@@ -692,8 +699,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const DecodeArgs
 #pragma unroll
   for (int i = 0; i < kJoinTokens / kJoinThreads; ++i) {
     const int tok = token0 + i * kJoinThreads + tid;
-    if (tok >= len) continue;
-    const int64_t page = a.block_table[(int64_t)b * a.max_pages + tok / kPage];
+    const int64_t page = page_of[i];  // (-1 behind the last token)
     if (page < 0 || page >= a.pool.n_pages) continue;
     // one addition a token and call: atomic only for a page that two tables share
     atomicAdd(&a.pool.weights[(page * a.pool.h_kv + kv) * kPage + tok % kPage], add[i]);
@@ -714,12 +720,13 @@ Kv4DecodePlan plan_kv4_decode(const Ctx& c, int batch, int max_pages, bool accum
   const int64_t most = (int64_t)batch * p.units * max_pages;
   const int64_t round = (int64_t)sms * kCtas;
   p.ctas = max_pages <= kWholePages ? 0 : (int)(most / 8 < round ? most / 8 : round);
-  p.score_heads = !accumulate ? 0 : c.group == 1 ? 1 : (c.group + 1) / 2 * 2;
+  p.score_heads = !accumulate ? 0 : c.group <= 2 ? c.group : (c.group + 3) / 4 * 4;
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t rows = (size_t)p.ctas * 2 * kHeads;
   p.off_ml = al(rows * f.head_dim * 4);
   p.off_unit = p.off_ml + al(rows * 8);
-  p.off_scores = p.off_unit + (accumulate ? al((size_t)batch * p.units * kHeads * 8) : 0);
+  p.off_before = p.off_unit + (accumulate ? al((size_t)batch * p.units * kHeads * 8) : 0);
+  p.off_scores = p.off_before + (p.ctas > 0 ? al(((size_t)batch + 1) * 8) : 0);
   p.ws_bytes = p.off_scores + al((size_t)batch * f.num_kv_heads * max_pages * kPage * p.score_heads * 4);
   return p;
 }
@@ -759,6 +766,7 @@ cudaError_t launch_kv4_decode(const Ctx& c, const starkv_kv4_cache& cache, const
   a.part_o = (float*)ws;
   a.part_ml = (float2*)((char*)ws + plan.off_ml);
   a.unit_ml = accumulate ? (float2*)((char*)ws + plan.off_unit) : nullptr;
+  a.before = (int64_t*)((char*)ws + plan.off_before);
   a.scores = accumulate ? (float*)((char*)ws + plan.off_scores) : nullptr;
   a.status = c.status;
   return c.cfg.head_dim == 64 ? launch_decode_d<64>(c, a, s) : launch_decode_d<128>(c, a, s);

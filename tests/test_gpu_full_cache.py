@@ -309,6 +309,44 @@ def test_evict_longer(n):
     check_evict((2, 1, 64), [n], [n // 3], 17, seed=n)
 
 
+def check_selection(h, lens, keeps, recent, weights):
+    """The kept tokens of long sequences in scattered pages against a stable sort."""
+    S = skv()
+    kv = context(h, h, 64)
+    rng = np.random.default_rng(len(lens) + lens[0])
+    room = [-(-min(n, k) // 16) for n, k in zip(lens, keeps)]
+    t, spare, n_pages = tables(rng, lens, extra=sum(room))
+    dst = np.zeros((len(lens), max(room)), np.int32)
+    at = 0
+    for b, r in enumerate(room):
+        dst[b, :r] = spare[at:at + r]
+        at += r
+    w = weights(rng, (n_pages, h, 16)).astype(np.float32)
+    cache = S.KV4Cache(kv.cfg, n_pages, weights=torch.from_numpy(w).cuda())
+    new, kept = kv.kv4_evict(cache, i32(t), i32(lens), i32(keeps), recent, i32(dst))
+    assert kv.status() == 0
+    kept = kept.cpu().numpy()
+    for b, (n, keep) in enumerate(zip(lens, keeps)):
+        src = F.slots_of(t[b], n)
+        keep = min(n, keep)
+        for head in range(h):
+            x = w[src // 16, head, src % 16].copy()
+            x[n - min(keep, recent):] = np.inf
+            stay = np.sort(np.argsort(-x, kind="stable")[:keep])
+            np.testing.assert_array_equal(kept[b, head, :keep], stay)
+            assert (kept[b, head, keep:] == -1).all()
+
+
+@pytest.mark.parametrize("h,lens", [(1, [20000]), (3, [9000, 300]), (2, [70001]), (1, [140000]), (160, [5000])])
+def test_evict_selects_from_long_sequences(h, lens):
+    """On one CTA a list and on clusters of two, four and eight; more tokens than registers hold."""
+    keeps = [max(1, n * 2 // 5) for n in lens]
+    check_selection(h, lens, keeps, 33, lambda rng, s: np.exp(1.5 * rng.standard_normal(s)))
+    if h < 100:
+        check_selection(h, lens, [n - 1 for n in lens], 1, lambda rng, s: rng.integers(0, 3, s))   # ties across CTAs
+        check_selection(h, lens, [5] * len(lens), 0, lambda rng, s: rng.standard_normal(s))
+
+
 def test_evict_of_equal_weights_takes_the_lowest_index():
     check_evict((4, 2, 64), [90, 50], [30, 20], 4, weights=lambda rng, s: np.zeros(s, np.float32))
     check_evict((4, 2, 64), [90, 50], [30, 20], 4, weights=lambda rng, s: rng.integers(0, 3, s).astype(np.float32))
