@@ -429,42 +429,64 @@ def starkv_kv4_append(ctx, cfg, cache: starkv_kv4_cache, k, v, slot_mapping, wei
                                    k.shape[0], _on(stream)))
 
 
-def starkv_kv4_read(ctx, cfg, cache: starkv_kv4_cache, block_table, cu, k_out, v_out, starts=None, stream=None):
-    """Rows cu[b] .. cu[b+1]-1 of k_out and v_out become tokens starts[b] .. of sequence b, in bf16."""
+# Each entry has its checks of what the caller gives apart from its call: the methods of StarKV below make their own
+# outputs and workspaces, which need none.
+def _check_read(block_table, cu, starts):
     _need(block_table, torch.int32, "block_table", 2)
     _need(cu, torch.int32, "cu", 1)
-    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
-        _need(t, torch.bfloat16, n, 3)
-        if t.shape[0] != k_out.shape[0] or tuple(t.shape[1:]) != (cfg.num_kv_heads, cfg.head_dim):
-            raise ValueError(f"{n} must be [total, {cfg.num_kv_heads}, {cfg.head_dim}]")
     B = block_table.shape[0]
     if starts is not None:
         _need(starts, torch.int32, "starts", 1)
     if cu.shape[0] != B + 1 or (starts is not None and starts.shape[0] != B):
         raise ValueError("block_table / cu / starts disagree on the batch")
+
+
+def _call_read(ctx, cache, block_table, cu, k_out, v_out, starts, stream):
+    B, pages = block_table.shape
+    _check(lib().starkv_kv4_read(ctx, ctypes.byref(cache), _at(block_table), _at(starts), _at(cu), B, pages,
+                                 k_out.shape[0], _at(k_out), _at(v_out), _on(stream)))
+
+
+def starkv_kv4_read(ctx, cfg, cache: starkv_kv4_cache, block_table, cu, k_out, v_out, starts=None, stream=None):
+    """Rows cu[b] .. cu[b+1]-1 of k_out and v_out become tokens starts[b] .. of sequence b, in bf16."""
+    _check_read(block_table, cu, starts)
+    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+        _need(t, torch.bfloat16, n, 3)
+        if t.shape[0] != k_out.shape[0] or tuple(t.shape[1:]) != (cfg.num_kv_heads, cfg.head_dim):
+            raise ValueError(f"{n} must be [total, {cfg.num_kv_heads}, {cfg.head_dim}]")
     _one_device(k_out, v_out, block_table, cu, starts)
-    _check(lib().starkv_kv4_read(ctx, ctypes.byref(cache), _at(block_table), _at(starts), _at(cu), B,
-                                 block_table.shape[1], k_out.shape[0], _at(k_out), _at(v_out), _on(stream)))
+    _call_read(ctx, cache, block_table, cu, k_out, v_out, starts, stream)
+
+
+def _check_decode(cfg, q, block_table, seq_lens):
+    _need(q, torch.bfloat16, "q", 3)
+    _need(block_table, torch.int32, "block_table", 2)
+    _need(seq_lens, torch.int32, "seq_lens", 1)
+    B, H, d = q.shape
+    if H != cfg.num_q_heads or d != cfg.head_dim:
+        raise ValueError(f"q must be [batch, {cfg.num_q_heads}, {cfg.head_dim}]")
+    if block_table.shape[0] != B or seq_lens.shape[0] != B:
+        raise ValueError("q / block_table / seq_lens disagree on the batch")
+
+
+def _call_decode(ctx, cache, q, block_table, seq_lens, accumulate, out, workspace, stream):
+    B, pages = block_table.shape
+    _check(lib().starkv_kv4_decode_attn(ctx, ctypes.byref(cache), _at(q), _at(block_table), _at(seq_lens), B, pages,
+                                        int(bool(accumulate)), _at(out), _at(workspace),
+                                        0 if workspace is None else workspace.numel(), _on(stream)))
 
 
 def starkv_kv4_decode_attn(ctx, cfg, cache: starkv_kv4_cache, q, block_table, seq_lens, accumulate, out, workspace,
                            stream=None):
     """Single-query attention over the 4-bit cache; accumulate: add the probabilities to the cache's weights."""
-    _need(q, torch.bfloat16, "q", 3)
-    _need(block_table, torch.int32, "block_table", 2)
-    _need(seq_lens, torch.int32, "seq_lens", 1)
+    _check_decode(cfg, q, block_table, seq_lens)
     _need(out, torch.bfloat16, "out", 3)
-    B = q.shape[0]
-    if tuple(q.shape[1:]) != (cfg.num_q_heads, cfg.head_dim):
-        raise ValueError(f"q must be [batch, {cfg.num_q_heads}, {cfg.head_dim}]")
-    if block_table.shape[0] != B or seq_lens.shape[0] != B or tuple(out.shape) != tuple(q.shape):
-        raise ValueError("q / block_table / seq_lens / out disagree on the batch")
+    if out.shape != q.shape:
+        raise ValueError("q and out disagree")
     if workspace is not None:
         _need(workspace, torch.uint8, "workspace", 1)
     _one_device(q, block_table, seq_lens, out, workspace)
-    _check(lib().starkv_kv4_decode_attn(ctx, ctypes.byref(cache), _at(q), _at(block_table), _at(seq_lens), B,
-                                        block_table.shape[1], int(bool(accumulate)), _at(out), _at(workspace),
-                                        0 if workspace is None else workspace.numel(), _on(stream)))
+    _call_decode(ctx, cache, q, block_table, seq_lens, accumulate, out, workspace, stream)
 
 
 def starkv_kv4_evict(ctx, cfg, cache: starkv_kv4_cache, block_table, seq_lens, keep_lens, recent, dst_block_table,
@@ -502,23 +524,34 @@ def starkv_prompt_workspace_bytes(ctx, batch: int, total_q: int, total_k: int) -
     return out.value
 
 
-def starkv_prompt_attn(ctx, cfg, q, k, v, cu_q, cu_k, max_q_len, out, lse=None, workspace=None, stream=None):
-    """Causal attention of packed sequences over their own keys and values."""
+def _check_prompt(cfg, q, k, v, cu_q, cu_k):
     qs, ks = _packed(cfg, q, k, cu_q, cu_k)
     vs = _rows(v, cfg.num_kv_heads, cfg.head_dim, "v")
+    if v.shape[0] != k.shape[0]:
+        raise ValueError("k and v disagree on their rows")
+    return qs, ks, vs
+
+
+def _call_prompt(ctx, q, k, v, strides, cu_q, cu_k, max_q_len, out, lse, workspace, stream):
+    _check(lib().starkv_prompt_attn(ctx, _at(q), _at(k), _at(v), *strides, _at(cu_q), _at(cu_k), cu_q.shape[0] - 1,
+                                    q.shape[0], k.shape[0], int(max_q_len), _at(out), _at(lse), _at(workspace),
+                                    0 if workspace is None else workspace.numel(), _on(stream)))
+
+
+def starkv_prompt_attn(ctx, cfg, q, k, v, cu_q, cu_k, max_q_len, out, lse=None, workspace=None, stream=None):
+    """Causal attention of packed sequences over their own keys and values."""
+    strides = _check_prompt(cfg, q, k, v, cu_q, cu_k)
     _need(out, torch.bfloat16, "out", 3)
-    if v.shape[0] != k.shape[0] or tuple(out.shape) != tuple(q.shape):
-        raise ValueError("k and v, or q and out, disagree on their rows")
+    if out.shape != q.shape:
+        raise ValueError("q and out disagree on their rows")
     if lse is not None:
         _need(lse, torch.float32, "lse", 2)
-        if tuple(lse.shape) != tuple(q.shape[:2]):
+        if lse.shape != q.shape[:2]:
             raise ValueError("lse must be [total_q, num_q_heads]")
     if workspace is not None:
         _need(workspace, torch.uint8, "workspace", 1)
     _one_device(q, k, v, cu_q, cu_k, out, lse, workspace)
-    _check(lib().starkv_prompt_attn(ctx, _at(q), _at(k), _at(v), qs, ks, vs, _at(cu_q), _at(cu_k), cu_q.shape[0] - 1,
-                                    q.shape[0], k.shape[0], int(max_q_len), _at(out), _at(lse), _at(workspace),
-                                    0 if workspace is None else workspace.numel(), _on(stream)))
+    _call_prompt(ctx, q, k, v, strides, cu_q, cu_k, max_q_len, out, lse, workspace, stream)
 
 
 def starkv_prompt_weights(ctx, cfg, q, k, lse, cu_q, cu_k, max_k_len, window, weights, stream=None):
@@ -591,13 +624,20 @@ class KV4Cache:
         return self.pages.numel() + (0 if self.weights is None else 4 * self.weights.numel())
 
 
-def _new(like, shape, dtype, stream):
-    """An uninitialised tensor beside `like` that a call on `stream` may use (it is given back behind that stream's work)."""
-    t = like.new_empty(shape, dtype=dtype)
+def _lent(t, stream):
+    """A new tensor that a call on `stream` uses: it is given back behind that stream's work."""
     if stream is not None:
         t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
                         torch.cuda.ExternalStream(int(stream), device=t.device))
     return t
+
+
+def _new(like, shape, dtype, stream):
+    return _lent(like.new_empty(shape, dtype=dtype), stream)
+
+
+def _new_like(t, stream):
+    return _lent(torch.empty_like(t, memory_format=torch.contiguous_format), stream)
 
 
 class StarKV:
@@ -653,18 +693,25 @@ class StarKV:
 
     def kv4_read(self, cache: KV4Cache, block_table, cu, total: int, starts=None, stream=None):
         """Keys and values [total, num_kv_heads, head_dim] of tokens starts[b] .. of each sequence."""
-        shape = (total, self.cfg.num_kv_heads, self.cfg.head_dim)
-        k = _new(cache.pages, shape, torch.bfloat16, stream)
-        v = _new(cache.pages, shape, torch.bfloat16, stream)
-        starkv_kv4_read(self.ctx, self.cfg, cache.struct, block_table, cu, k, v, starts, stream)
+        _check_read(block_table, cu, starts)
+        _one_device(cache.pages, block_table, cu, starts)
+        k = _new(cache.pages, (total, self.cfg.num_kv_heads, self.cfg.head_dim), torch.bfloat16, stream)
+        v = _new_like(k, stream)
+        _call_read(self.ctx, cache.struct, block_table, cu, k, v, starts, stream)
         return k, v
 
     def kv4_decode(self, cache: KV4Cache, q, block_table, seq_lens, accumulate=False, out=None, stream=None):
-        _one_device(cache.pages)
-        n = starkv_workspace_bytes(self.ctx, OP_KV4_DECODE, block_table.shape[0], block_table.shape[1], int(accumulate))
-        ws = _new(cache.pages, n, torch.uint8, stream) if n else None
-        out = _new(q, q.shape, q.dtype, stream) if out is None else out
-        starkv_kv4_decode_attn(self.ctx, self.cfg, cache.struct, q, block_table, seq_lens, accumulate, out, ws, stream)
+        _check_decode(self.cfg, q, block_table, seq_lens)
+        _one_device(cache.pages, q, block_table, seq_lens, out)
+        n = starkv_workspace_bytes(self.ctx, OP_KV4_DECODE, *block_table.shape, int(bool(accumulate)))
+        ws = _new(q, n, torch.uint8, stream) if n else None
+        if out is None:
+            out = _new_like(q, stream)
+        else:
+            _need(out, torch.bfloat16, "out", 3)
+            if out.shape != q.shape:
+                raise ValueError("q and out disagree")
+        _call_decode(self.ctx, cache.struct, q, block_table, seq_lens, accumulate, out, ws, stream)
         return out
 
     def kv4_evict(self, cache: KV4Cache, block_table, seq_lens, keep_lens, recent: int, dst_block_table, stream=None):
@@ -680,11 +727,18 @@ class StarKV:
 
     def prompt(self, q, k, v, cu_q, cu_k, max_q_len: int, out=None, stream=None):
         """Causal attention of packed prompts: (out [total_q, H, d], lse [total_q, H])."""
-        out = _new(q, q.shape, q.dtype, stream) if out is None else out
+        strides = _check_prompt(self.cfg, q, k, v, cu_q, cu_k)
+        _one_device(q, k, v, cu_q, cu_k, out)
+        if out is None:
+            out = _new_like(q, stream)
+        else:
+            _need(out, torch.bfloat16, "out", 3)
+            if out.shape != q.shape:
+                raise ValueError("q and out disagree on their rows")
         lse = _new(q, q.shape[:2], torch.float32, stream)
         n = starkv_prompt_workspace_bytes(self.ctx, cu_q.shape[0] - 1, q.shape[0], k.shape[0])
         ws = _new(q, n, torch.uint8, stream) if n else None
-        starkv_prompt_attn(self.ctx, self.cfg, q, k, v, cu_q, cu_k, max_q_len, out, lse, ws, stream)
+        _call_prompt(self.ctx, q, k, v, strides, cu_q, cu_k, max_q_len, out, lse, ws, stream)
         return out, lse
 
     def prompt_weights(self, q, k, lse, cu_q, cu_k, max_k_len: int, window: int, stream=None):
