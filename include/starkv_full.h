@@ -78,7 +78,8 @@ STARKV_API starkv_status starkv_kv4_layout(const starkv_config* cfg, int64_t n_p
  * distinct within one call.  weights: device fp32 [n][num_kv_heads], the tokens' first
  * accumulated weights (starkv_prompt_weights), or NULL for zero; written where the
  * cache keeps weights.  Only the written tokens' bytes change.
- * Errors: INVALID_ARG; device bits BAD_SLOT, QUANT_OVERFLOW. */
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE (2^35 channels of k or more); device bits BAD_SLOT,
+ * QUANT_OVERFLOW. */
 STARKV_API starkv_status starkv_kv4_append(starkv_ctx* ctx, const starkv_kv4_cache* cache, const void* k,
                                            const void* v, int64_t k_stride, int64_t v_stride,
                                            const int64_t* slot_mapping, const float* weights, int64_t n,

@@ -98,7 +98,7 @@ starkv_status starkv_kv4_append(starkv_ctx* ctx, const starkv_kv4_cache* cache, 
   if (st) return st;
   if (!slot_mapping) return fail(STARKV_ERR_INVALID_ARG, "slot_mapping is NULL");
   if (cache->n_pages == 0) return fail(STARKV_ERR_INVALID_ARG, "cache has no pages");
-  if (n > kMaxBlocks * 8 / width) return fail(STARKV_ERR_UNSUPPORTED_SHAPE, "n %lld: too many tokens", (long long)n);
+  if (n > kMaxBlocks * 16 / width) return fail(STARKV_ERR_UNSUPPORTED_SHAPE, "n %lld: too many tokens", (long long)n);
   const cudaError_t e =
       launch_kv4_append(*c, *cache, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, k_stride, v_stride, slot_mapping,
                         weights, n, (cudaStream_t)stream);
