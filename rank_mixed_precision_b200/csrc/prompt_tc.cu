@@ -938,8 +938,9 @@ struct WeightSmem {
   static constexpr int kStages = D == 128 ? 3 : 6;   // Q tiles
   static constexpr int kKeys = D == 128 ? 3 : 4;     // K tiles
   static constexpr uint32_t kRing = kKeys * kTileBytes;
-  static constexpr uint32_t kCols = kRing + kStages * kTileBytes;  // [stage][128] -lse in log2 units, [stage][128] last key
-  static constexpr uint32_t kSums = kCols + kStages * kTile * 8;   // [2][3][128] sums of warps 4 .. 15
+  static constexpr int kSlots = 8;                   // steps' columns: they are read longer than the Q tile is
+  static constexpr uint32_t kCols = kRing + kStages * kTileBytes;  // [slot][128] -lse in log2 units, [slot][128] last key
+  static constexpr uint32_t kSums = kCols + kSlots * kTile * 8;    // [2][3][128] sums of warps 4 .. 15
   static constexpr uint32_t kNotes = kSums + 2 * 3 * kTile * 4;    // [4] what a product's sums go by
   static constexpr uint32_t kBar = kNotes + 4 * 32;
   static constexpr uint32_t kBytes = kBar + 512 + 1024;
@@ -947,8 +948,8 @@ struct WeightSmem {
 
 // One product's note, beside its TMEM buffer.
 struct __align__(16) Note {
-  int flags;     // kWhole: no column is masked for any key; kLast: the item's last step; kLeave: its Q tile's last use; kStop
-  int stage;     // the Q tile's
+  int flags;     // kWhole: no column is masked for any key; kLast: the item's last step; kLeave: its columns' last use; kStop
+  int slot;      // the columns'
   int live;      // columns that hold queries
   int key0, keys;  // the item's first key, and the keys of its sequence
   int unused;
@@ -1042,15 +1043,17 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   uint64_t* kfull = bar;           // [KS]
   uint64_t* kempty = kfull + KS;   // [KS]
   uint64_t* full = kempty + KS;    // [ST] Q tile landed
-  uint64_t* empty = full + ST;     // [ST] Q tile read by its products, its columns by 8 warps
-  uint64_t* sfull = empty + ST;    // [4] a product, its columns (2 warps) and its note are there,
+  uint64_t* empty = full + ST;     // [ST] and read by its products
+  uint64_t* cfree = empty + ST;    // [kSlots] columns read by 8 warps
+  uint64_t* sfull = cfree + SM::kSlots;  // [4] a product, and its columns and note are there,
   uint64_t* sempty = sfull + 4;    // [4] and have been read
   uint64_t* sums = sempty + 4;     // [2][4] three warps' sums are there
   uint64_t* taken = sums + 8;      // [2][4] and have been added
   uint64_t* done = taken + 8;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* both = done + 1;       // resident: warps 18 and 19 have laid a (sequence, KV head)'s columns out
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(both + 1);
   float* lse2 = reinterpret_cast<float*>(sm + SM::kCols);
-  int* last = reinterpret_cast<int*>(sm + SM::kCols + ST * kTile * 4);
+  int* last = reinterpret_cast<int*>(sm + SM::kCols + SM::kSlots * kTile * 4);
   float* other = reinterpret_cast<float*>(sm + SM::kSums);
   Note* notes = reinterpret_cast<Note*>(sm + SM::kNotes);
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
@@ -1073,10 +1076,11 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     }
     for (int s = 0; s < ST; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 9);
+      mbar_init(&empty[s], 1);
     }
+    for (int s = 0; s < SM::kSlots; ++s) mbar_init(&cfree[s], 8);
     for (int s = 0; s < 4; ++s) {
-      mbar_init(&sfull[s], 3);
+      mbar_init(&sfull[s], 2);
       mbar_init(&sempty[s], 8);
     }
     for (int s = 0; s < 8; ++s) {
@@ -1084,6 +1088,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       mbar_init(&taken[s], 1);
     }
     mbar_init(done, 1);
+    mbar_init(both, 2);
     fence_mbar_init();
   }
   pdl_wait();
@@ -1261,20 +1266,25 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     mbar_wait(done, 0, ok ? 2000000000ull : 100000000ull);
   } else if (warp >= 18) {
     // ---------------- columns and notes (and the zeros of keys that no counting query sees) ----------------
-    int u = 0, st = 0;
-    uint32_t sph = 0;
-    int col_r[2], col_h[2];  // the lane's columns: query within the tile, head within the block
+    // warp 18 does the even steps, warp 19 the odd ones: a step's work in one warp is longer than a step
+    int u = 0, laid = 0, laid_units = 0;  // notes, (streamed) columns and (resident) (sequence, KV head)s so far
+    auto my_turn = [&]() { return (u & 1) == warp - 18; };
+    int col_r[4], col_h[4];  // the lane's columns: query within the tile, head within the block
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int c = (warp - 18) * 64 + e * 32 + lane;
+    for (int e = 0; e < 4; ++e) {
+      const int c = e * 32 + lane;
       col_r[e] = c / a.gb;
       col_h[e] = c % a.gb;
     }
     auto note = [&](const Note& n) {  // for the u-th product, whose buffer must be free
       const int w = u & 3;
+      if (!my_turn()) {
+        ++u;
+        return true;
+      }
       if (!__all_sync(0xffffffffu, mbar_wait_short(&sempty[w], ((u >> 2) & 1) ^ 1))) return false;
       if (lane == 0) {
-        if (warp == 18) notes[w] = n;
+        notes[w] = n;
         mbar_arrive(&sfull[w]);
       }
       ++u;
@@ -1292,66 +1302,78 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         continue;
       }
       const bool lay = !resident || fresh, leave = !resident || !more || it.fresh;
-      // the next step's log-sum-exps are asked for before this step's stage is free
-      float x[2], next_x[2];
-      int k[2], next_k[2];
+      // the log-sum-exps of the warp's next step are asked for before this step's slot is free
+      float x[4], next_x[4];
       int hb = rank / per, i0 = first + rank % per * a.R;  // the step's head block and first query
-      auto fetch = [&](int v, int hb, int i0) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int i = i0 + col_r[e], h = hb * a.gb + col_h[e];
-          const bool live = v < steps && col_r[e] < a.R && i < n && h < a.group;
-          next_x[e] = 0.f;
-          next_k[e] = kColNone;
-          if (live) {
-            next_x[e] = a.lse_in[(int64_t)(q0 + i) * a.H + kv * a.group + h];
-            next_k[e] = off + i;
-          }
-        }
-      };
-      if (lay) fetch(rank, hb, i0);
-      for (int v = rank; v < steps; v += split) {
-        const int s = resident ? v : st;
-        const uint32_t ph = resident ? (flips >> v) & 1u : sph;
-        if (++st == ST) {
-          st = 0;
-          sph ^= 1;
-        }
-        // a column is masked for some key of the tile in the first tiles only
-        const bool whole = off + i0 >= key0 + kTile - 1 && (hb + 1) * a.gb <= a.group;
-        const Note told{(whole ? kWhole : 0) | (v + 2 * split >= steps ? kLast : 0) | (leave ? kLeave : 0), s,
-                        min(a.R, n - i0) * a.gb, key0, keys, 0, row};
+      auto advance = [&](int& hb, int& i0) {
         i0 += split * a.R;
         while (i0 >= first + per * a.R) {
           i0 -= per * a.R;
           ++hb;
         }
+      };
+      auto live = [&](int e, int hb, int i0) {
+        return col_r[e] < a.R && i0 + col_r[e] < n && hb * a.gb + col_h[e] < a.group;
+      };
+      auto fetch = [&](int v, int hb, int i0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          next_x[e] = 0.f;
+          if (v < steps && live(e, hb, i0))
+            next_x[e] = a.lse_in[(int64_t)(q0 + i0 + col_r[e]) * a.H + kv * a.group + hb * a.gb + col_h[e]];
+        }
+      };
+      if (lay) {
+        int h = hb, i = i0, v = rank;
+        if (!my_turn()) {
+          advance(h, i);
+          v += split;
+        }
+        fetch(v, h, i);
+      }
+      for (int v = rank; v < steps; v += split) {
+        const int s = resident ? v : laid % SM::kSlots;
+        const uint32_t ph = resident ? (flips >> v) & 1u : (uint32_t)(laid / SM::kSlots) & 1u;
+        ++laid;
+        if (!my_turn()) {
+          ++u;
+          advance(hb, i0);
+          continue;
+        }
         if (lay) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            x[e] = next_x[e];
-            k[e] = next_k[e];
-          }
-          fetch(v + split, hb, i0);
-          if (!__all_sync(0xffffffffu, mbar_wait_short(&empty[s], ph ^ 1))) {
+          for (int e = 0; e < 4; ++e) x[e] = next_x[e];
+          int h = hb, i = i0;
+          advance(h, i);
+          advance(h, i);
+          fetch(v + 2 * split, h, i);
+          if (!__all_sync(0xffffffffu, mbar_wait_short(&cfree[s], ph ^ 1))) {
             ok = false;
             break;
           }
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int c = (warp - 18) * 64 + e * 32 + lane;
-            lse2[s * kTile + c] = x[e] * -kLog2e;
-            last[s * kTile + c] = k[e];
+          for (int e = 0; e < 4; ++e) {
+            lse2[s * kTile + e * 32 + lane] = x[e] * -kLog2e;
+            last[s * kTile + e * 32 + lane] = live(e, hb, i0) ? off + i0 + col_r[e] : kColNone;
           }
           __syncwarp();
         }
-        if (!note(told)) {
+        // a column is masked for some key of the tile in the first tiles only
+        const bool whole = off + i0 >= key0 + kTile - 1 && (hb + 1) * a.gb <= a.group;
+        if (!note(Note{(whole ? kWhole : 0) | (v + 2 * split >= steps ? kLast : 0) | (leave ? kLeave : 0), s,
+                       min(a.R, n - i0) * a.gb, key0, keys, 0, row})) {
           ok = false;
           break;
         }
+        advance(hb, i0);
       }
       if (ok && rank < steps && rank + split >= steps) ok = note(Note{kLast, 0, 0, key0, keys, 0, row});
       if (lay) flips ^= (1u << min(steps, ST)) - 1;
+      if (ok && resident && fresh) {  // the next item's notes may be the other warp's
+        if (lane == 0) mbar_arrive(both);
+        ok = __all_sync(0xffffffffu, mbar_wait_short(both, laid_units & 1));
+        ++laid_units;
+      }
     }
     for (int e = 0; ok && e < 2; ++e) ok = note(Note{kStop, 0, 0, 0, 0, 0, 0});
   } else {
@@ -1368,7 +1390,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       const Note note = notes[w];
       if (note.flags & kStop) break;
       tc_fence_after();
-      const int s = note.stage, key = note.key0 + row;
+      const int s = note.slot, key = note.key0 + row;
       const int live = note.live - half * 64;  // of the warp's columns
       const float* x = lse2 + s * kTile + half * 64;
       const int* k = last + s * kTile + half * 64;
@@ -1412,7 +1434,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       acc += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       if (note.flags & kLeave) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);
+        if (lane == 0) mbar_arrive(&cfree[s]);
       }
       if (!(note.flags & kLast)) continue;
       // the four groups' sums: warps 4..15 hand theirs over, warps 0..3 add and store
