@@ -6,8 +6,8 @@
 // start (its queries, its first copies) is paid once for about a hundred pages.  A unit
 // that a cut goes through leaves partial results, which a second kernel joins; where the
 // tables are short, a CTA takes a whole unit and there is no second kernel.
-// A CTA's four warps take a stretch's pages in turn, each with its own ring of bulk
-// copies (one 16-token page of one head is one contiguous copy), its own running maximum
+// A CTA's four warps take a stretch's pages two at a time in turn, each with its own ring of
+// bulk copies (one 16-token page of one head is one contiguous copy), its own running maximum
 // and sum, and its own output accumulators.  Scores and outputs run on mma.sync
 // m16n8k16: the eight query heads are the N of both products, so a page's codes are read
 // once for all of them.  With N = 8 the products are small (2 x 16 x 8 x D per page) and
@@ -15,7 +15,7 @@
 // or tensor memory, N of a whole tile) could only take after a round trip through shared
 // memory.
 //
-//   scores   s[t, h] = sum_g ( sc[t, g] * sum_{c in g} n[t, c] q[h, c] + z[t, g] * sum_{c in g} q[h, c] )
+//   scores   s[t, h] = sum_g ( sc[t, g] * sum_{c in g} n[t, c] q[h, c] ) + sum_g z[t, g] * sum_{c in g} q[h, c]
 //     A = the codes n of the page's tokens, B = q.  A masked code (w & 0x000f000f) is
 //     already two fp16 numbers, n 2^-24 (subnormal, exact), and (w & 0x00f000f0) is
 //     16 n 2^-24, so widening costs one AND for two codes; q is bf16, scaled by a power
@@ -60,8 +60,9 @@ struct DecodeArgs {
 
 template <int D>
 struct DecodeSmem {
-  static constexpr int kStages = D == 128 ? 4 : 6;
-  static constexpr int kRing = kWarps * kStages * Kv4<D>::kBytes;
+  static constexpr int kPair = 2 * Kv4<D>::kBytes;   // a stage: two pages
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kRing = kWarps * kStages * kPair;
   static constexpr int kMerge = kWarps * kHeads * D * 4;  // shares the ring's bytes
   static constexpr int kBytes = (kRing > kMerge ? kRing : kMerge);
 };
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_decode_kernel(const Decod
   __shared__ int64_t sums[kWarps];
   __shared__ int64_t begin[2];  // the stretch's first sequence, and the pages before it
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  if (lane < ST) mbar_init(&full[warp * ST + lane], 1);
+  if (lane < ST) mbar_init(&full[warp * ST + lane], 2);
   fence_mbar_init();
   pdl_wait();
   pdl_launch_dependents();
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_decode_kernel(const Decod
     before = begin[1];
   }
 
-  uint8_t* ring = sm + warp * ST * P::kBytes;
+  uint8_t* ring = sm + warp * ST * SM::kPair;
   uint64_t* bar = full + warp * ST;
   int s = 0;           // the ring's next stage
   uint32_t ph = 0;     // and its phase
@@ -221,15 +222,17 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_decode_kernel(const Decod
     const int kv = u / a.head_blocks, hb = u % a.head_blocks;
     const int heads = min(kHeads, a.group - hb * kHeads);
     const int h0 = kv * a.group + hb * kHeads;
-    // ---- the warp's copies: pages p0 + warp + 4 i
-    const int mine = (p1 - p0 - warp + kWarps - 1) / kWarps;  // pages of this warp (may be <= 0)
-    const int32_t* table = a.block_table + (int64_t)b * a.max_pages + p0 + warp;
+    // ---- the warp's copies: pairs of pages first + 8 i, first + 8 i + 1
+    const int first = p0 + 2 * warp;
+    const int mine = (p1 - first + 2 * kWarps - 1) / (2 * kWarps);  // pairs of this warp (may be <= 0; the last may lack its second page)
+    const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
     const uint8_t* head_pages = a.pool.pages + (int64_t)kv * P::kBytes;
-    int32_t ids = 0, ids_next = 0;  // lane i: page of iteration (base of 32) + i, and of 32 further
+    int32_t ids = 0, ids_next = 0;  // lane 2 i + f: page f of iteration (base of 16) + i, and of 16 further
     auto load_ids = [&](int base) -> int32_t {
+      const int page = first + (base + (lane >> 1)) * 2 * kWarps + (lane & 1);
       int32_t id = -1;
-      if (base + lane < mine) {
-        id = table[(base + lane) * kWarps];
+      if (page < p1) {
+        id = table[page];
         if (id < 0 || id >= a.pool.n_pages) {
           set_status(a.status, STARKV_DEV_BAD_PAGE);
           id = -1;
@@ -238,17 +241,18 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_decode_kernel(const Decod
       return id;
     };
     ids = load_ids(0);
-    ids_next = load_ids(32);
+    ids_next = load_ids(16);
     uint32_t there = __ballot_sync(0xffffffffu, ids >= 0);
-    // issue the copy of iteration i to stage st: the lane that holds the page's id does
+    // issue the copies of iteration i to stage st: the lanes that hold the pages' ids do
     auto issue = [&](int i, int base, int st) {
-      if (lane == (i & 31) && i < mine) {
-        const int32_t id = i - base < 32 ? ids : ids_next;
+      if ((lane >> 1) == (i & 15) && i < mine) {
+        const int32_t id = i - base < 16 ? ids : ids_next;
         if (id < 0) {
-          mbar_arrive(&bar[st]);  // nothing to copy: the page is left out
+          mbar_arrive(&bar[st]);  // nothing to copy: there is no page, or it is left out
         } else {
           mbar_arrive_expect_tx(&bar[st], P::kBytes);
-          bulk_g2s(ring + st * P::kBytes, head_pages + (int64_t)id * a.pool.h_kv * P::kBytes, P::kBytes, &bar[st]);
+          bulk_g2s(ring + st * SM::kPair + (lane & 1) * P::kBytes, head_pages + (int64_t)id * a.pool.h_kv * P::kBytes,
+                   P::kBytes, &bar[st]);
         }
       }
     };
@@ -257,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_decode_kernel(const Decod
 
     // ---- q: B operands of the score products, and the sums that the zero-points take
     uint32_t qb[NG][4];
-    float qsum[NG][2];
+    uint32_t qz[2] = {0, 0};
     float fq[2];
     {
       const __nv_bfloat16* qrow = a.q + ((int64_t)b * a.H + h0 + g) * D;
@@ -298,10 +302,16 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_decode_kernel(const Decod
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        sum *= 5.9604644775390625e-8f;  // 2^-24: the unit of the products' sums
-        // D's columns 2t, 2t+1 are heads 2t, 2t+1: their sums sit in lanes 4 h
-        qsum[kp][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
-        qsum[kp][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+        // the zero-points' operand: the head's sum in three fp16 pieces (33 bits, as good as fp32), piece e of
+        // group kp at k = NG e + kp; scaled by 2^-5 the first is at most 2^14
+        sum *= 0.03125f;
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+          const __half piece = __float2half_rn(sum);
+          sum -= __half2float(piece);
+          const int k = NG * e + kp;  // the lane holds k = 2 t, 2 t + 1 (and 8 further)
+          if (t == (k & 7) >> 1) qz[k >> 3] |= (uint32_t)__half_as_ushort(piece) << (16 * (k & 1));
+        }
         // code i of a word sits at bits 4 i: the pairs are (0, 4), (1, 5), (2, 6), (3, 7)
         qb[kp][0] = pack_h2(x[kp][0], x[kp][4]);
         qb[kp][1] = pack_h2(x[kp][1] * 0.0625f, x[kp][5] * 0.0625f);
@@ -316,92 +326,112 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_decode_kernel(const Decod
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[m][i] = 0.f;
     float mx[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f};
-    float* srow = nullptr;  // scores of the warp's page, from token tok_a and head 2 t on
+    float* srow = nullptr;  // scores of the warp's pair, from token tok_a and head 2 t on
     if (a.scores && 2 * t < heads)
-      srow = a.scores + (((int64_t)b * a.pool.h_kv + kv) * a.max_pages * kPage + (p0 + warp) * kPage + tok_a) * a.score_heads +
+      srow = a.scores + (((int64_t)b * a.pool.h_kv + kv) * a.max_pages * kPage + (int64_t)first * kPage + tok_a) * a.score_heads +
              hb * kHeads + 2 * t;
-    int left = len - (p0 + warp) * kPage;  // tokens of the page (16 or more: all)
+    int left = len - first * kPage;  // tokens of the pair's pages (32 or more: all)
     int done = 0;
 
 #pragma unroll 1
     for (int i = 0; i < mine; ++i) {
-      if ((i & 31) == 0 && i > 0) {
+      if ((i & 15) == 0 && i > 0) {
         ids = ids_next;
-        ids_next = load_ids(i + 32);
+        ids_next = load_ids(i + 16);
         there = __ballot_sync(0xffffffffu, ids >= 0);
       }
-      issue(i + ST - 1, i & ~31, s == 0 ? ST - 1 : s - 1);
+      issue(i + ST - 1, i & ~15, s == 0 ? ST - 1 : s - 1);
       if (!__all_sync(0xffffffffu, mbar_test(&bar[s], ph)) && !__all_sync(0xffffffffu, mbar_wait(&bar[s], ph))) {
         ok = false;
         break;
       }
       done = i + 1;
-      const uint8_t* pg = ring + s * P::kBytes;
+      const uint8_t* pair_at = ring + s * SM::kPair;
       if (++s == ST) {
         s = 0;
         ph ^= 1;
       }
-      const int held = (there >> (i & 31)) & 1 ? left : 0;  // the page's tokens that count
-      left -= kWarps * kPage;
-      // ---- scores of tokens tok_a (row g) and tok_a + 8 (row g + 8), without fq
-      uint32_t ka[NG], kb[NG], ma[NG], mb[NG];
-      if constexpr (D == 128) {
-        const uint4 x = *reinterpret_cast<const uint4*>(pg + tok_a * P::kRow + t * 16);
-        const uint4 y = *reinterpret_cast<const uint4*>(pg + (tok_a + 8) * P::kRow + t * 16);
-        const uint4 z = *reinterpret_cast<const uint4*>(pg + P::kKMeta + tok_a * P::kMetaRow);
-        const uint4 w = *reinterpret_cast<const uint4*>(pg + P::kKMeta + (tok_a + 8) * P::kMetaRow);
-        ka[0] = x.x, ka[1] = x.y, ka[2] = x.z, ka[3] = x.w;
-        kb[0] = y.x, kb[1] = y.y, kb[2] = y.z, kb[3] = y.w;
-        ma[0] = z.x, ma[1] = z.y, ma[2] = z.z, ma[3] = z.w;
-        mb[0] = w.x, mb[1] = w.y, mb[2] = w.z, mb[3] = w.w;
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(pg + tok_a * P::kRow + t * 8);
-        const uint2 y = *reinterpret_cast<const uint2*>(pg + (tok_a + 8) * P::kRow + t * 8);
-        const uint2 z = *reinterpret_cast<const uint2*>(pg + P::kKMeta + tok_a * P::kMetaRow);
-        const uint2 w = *reinterpret_cast<const uint2*>(pg + P::kKMeta + (tok_a + 8) * P::kMetaRow);
-        ka[0] = x.x, ka[1] = x.y;
-        kb[0] = y.x, kb[1] = y.y;
-        ma[0] = z.x, ma[1] = z.y;
-        mb[0] = w.x, mb[1] = w.y;
-      }
-      float sa[2] = {0.f, 0.f}, sb[2] = {0.f, 0.f};
+      const uint32_t in = there >> (2 * (i & 15));
+      const int held[2] = {in & 1 ? left : 0, in & 2 ? left - kPage : 0};  // the pages' tokens that count
+      // ---- scores of tokens tok_a (row g) and tok_a + 8 (row g + 8) of both pages, without fq
+      float sa[2][2], sb[2][2];
 #pragma unroll
-      for (int kp = 0; kp < NG; ++kp) {
-        float d[4];
-        const uint32_t wa = ka[kp], wb = kb[kp], va = wa >> 8, vb = wb >> 8;
-        mma16816_zero(d, wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u, qb[kp][0], qb[kp][1]);
-        mma16816(d, va & 0x000f000fu, vb & 0x000f000fu, va & 0x00f000f0u, vb & 0x00f000f0u, qb[kp][2], qb[kp][3]);
-        const float2 sza = unpack_meta(ma[kp]), szb = unpack_meta(mb[kp]);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          sa[c] = fmaf(sza.x, d[c], fmaf(sza.y, qsum[kp][c], sa[c]));
-          sb[c] = fmaf(szb.x, d[2 + c], fmaf(szb.y, qsum[kp][c], sb[c]));
-        }
-      }
-      if (held < kPage) {  // a sequence's last page, or one that is left out: free slots may hold anything
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (tok_a >= held) sa[c] = -INFINITY;
-          if (tok_a + 8 >= held) sb[c] = -INFINITY;
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        sa[c] *= fq[c];
-        sb[c] *= fq[c];
-      }
-      if (srow) {
-        if (a.score_heads == 1) {
-          srow[0] = sa[0];
-          srow[8] = sb[0];
+      for (int f = 0; f < 2; ++f) {
+        const uint8_t* pg = pair_at + f * P::kBytes;
+        uint32_t ka[NG], kb[NG], ma[NG], mb[NG];
+        uint32_t za, zb;  // A of the zero-points' product: the k-th column holds group k mod NG's
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(pg + tok_a * P::kRow + t * 16);
+          const uint4 y = *reinterpret_cast<const uint4*>(pg + (tok_a + 8) * P::kRow + t * 16);
+          const uint4 z = *reinterpret_cast<const uint4*>(pg + P::kKMeta + tok_a * P::kMetaRow);
+          const uint4 w = *reinterpret_cast<const uint4*>(pg + P::kKMeta + (tok_a + 8) * P::kMetaRow);
+          ka[0] = x.x, ka[1] = x.y, ka[2] = x.z, ka[3] = x.w;
+          kb[0] = y.x, kb[1] = y.y, kb[2] = y.z, kb[3] = y.w;
+          ma[0] = z.x, ma[1] = z.y, ma[2] = z.z, ma[3] = z.w;
+          mb[0] = w.x, mb[1] = w.y, mb[2] = w.z, mb[3] = w.w;
+          za = t & 1 ? __byte_perm(z.z, z.w, 0x7632) : __byte_perm(z.x, z.y, 0x7632);
+          zb = t & 1 ? __byte_perm(w.z, w.w, 0x7632) : __byte_perm(w.x, w.y, 0x7632);
         } else {
-          *reinterpret_cast<float2*>(srow) = make_float2(sa[0], sa[1]);
-          *reinterpret_cast<float2*>(srow + 8 * a.score_heads) = make_float2(sb[0], sb[1]);
+          const uint2 x = *reinterpret_cast<const uint2*>(pg + tok_a * P::kRow + t * 8);
+          const uint2 y = *reinterpret_cast<const uint2*>(pg + (tok_a + 8) * P::kRow + t * 8);
+          const uint2 z = *reinterpret_cast<const uint2*>(pg + P::kKMeta + tok_a * P::kMetaRow);
+          const uint2 w = *reinterpret_cast<const uint2*>(pg + P::kKMeta + (tok_a + 8) * P::kMetaRow);
+          ka[0] = x.x, ka[1] = x.y;
+          kb[0] = y.x, kb[1] = y.y;
+          ma[0] = z.x, ma[1] = z.y;
+          mb[0] = w.x, mb[1] = w.y;
+          za = __byte_perm(z.x, z.y, 0x7632);
+          zb = __byte_perm(w.x, w.y, 0x7632);
         }
-        srow += kWarps * kPage * a.score_heads;
+        float d[4];
+        mma16816_zero(d, za, zb, za, zb, qz[0], qz[1]);
+        // 2^5 (the pieces' scale) 2^-24 (the unit of the codes' products)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          sa[f][c] = d[c] * 1.9073486328125e-6f;
+          sb[f][c] = d[2 + c] * 1.9073486328125e-6f;
+        }
+#pragma unroll
+        for (int kp = 0; kp < NG; ++kp) {
+          const uint32_t wa = ka[kp], wb = kb[kp], va = wa >> 8, vb = wb >> 8;
+          mma16816_zero(d, wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u, qb[kp][0], qb[kp][1]);
+          mma16816(d, va & 0x000f000fu, vb & 0x000f000fu, va & 0x00f000f0u, vb & 0x00f000f0u, qb[kp][2], qb[kp][3]);
+          const float sca = __low2float(*reinterpret_cast<const __half2*>(&ma[kp]));
+          const float scb = __low2float(*reinterpret_cast<const __half2*>(&mb[kp]));
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            sa[f][c] = fmaf(sca, d[c], sa[f][c]);
+            sb[f][c] = fmaf(scb, d[2 + c], sb[f][c]);
+          }
+        }
+        if (held[f] < kPage) {  // a sequence's last page, or one that is left out: free slots may hold anything
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if (tok_a >= held[f]) sa[f][c] = -INFINITY;
+            if (tok_a + 8 >= held[f]) sb[f][c] = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          sa[f][c] *= fq[c];
+          sb[f][c] *= fq[c];
+        }
+        if (srow && (f == 0 || first + i * 2 * kWarps + 1 < p1)) {
+          float* to = srow + f * kPage * a.score_heads;
+          if (a.score_heads == 1) {
+            to[0] = sa[f][0];
+            to[8] = sb[f][0];
+          } else {
+            *reinterpret_cast<float2*>(to) = make_float2(sa[f][0], sa[f][1]);
+            *reinterpret_cast<float2*>(to + 8 * a.score_heads) = make_float2(sb[f][0], sb[f][1]);
+          }
+        }
       }
+      if (srow) srow += 2 * kWarps * kPage * a.score_heads;
+      left -= 2 * kWarps * kPage;
       // ---- running maximum (per head; the same in the eight lanes that share its columns)
-      const float c0 = fmaxf(sa[0], sb[0]), c1 = fmaxf(sa[1], sb[1]);
+      const float c0 = fmaxf(fmaxf(sa[0][0], sb[0][0]), fmaxf(sa[1][0], sb[1][0]));
+      const float c1 = fmaxf(fmaxf(sa[0][1], sb[0][1]), fmaxf(sa[1][1], sb[1][1]));
       if (__any_sync(0xffffffffu, c0 > mx[0] + kMoveMax || c1 > mx[1] + kMoveMax)) {
         float n0 = fmaxf(mx[0], c0), n1 = fmaxf(mx[1], c1);
 #pragma unroll
@@ -422,64 +452,68 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_decode_kernel(const Decod
           o[m][3] *= r1;
         }
       }
-      const float pa0 = ex2(sa[0] - mx[0]), pa1 = ex2(sa[1] - mx[1]);
-      const float pb0 = ex2(sb[0] - mx[0]), pb1 = ex2(sb[1] - mx[1]);
-      l[0] += pa0 + pb0;
-      l[1] += pa1 + pb1;
-      const uint32_t b0 = movm_trans(pack_h2(pa0, pa1)), b1 = movm_trans(pack_h2(pb0, pb1));
-      // ---- V: the thread's D/8 channels (from (D/8) g) of tokens (e, f) = j, all in one group
-      uint32_t vm[4], vw[4][2];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int tok = token_of(t, j & 1, j >> 1);
-        if constexpr (D == 128) {
-          const uint2 x = *reinterpret_cast<const uint2*>(pg + P::kV + tok * P::kRow + g * 8);
-          vw[j][0] = x.x;
-          vw[j][1] = x.y;
-          vm[j] = *reinterpret_cast<const uint32_t*>(pg + P::kVMeta + tok * P::kMetaRow + (g >> 1) * 4);
-        } else {
-          vw[j][0] = *reinterpret_cast<const uint32_t*>(pg + P::kV + tok * P::kRow + g * 4);
-          vm[j] = *reinterpret_cast<const uint32_t*>(pg + P::kVMeta + tok * P::kMetaRow + (g >> 2) * 4);
-        }
-      }
-      if (held < kPage) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (token_of(t, j & 1, j >> 1) >= held) vm[j] = 0;
-      }
-      uint32_t sc[2], ze[2];
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        sc[f] = __byte_perm(vm[2 * f], vm[2 * f + 1], 0x5410);
-        ze[f] = __byte_perm(vm[2 * f], vm[2 * f + 1], 0x7632);
-      }
-      const __half2 k1024 = __halves2half2(__ushort_as_half(0x6400), __ushort_as_half(0x6400));
-      const __half2 k16th = __halves2half2(__ushort_as_half(0x2c00), __ushort_as_half(0x2c00));
-      const __half2 km64 = __halves2half2(__ushort_as_half(0xd400), __ushort_as_half(0xd400));
-      // codes at bits 0..3 (or 4..7) of both halves -> fp16 values code * s + z
-      auto even = [&](uint32_t y, int f) -> uint32_t {
-        const uint32_t x = (y & 0x000f000fu) | 0x64006400u;  // 1024 + n
-        const __half2 n = __hsub2(*reinterpret_cast<const __half2*>(&x), k1024);
-        const __half2 v = __hfma2(n, *reinterpret_cast<const __half2*>(&sc[f]), *reinterpret_cast<const __half2*>(&ze[f]));
-        return *reinterpret_cast<const uint32_t*>(&v);
-      };
-      auto odd = [&](uint32_t y, int f) -> uint32_t {
-        const uint32_t x = (y & 0x00f000f0u) | 0x64006400u;  // 1024 + 16 n
-        const __half2 n = __hfma2(*reinterpret_cast<const __half2*>(&x), k16th, km64);
-        const __half2 v = __hfma2(n, *reinterpret_cast<const __half2*>(&sc[f]), *reinterpret_cast<const __half2*>(&ze[f]));
-        return *reinterpret_cast<const uint32_t*>(&v);
-      };
+        const uint8_t* pg = pair_at + f * P::kBytes;
+        const float pa0 = ex2(sa[f][0] - mx[0]), pa1 = ex2(sa[f][1] - mx[1]);
+        const float pb0 = ex2(sb[f][0] - mx[0]), pb1 = ex2(sb[f][1] - mx[1]);
+        l[0] += pa0 + pb0;
+        l[1] += pa1 + pb1;
+        const uint32_t b0 = movm_trans(pack_h2(pa0, pa1)), b1 = movm_trans(pack_h2(pb0, pb1));
+        // ---- V: the thread's D/8 channels (from (D/8) g) of tokens (e, h) = j, all in one group
+        uint32_t vm[4], vw[4][2];
 #pragma unroll
-      for (int w = 0; w < D / 64; ++w) {
-        // channels 0..3 (x) and 4..7 (y) of word w, tokens j = 0, 1 and j = 2, 3 in the halves
-        const uint32_t x0 = __byte_perm(vw[0][w], vw[1][w], 0x5410), y0 = __byte_perm(vw[0][w], vw[1][w], 0x7632);
-        const uint32_t x1 = __byte_perm(vw[2][w], vw[3][w], 0x5410), y1 = __byte_perm(vw[2][w], vw[3][w], 0x7632);
-        mma16816(o[4 * w], even(x0, 0), even(y0, 0), even(x1, 1), even(y1, 1), b0, b1);
-        mma16816(o[4 * w + 1], odd(x0, 0), odd(y0, 0), odd(x1, 1), odd(y1, 1), b0, b1);
-        mma16816(o[4 * w + 2], even(x0 >> 8, 0), even(y0 >> 8, 0), even(x1 >> 8, 1), even(y1 >> 8, 1), b0, b1);
-        mma16816(o[4 * w + 3], odd(x0 >> 8, 0), odd(y0 >> 8, 0), odd(x1 >> 8, 1), odd(y1 >> 8, 1), b0, b1);
+        for (int j = 0; j < 4; ++j) {
+          const int tok = token_of(t, j & 1, j >> 1);
+          if constexpr (D == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(pg + P::kV + tok * P::kRow + g * 8);
+            vw[j][0] = x.x;
+            vw[j][1] = x.y;
+            vm[j] = *reinterpret_cast<const uint32_t*>(pg + P::kVMeta + tok * P::kMetaRow + (g >> 1) * 4);
+          } else {
+            vw[j][0] = *reinterpret_cast<const uint32_t*>(pg + P::kV + tok * P::kRow + g * 4);
+            vm[j] = *reinterpret_cast<const uint32_t*>(pg + P::kVMeta + tok * P::kMetaRow + (g >> 2) * 4);
+          }
+        }
+        if (held[f] < kPage) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (token_of(t, j & 1, j >> 1) >= held[f]) vm[j] = 0;
+        }
+        uint32_t sc[2], ze[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          sc[h] = __byte_perm(vm[2 * h], vm[2 * h + 1], 0x5410);
+          ze[h] = __byte_perm(vm[2 * h], vm[2 * h + 1], 0x7632);
+        }
+        const __half2 k1024 = __halves2half2(__ushort_as_half(0x6400), __ushort_as_half(0x6400));
+        const __half2 k16th = __halves2half2(__ushort_as_half(0x2c00), __ushort_as_half(0x2c00));
+        const __half2 km64 = __halves2half2(__ushort_as_half(0xd400), __ushort_as_half(0xd400));
+        // codes at bits 0..3 (or 4..7) of both halves -> fp16 values code * s + z
+        auto even = [&](uint32_t y, int h) -> uint32_t {
+          const uint32_t x = (y & 0x000f000fu) | 0x64006400u;  // 1024 + n
+          const __half2 n = __hsub2(*reinterpret_cast<const __half2*>(&x), k1024);
+          const __half2 v = __hfma2(n, *reinterpret_cast<const __half2*>(&sc[h]), *reinterpret_cast<const __half2*>(&ze[h]));
+          return *reinterpret_cast<const uint32_t*>(&v);
+        };
+        auto odd = [&](uint32_t y, int h) -> uint32_t {
+          const uint32_t x = (y & 0x00f000f0u) | 0x64006400u;  // 1024 + 16 n
+          const __half2 n = __hfma2(*reinterpret_cast<const __half2*>(&x), k16th, km64);
+          const __half2 v = __hfma2(n, *reinterpret_cast<const __half2*>(&sc[h]), *reinterpret_cast<const __half2*>(&ze[h]));
+          return *reinterpret_cast<const uint32_t*>(&v);
+        };
+#pragma unroll
+        for (int w = 0; w < D / 64; ++w) {
+          // channels 0..3 (x) and 4..7 (y) of word w, tokens j = 0, 1 and j = 2, 3 in the halves
+          const uint32_t x0 = __byte_perm(vw[0][w], vw[1][w], 0x5410), y0 = __byte_perm(vw[0][w], vw[1][w], 0x7632);
+          const uint32_t x1 = __byte_perm(vw[2][w], vw[3][w], 0x5410), y1 = __byte_perm(vw[2][w], vw[3][w], 0x7632);
+          mma16816(o[4 * w], even(x0, 0), even(y0, 0), even(x1, 1), even(y1, 1), b0, b1);
+          mma16816(o[4 * w + 1], odd(x0, 0), odd(y0, 0), odd(x1, 1), odd(y1, 1), b0, b1);
+          mma16816(o[4 * w + 2], even(x0 >> 8, 0), even(y0 >> 8, 0), even(x1 >> 8, 1), even(y1 >> 8, 1), b0, b1);
+          mma16816(o[4 * w + 3], odd(x0 >> 8, 0), odd(y0 >> 8, 0), odd(x1 >> 8, 1), odd(y1 >> 8, 1), b0, b1);
+        }
       }
-      __syncwarp();  // every lane has read the stage before its next copy is issued
+      __syncwarp();  // every lane has read the stage before its next copies are issued
     }
     if (!ok) {
       // give up: wait (with a limit) for the copies in flight before the memory is left
