@@ -101,12 +101,13 @@ STARKV_API starkv_status starkv_kv4_read(starkv_ctx* ctx, const starkv_kv4_cache
  * [batch][num_q_heads][head_dim] (dense); sequence b's query attends to tokens
  * [0, seq_lens[b]).  out: device bf16 [batch][num_q_heads][head_dim]; seq_len 0 gives a
  * zero row.  accumulate != 0: cache.weights of each attended token gains the
- * probabilities that the query heads of its KV head gave it (every page at most
- * once among the tables' used entries: a page in two tables gains both, in an order
- * that is not fixed).  A bad length sets its bit and gives a zero row and no weight; a bad
- * page sets its bit, and its tokens are left out.
+ * probabilities that the query heads of its KV head gave it.  A page that stands in two
+ * tables gains both sequences' share; the order of those additions is not fixed, all else
+ * is.  A bad length sets its bit and gives a zero row and no weight; a bad page sets its
+ * bit, and its tokens are left out.
  * workspace: >= starkv_workspace_bytes(STARKV_OP_KV4_DECODE, batch, max_pages, total_q =
  * accumulate), 256-byte aligned; it must not be used by another call at the same time.
+ * It grows with max_pages where weights are accumulated (4 bytes a token and query head).
  * Errors: INVALID_ARG, WORKSPACE_TOO_SMALL; device bits BAD_PAGE, BAD_SEQ_LEN. */
 STARKV_API starkv_status starkv_kv4_decode_attn(starkv_ctx* ctx, const starkv_kv4_cache* cache, const void* q,
                                                 const int32_t* block_table, const int32_t* seq_lens, int32_t batch,

@@ -429,3 +429,111 @@ def test_steps_captured_into_graphs_that_run_in_turn():
     for g, cache, *_ in graphs:
         assert torch.equal(cache.pages, plain.pages) and torch.equal(cache.weights, plain.weights)
     assert kv.status() == 0
+
+
+# ---------------------------------------------------------------------------------------------------------------------
+# refusals: from the host's checks, before anything is launched
+# ---------------------------------------------------------------------------------------------------------------------
+def test_calls_that_are_refused():
+    S = skv()
+    H, h, d = 8, 2, 64
+    kv = context(H, h, d)
+    L = S.lib()
+    cache = kv.new_kv4_cache(4, keep_weights=True)
+    bare = kv.new_kv4_cache(4)
+    no_pages = S.starkv_kv4_cache(None, None, 0)
+    big = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    p = big.data_ptr()
+    import ctypes
+    ref, width = ctypes.byref, h * d
+
+    def append(c=cache.struct, k=p, v=p, ks=width, vs=width, slots=p, n=1):
+        return L.starkv_kv4_append(kv.ctx, ref(c), k, v, ks, vs, slots, None, n, None)
+
+    def decode(c=cache.struct, q=p, table=p, lens=p, batch=1, pages=40, acc=0, out=p, ws=p, size=1 << 20):
+        return L.starkv_kv4_decode_attn(kv.ctx, ref(c), q, table, lens, batch, pages, acc, out, ws, size, None)
+
+    def evict(c=cache.struct, recent=1, batch=1, pages=1, dst=1, kept=p):
+        return L.starkv_kv4_evict(kv.ctx, ref(c), p, p, p, recent, batch, pages, p, dst, p, kept, None)
+
+    def read(batch=1, pages=1, total=1, out=p, cu=p):
+        return L.starkv_kv4_read(kv.ctx, ref(cache.struct), p, None, cu, batch, pages, total, out, p, None)
+
+    def prompt(q=p, k=p, v=p, qs=H * d, ks=width, vs=width, batch=1, nq=1, nk=1, most=1, out=p, lse=p, ws=p, size=1 << 20):
+        return L.starkv_prompt_attn(kv.ctx, q, k, v, qs, ks, vs, p, p, batch, nq, nk, most, out, lse, ws, size, None)
+
+    def weigh(lse=p, batch=1, nq=1, nk=1, most=1, window=1, out=p, ks=width):
+        return L.starkv_prompt_weights(kv.ctx, p, p, H * d, ks, lse, p, p, batch, nq, nk, most, window, out, None)
+
+    bad, shape, small = S.ERR_INVALID_ARG, S.ERR_UNSUPPORTED_SHAPE, S.ERR_WORKSPACE_TOO_SMALL
+    refused = [
+        (append(n=-1), bad), (append(k=None), bad), (append(v=p + 2), bad), (append(ks=width - 8), bad), (append(vs=width + 4), bad),
+        (append(slots=None), bad), (append(c=no_pages), bad), (append(n=1 << 40), shape),
+        (append(c=S.starkv_kv4_cache(p + 8, None, 1)), bad), (append(c=S.starkv_kv4_cache(p, p + 4, 1)), bad),
+        (append(c=S.starkv_kv4_cache(None, None, 1)), bad), (append(c=S.starkv_kv4_cache(p, None, -1)), bad),
+        (decode(batch=-1), bad), (decode(pages=0), bad), (decode(batch=65536), shape), (decode(pages=(1 << 26) + 1), shape),
+        (decode(q=None), bad), (decode(out=p + 4), bad), (decode(c=bare.struct, acc=1), bad), (decode(size=16), small),
+        (decode(ws=None), small), (decode(ws=p + 16), bad),
+        (evict(recent=-1), bad), (evict(dst=0), bad), (evict(kept=None), bad), (evict(c=bare.struct), bad), (evict(batch=1 << 17), shape),
+        (read(total=-1), bad), (read(batch=0), bad), (read(out=p + 2), bad), (read(cu=None), bad), (read(total=1 << 40), shape),
+        (prompt(nq=-1), bad), (prompt(most=0), bad), (prompt(batch=0), bad), (prompt(batch=1 << 16), shape), (prompt(nk=1 << 31), shape),
+        (prompt(q=p + 8), bad), (prompt(qs=H * d - 8), bad), (prompt(ks=0), bad), (prompt(vs=width + 1), bad), (prompt(out=None), bad),
+        (prompt(lse=p + 2), bad), (prompt(nk=4096, ws=None), small), (prompt(nk=4096, size=64), small),
+        (prompt(nk=4096, ws=p + 64), small),  # 32 parts of 256 rows take 4 MB, and 1 MB is given
+        (prompt(nk=4096, ws=p + 64, size=1 << 23), bad),
+        (weigh(window=-1), bad), (weigh(most=0), bad), (weigh(lse=None), bad), (weigh(out=p + 2), bad), (weigh(ks=8), bad),
+        (weigh(batch=1 << 16), shape), (weigh(nk=1 << 31, most=1 << 30), shape),
+    ]
+    for i, (got, want) in enumerate(refused):
+        assert got == want, (i, got, want, S.starkv_last_error())
+    # nothing to do is not an error
+    assert append(n=0, k=None, v=None, slots=None) == 0 and decode(batch=0, pages=0) == 0 and evict(batch=0, pages=0, dst=0) == 0
+    assert read(total=0) == 0 and prompt(nq=0, batch=0) == 0 and weigh(nk=0, batch=0) == 0
+    assert kv.status() == 0
+    q = torch.zeros((2, H, d), dtype=torch.bfloat16, device="cuda")
+    table, lens = i32(np.zeros((2, 1))), i32([0, 0])
+    for call in (lambda: kv.kv4_decode(cache, q[:1], table, lens), lambda: kv.kv4_decode(cache, q[:, :4], table, lens),
+                 lambda: kv.kv4_decode(cache, q, table, lens, out=q[:1]), lambda: kv.kv4_read(cache, table, lens, 2),
+                 lambda: kv.prompt(q, q[:, :2], q[:1, :2], lens, lens, 1), lambda: kv.prompt(q[:, :, :32], q, q, lens, lens, 1),
+                 lambda: kv.kv4_append(cache, q[:, :2], q[:, :2], torch.zeros(3, dtype=torch.int64, device="cuda")),
+                 lambda: kv.kv4_decode(cache, q.cpu(), table, lens), lambda: kv.kv4_evict(cache, table, lens, lens, 0, table[:1])):
+        with pytest.raises((ValueError, TypeError)):
+            call()
+
+
+def test_pages_whose_offsets_pass_32_bits():
+    """A pool of more than 4 GB, its last pages in use: write, read, decode with weights, evict."""
+    S = skv()
+    shape = H, h, d = 16, 8, 128
+    rng = np.random.default_rng(15)
+    kv = context(*shape)
+    n_pages = (1 << 32) // (h * F.page_bytes(d)) + 40
+    cache = kv.new_kv4_cache(n_pages, keep_weights=True)
+    n, keep = 70, 40
+    t = np.arange(n_pages - 5, n_pages, dtype=np.int32)[None]
+    dst = np.arange(n_pages - 20, n_pages - 17, dtype=np.int32)[None]
+    slots = F.slots_of(t[0], n)
+    kd, k = keys(rng, n, h, d)
+    vd, v = bf16(rng, n, h, d)
+    kv.kv4_append(cache, kd, vd, torch.from_numpy(slots).cuda())
+    small = np.zeros((5, h, F.page_bytes(d)), np.uint8)
+    F.write(small, k, v, slots - int(t[0, 0]) * 16)
+    np.testing.assert_array_equal(cache.pages[n_pages - 5:].cpu().numpy(), small)
+    kk, vv = F.values(small, slots - int(t[0, 0]) * 16, d)
+    got, _ = kv.kv4_read(cache, i32(t), i32([0, n]), n)
+    np.testing.assert_array_equal(got.float().cpu().numpy(), torch.from_numpy(kk.astype(np.float32)).bfloat16().float().numpy())
+    qd, q = bf16(rng, 1, H, d)
+    out = kv.kv4_decode(cache, qd, i32(t), i32([n]), accumulate=True).double().cpu().numpy()
+    o, _, p, mag = F.attend(q.astype(np.float64), kk, vv, [n])
+    assert (np.abs(out - o) <= 2.0**-8 * np.abs(o) + 2.0**-10 * (mag + np.abs(vv).max())).all()
+    w = cache.weights[n_pages - 5:].cpu().numpy()
+    _, kept = kv.kv4_evict(cache, i32(t), i32([n]), i32([keep]), 4, i32(dst))
+    assert kv.status() == 0
+    local = slots - int(t[0, 0]) * 16
+    moved = cache.pages[n_pages - 20:n_pages - 17].cpu().numpy()
+    for head in range(h):
+        stay = F.kept_tokens(w[local // 16, head, local % 16], n, keep, 4)
+        np.testing.assert_array_equal(kept[0, head, :keep].cpu().numpy(), stay)
+        km, vm = F.values(moved[:, head:head + 1], np.arange(keep), d)
+        np.testing.assert_array_equal(km[:, 0], kk[stay, head])
+        np.testing.assert_array_equal(vm[:, 0], vv[stay, head])

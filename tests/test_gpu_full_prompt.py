@@ -359,3 +359,24 @@ def test_weights_of_every_way_to_share_the_work(shape, n_q, n_k, window):
                 tol = want * (e + 2.0**-17 + 2.0**-14) + 2.0**-24
                 got = w[k0:k0 + m, head].double()
                 assert ((got - want).abs() <= tol).all(), (b, head, (got - want).abs().max())
+
+
+def test_prompt_whose_keys_leave_the_cache():
+    """Keys and values of more than 96 MB with units for every SM: whole units a CTA, the longest first."""
+    shape = H, h, d = 32, 32, 128
+    n, m = 1291, 6400
+    kv = context(*shape)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q = torch.randn((n, H, d), generator=g, device="cuda").bfloat16()
+    k, v = (torch.randn((m, h, d), generator=g, device="cuda").bfloat16() for _ in range(2))
+    out, lse = kv.prompt(q, k, v, i32([0, n]), i32([0, m]), n)
+    assert kv.status() == 0
+    seen = torch.arange(m, device="cuda")[None] <= (m - n + torch.arange(n, device="cuda"))[:, None]
+    for head in (0, 13, 31):
+        z = (q[:, head].double() @ k[:, head].double().t()) / d**0.5
+        e = (q[:, head].double().abs() @ k[:, head].double().abs().t()).amax() * 2.0**-20 / d**0.5
+        z = torch.where(seen, z, -torch.inf)
+        p = torch.softmax(z, -1)
+        o, mag = p @ v[:, head].double(), p @ v[:, head].double().abs()
+        assert ((out[:, head].double() - o).abs() <= 2.0**-8 * (o.abs() + mag) + mag * (2 * e + 2.0**-18)).all()
+        assert ((lse[:, head].double() - torch.logsumexp(z, -1)).abs() <= e + 2.0**-18 + 2.0**-20).all()
