@@ -164,7 +164,7 @@ __device__ __forceinline__ int64_t cta_of(int64_t x, int64_t total, int ctas) {
 // ===========================================================================
 // A unit is two query tiles (2 R queries) of one (sequence, KV head, head block) with all the
 // key tiles that they see.  One CTA an SM takes an equal stretch of the units' key tiles, laid
-// end to end (each unit one position longer, for its start and its end), so that neither few
+// end to end (each unit somewhat longer, for its start and its end), so that neither few
 // long units nor many of unequal lengths leave SMs idle; a unit that a cut goes through leaves
 // partial results, which a second kernel joins.  Where there are few keys, a CTA takes a whole
 // unit and there is no second kernel.
@@ -186,6 +186,9 @@ constexpr int kAttnThreads = 384;
 constexpr int kFewKeys = 1024;
 constexpr int64_t kMostCached = (int64_t)96 << 20;  // bytes of keys and values
 constexpr int kLeastTiles = 2;    // key tiles of a stretch, where there are few
+// Positions that a unit counts for beside its key tiles: its start and its end cost as much as two
+// (sixteen prompts of 1 to 1999 tokens: counted as 1, 2, 3, 4: 261, 243, 249, 255 us).
+constexpr int kUnitCost = 2;
 // Pairs of exponentials that go to the FMA pipe: one of eight.  (2048 queries over 32768 keys: none
 // 914 us, one of eight 894, one of four 982, half 1070: the softmax warps' issue slots bound them too.)
 __device__ constexpr bool on_fma_pipe(int pair) { return pair % 8 == 7; }
@@ -228,11 +231,11 @@ struct Pairs {
     const int64_t seen = (int64_t)off + min((int64_t)n, (int64_t)(i + 1) * M);
     return seen > 0 ? (int)((seen + kTile - 1) / kTile) : 0;
   }
-  // positions (key tiles, and one a pair) of the pairs before pair x
+  // positions (key tiles, and kUnitCost a pair) of the pairs before pair x
   __device__ int64_t before(int x) const {
     const int64_t whole = min(x, count - 1);                               // pairs of M queries
     const int64_t first = off >= 0 ? 0 : ((int64_t)M - off) / M - 1;       // the first that sees a key
-    int64_t sum = x;
+    int64_t sum = (int64_t)x * kUnitCost;
     if (whole > first) sum += floor_sum(whole - first, kTile, M, off + (first + 1) * M + kTile - 1);
     if (x == count && x > 0) sum += tiles(count - 1);
     return sum;
@@ -274,16 +277,16 @@ struct Pieces {
         }
       }
       nt = pairs.tiles(i);
-      const int take = (int)min((int64_t)(nt + 1 - p), end - pos);
-      j0 = max(0, p - 1);
-      j1 = p + take - 1;
+      const int take = (int)min((int64_t)(nt + kUnitCost - p), end - pos);
+      j0 = max(0, p - kUnitCost);
+      j1 = max(0, p + take - kUnitCost);
       kv = u / a.head_blocks;
       hb = u % a.head_blocks;
       pair = i;
       pos += take;
       p += take;
-      fresh = p > nt;
-      if (j1 > j0 || nt == 0) return true;
+      fresh = p == nt + kUnitCost;
+      if (j1 > j0 || (nt == 0 && fresh)) return true;
     }
     return false;
   }
@@ -395,7 +398,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       first_span = q;
       if (!q.ok) set_status(a.status, STARKV_DEV_BAD_QUERY_SPAN);
       const Pairs pairs(q, a.R);
-      begin[1] = i < pairs.count ? pairs.tiles(i) + 1 : 0;
+      begin[1] = i < pairs.count ? pairs.tiles(i) + kUnitCost : 0;
     }
     tc_fence_before();
     __syncthreads();
