@@ -38,7 +38,14 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kHeads = 8;            // query heads of one CTA (the N of the products)
 constexpr int kCtas = 4;             // CTAs of an SM
-constexpr int kWholePages = 32;      // tables of at most this many pages: a CTA takes a whole unit
+// A CTA takes a whole unit where tables hold at most kWholePages pages, or kWholePagesMany where there
+// are kManyUnits units or more; else the pages are cut evenly (a second segment's start in most CTAs,
+// and the join).  Whole and cut in us: 4 heads of 64, 512 tokens 6.2 and 8.4, 2048 tokens 15.4 and 9.1;
+// heads of 128, 64 units of 1024 tokens 12.9 and 14.5, 256 units of 2048 28.4 and 34.7, of 4096 52.8
+// and 52.9 (equal lengths: ragged ones favour the cut).
+constexpr int kWholePages = 32;
+constexpr int kWholePagesMany = 128;
+constexpr int kManyUnits = 64;
 constexpr float kMoveMax = 8.f;      // the running maximum moves when a score passes it by this (log2)
 constexpr float kNoMax = -1e30f;     // running maximum before the first score
 
@@ -666,31 +673,38 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const DecodeArgs
     }
     __syncthreads();
     if (blockIdx.x == 0) {
-      // a warp (or half a warp) a part: the threads of a head's row share its parts out, then add up
-      constexpr int kRow = D / 4;                       // threads of a row
-      constexpr int kWays = kJoinThreads / kRow;        // parts looked at together
-      const int c4 = (tid % kRow) * 4, way = tid / kRow;
-      for (int hh = 0; hh < heads; ++hh) {
-        const int h = h0 + hh;
+      // kRow threads hold a head's row; `side` heads go side by side, and what threads are left share a head's
+      // parts out, then add up
+      constexpr int kRow = D / 4;
+      constexpr int kRows = kJoinThreads / kRow;
+      int side = 1;
+      while (side < heads && side < kRows && side < kHeads) side *= 2;
+      const int ways = kRows / side;
+      const int c4 = (tid % kRow) * 4, way = tid / kRow / side;
+      for (int h1 = 0; h1 < heads; h1 += side) {
+        const int hh = h1 + tid / kRow % side, h = h0 + hh;
         int64_t c0, c1;
-        ctas_of(kv * a.head_blocks + h / kHeads, c0, c1);
-        if (c0 == c1) continue;  // (the same for the whole block)
+        ctas_of(kv * a.head_blocks + (h0 + h1) / kHeads, c0, c1);
+        if (c0 == c1) continue;  // (the same for the whole block: the heads side by side share a unit)
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int64_t c = c0 + way; c <= c1; c += kWays) {
-          const int64_t row = (c * 2 + (c == c0)) * kHeads + h % kHeads;
-          const float r = ex2(a.part_ml[row].x - norm[hh].x);
-          const float4 x = *reinterpret_cast<const float4*>(a.part_o + row * D + c4);
-          v.x = fmaf(x.x, r, v.x);
-          v.y = fmaf(x.y, r, v.y);
-          v.z = fmaf(x.z, r, v.z);
-          v.w = fmaf(x.w, r, v.w);
+        if (hh < heads)
+          for (int64_t c = c0 + way; c <= c1; c += ways) {
+            const int64_t row = (c * 2 + (c == c0)) * kHeads + h % kHeads;
+            const float r = ex2(a.part_ml[row].x - norm[hh].x);
+            const float4 x = *reinterpret_cast<const float4*>(a.part_o + row * D + c4);
+            v.x = fmaf(x.x, r, v.x);
+            v.y = fmaf(x.y, r, v.y);
+            v.z = fmaf(x.z, r, v.z);
+            v.w = fmaf(x.w, r, v.w);
+          }
+        if (ways > 1) {
+          __syncthreads();
+          acc[tid] = v;
+          __syncthreads();
         }
-        __syncthreads();
-        acc[tid] = v;
-        __syncthreads();
-        if (way == 0) {
-          for (int w = 1; w < kWays && w <= c1 - c0; ++w) {
-            const float4 x = acc[w * kRow + tid];
+        if (way == 0 && hh < heads) {
+          for (int w = 1; w < ways && w <= c1 - c0; ++w) {
+            const float4 x = acc[w * side * kRow + tid];
             v.x += x.x;
             v.y += x.y;
             v.z += x.z;
@@ -749,11 +763,11 @@ Kv4DecodePlan plan_kv4_decode(const Ctx& c, int batch, int max_pages, bool accum
   p.units = f.num_kv_heads * p.head_blocks;
   int sms = 148;
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c.device);
-  // One round of CTAs, with 8 pages (2 a warp) at least where the tables are full; a whole unit
-  // each where no table holds more than kWholePages.
+  // one round of CTAs, with 8 pages (a pair a warp) at least where the tables are full
+  const bool whole = max_pages <= ((int64_t)batch * p.units >= kManyUnits ? kWholePagesMany : kWholePages);
   const int64_t most = (int64_t)batch * p.units * max_pages;
   const int64_t round = (int64_t)sms * kCtas;
-  p.ctas = max_pages <= kWholePages ? 0 : (int)(most / 8 < round ? most / 8 : round);
+  p.ctas = whole ? 0 : (int)(most / 8 < round ? most / 8 : round);
   p.score_heads = !accumulate ? 0 : c.group <= 2 ? c.group : (c.group + 3) / 4 * 4;
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t rows = (size_t)p.ctas * 2 * kHeads;
