@@ -11,7 +11,7 @@ namespace {
 // ---------------------------------------------------------------------------
 // Append.  A thread quantises one group of 32 channels (four 16-byte loads, four code words):
 // the group's scale is worked out once and no thread waits for another.  The kernel is bound by
-// its instructions, about 80 a code word (with eight channels a thread, the group's ends by
+// its instructions, 127 a code word (with eight channels a thread, the group's ends by
 // shuffles and the scale worked out four times, it took 222, and 70 us instead of 46 for 8098
 // tokens of 32 heads of 128: 3.8 TB/s).
 // ---------------------------------------------------------------------------

@@ -8,7 +8,9 @@ fallback path.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
+import functools
 import os
 
 import torch
@@ -429,6 +431,10 @@ def starkv_kv4_append(ctx, cfg, cache: starkv_kv4_cache, k, v, slot_mapping, wei
                                    k.shape[0], _on(stream)))
 
 
+# What the checks below look up in a configuration, without a C structure's cost for each look.
+_Heads = collections.namedtuple("_Heads", "num_q_heads num_kv_heads head_dim")
+
+
 # Each entry has its checks of what the caller gives apart from its call: the methods of StarKV below make their own
 # outputs and workspaces, which need none.
 def _check_read(block_table, cu, starts):
@@ -489,23 +495,34 @@ def starkv_kv4_decode_attn(ctx, cfg, cache: starkv_kv4_cache, q, block_table, se
     _call_decode(ctx, cache, q, block_table, seq_lens, accumulate, out, workspace, stream)
 
 
+def _check_evict(block_table, seq_lens, keep_lens, dst_block_table):
+    _need(block_table, torch.int32, "block_table", 2)
+    _need(dst_block_table, torch.int32, "dst_block_table", 2)
+    _need(seq_lens, torch.int32, "seq_lens", 1)
+    _need(keep_lens, torch.int32, "keep_lens", 1)
+    B = block_table.shape[0]
+    if seq_lens.shape[0] != B or keep_lens.shape[0] != B or dst_block_table.shape[0] != B:
+        raise ValueError("block_table / seq_lens / keep_lens / dst_block_table disagree on the batch")
+
+
+def _call_evict(ctx, cache, block_table, seq_lens, keep_lens, recent, dst_block_table, new_lens, kept, stream):
+    B, pages = block_table.shape
+    _check(lib().starkv_kv4_evict(ctx, ctypes.byref(cache), _at(block_table), _at(seq_lens), _at(keep_lens), int(recent),
+                                  B, pages, _at(dst_block_table), dst_block_table.shape[1], _at(new_lens), _at(kept),
+                                  _on(stream)))
+
+
 def starkv_kv4_evict(ctx, cfg, cache: starkv_kv4_cache, block_table, seq_lens, keep_lens, recent, dst_block_table,
                      new_lens, kept, stream=None):
     """Gather the kept tokens (the `recent` last and the heaviest others, per KV head) into other pages."""
-    for t, n in ((block_table, "block_table"), (dst_block_table, "dst_block_table")):
-        _need(t, torch.int32, n, 2)
-    B, cap = block_table.shape[0], dst_block_table.shape[1] * PAGE_TOKENS
-    for t, n in ((seq_lens, "seq_lens"), (keep_lens, "keep_lens"), (new_lens, "new_lens")):
-        _need(t, torch.int32, n, 1)
-        if t.shape[0] != B:
-            raise ValueError(f"{n} and block_table disagree on the batch")
+    _check_evict(block_table, seq_lens, keep_lens, dst_block_table)
+    B, pages = dst_block_table.shape
+    _need(new_lens, torch.int32, "new_lens", 1)
     _need(kept, torch.int32, "kept", 3)
-    if dst_block_table.shape[0] != B or tuple(kept.shape) != (B, cfg.num_kv_heads, cap):
-        raise ValueError(f"dst_block_table must have {B} rows and kept be [{B}, {cfg.num_kv_heads}, {cap}]")
+    if new_lens.shape[0] != B or kept.shape != (B, cfg.num_kv_heads, pages * PAGE_TOKENS):
+        raise ValueError(f"new_lens must be [{B}] and kept [{B}, {cfg.num_kv_heads}, {pages * PAGE_TOKENS}]")
     _one_device(block_table, seq_lens, keep_lens, dst_block_table, new_lens, kept)
-    _check(lib().starkv_kv4_evict(ctx, ctypes.byref(cache), _at(block_table), _at(seq_lens), _at(keep_lens), int(recent),
-                                  B, block_table.shape[1], _at(dst_block_table), dst_block_table.shape[1],
-                                  _at(new_lens), _at(kept), _on(stream)))
+    _call_evict(ctx, cache, block_table, seq_lens, keep_lens, recent, dst_block_table, new_lens, kept, stream)
 
 
 def _packed(cfg, q, k, cu_q, cu_k):
@@ -645,13 +662,20 @@ class StarKV:
 
     def __init__(self, cfg: starkv_config, A_k, A_v, B_k, B_v, stream=None):
         self.cfg = cfg
+        self._heads = _Heads(cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim)
         self.ctx = starkv_create(cfg, A_k, A_v, B_k, B_v, stream)
         self._ws = None
+        # workspace sizes of the last shapes (a size, not a buffer: buffers are new in each call)
+        self._decode_ws = functools.lru_cache(64)(functools.partial(starkv_workspace_bytes, self.ctx, OP_KV4_DECODE))
+        self._prompt_ws = functools.lru_cache(64)(functools.partial(starkv_prompt_workspace_bytes, self.ctx))
 
     def close(self):
         if self.ctx is not None:
             starkv_destroy(self.ctx)
             self.ctx = None
+            # (refused like every other call from here on)
+            self._decode_ws = functools.partial(starkv_workspace_bytes, None, OP_KV4_DECODE)
+            self._prompt_ws = functools.partial(starkv_prompt_workspace_bytes, None)
 
     def __del__(self):
         try:
@@ -689,21 +713,21 @@ class StarKV:
 
     def kv4_append(self, cache: KV4Cache, k, v, slot_mapping, weights=None, stream=None):
         _one_device(cache.pages)
-        starkv_kv4_append(self.ctx, self.cfg, cache.struct, k, v, slot_mapping, weights, stream)
+        starkv_kv4_append(self.ctx, self._heads, cache.struct, k, v, slot_mapping, weights, stream)
 
     def kv4_read(self, cache: KV4Cache, block_table, cu, total: int, starts=None, stream=None):
         """Keys and values [total, num_kv_heads, head_dim] of tokens starts[b] .. of each sequence."""
         _check_read(block_table, cu, starts)
         _one_device(cache.pages, block_table, cu, starts)
-        k = _new(cache.pages, (total, self.cfg.num_kv_heads, self.cfg.head_dim), torch.bfloat16, stream)
+        k = _new(cache.pages, (total, *self._heads[1:]), torch.bfloat16, stream)
         v = _new_like(k, stream)
         _call_read(self.ctx, cache.struct, block_table, cu, k, v, starts, stream)
         return k, v
 
     def kv4_decode(self, cache: KV4Cache, q, block_table, seq_lens, accumulate=False, out=None, stream=None):
-        _check_decode(self.cfg, q, block_table, seq_lens)
+        _check_decode(self._heads, q, block_table, seq_lens)
         _one_device(cache.pages, q, block_table, seq_lens, out)
-        n = starkv_workspace_bytes(self.ctx, OP_KV4_DECODE, *block_table.shape, int(bool(accumulate)))
+        n = self._decode_ws(*block_table.shape, int(bool(accumulate)))
         ws = _new(q, n, torch.uint8, stream) if n else None
         if out is None:
             out = _new_like(q, stream)
@@ -717,17 +741,17 @@ class StarKV:
     def kv4_evict(self, cache: KV4Cache, block_table, seq_lens, keep_lens, recent: int, dst_block_table, stream=None):
         """Gather the kept tokens into dst_block_table's pages: their new lengths [batch], and their indices
         [batch, num_kv_heads, dst_max_pages * 16] (-1 behind the last)."""
-        _one_device(cache.pages)
-        B, h = block_table.shape[0], self.cfg.num_kv_heads
-        new_lens = _new(block_table, B, torch.int32, stream)
-        kept = _new(block_table, (B, h, dst_block_table.shape[1] * PAGE_TOKENS), torch.int32, stream)
-        starkv_kv4_evict(self.ctx, self.cfg, cache.struct, block_table, seq_lens, keep_lens, recent, dst_block_table,
-                         new_lens, kept, stream)
+        _check_evict(block_table, seq_lens, keep_lens, dst_block_table)
+        _one_device(cache.pages, block_table, seq_lens, keep_lens, dst_block_table)
+        B, pages = dst_block_table.shape
+        new_lens = _new_like(seq_lens, stream)
+        kept = _new(block_table, (B, self._heads.num_kv_heads, pages * PAGE_TOKENS), torch.int32, stream)
+        _call_evict(self.ctx, cache.struct, block_table, seq_lens, keep_lens, recent, dst_block_table, new_lens, kept, stream)
         return new_lens, kept
 
     def prompt(self, q, k, v, cu_q, cu_k, max_q_len: int, out=None, stream=None):
         """Causal attention of packed prompts: (out [total_q, H, d], lse [total_q, H])."""
-        strides = _check_prompt(self.cfg, q, k, v, cu_q, cu_k)
+        strides = _check_prompt(self._heads, q, k, v, cu_q, cu_k)
         _one_device(q, k, v, cu_q, cu_k, out)
         if out is None:
             out = _new_like(q, stream)
@@ -736,7 +760,7 @@ class StarKV:
             if out.shape != q.shape:
                 raise ValueError("q and out disagree on their rows")
         lse = _new(q, q.shape[:2], torch.float32, stream)
-        n = starkv_prompt_workspace_bytes(self.ctx, cu_q.shape[0] - 1, q.shape[0], k.shape[0])
+        n = self._prompt_ws(cu_q.shape[0] - 1, q.shape[0], k.shape[0])
         ws = _new(q, n, torch.uint8, stream) if n else None
         _call_prompt(self.ctx, q, k, v, strides, cu_q, cu_k, max_q_len, out, lse, ws, stream)
         return out, lse
@@ -744,7 +768,7 @@ class StarKV:
     def prompt_weights(self, q, k, lse, cu_q, cu_k, max_k_len: int, window: int, stream=None):
         """Attention weight [total_k, num_kv_heads] that each sequence's last `window` queries give to its keys."""
         weights = _new(k, k.shape[:2], torch.float32, stream)
-        starkv_prompt_weights(self.ctx, self.cfg, q, k, lse, cu_q, cu_k, max_k_len, window, weights, stream)
+        starkv_prompt_weights(self.ctx, self._heads, q, k, lse, cu_q, cu_k, max_k_len, window, weights, stream)
         return weights
 
     def status(self, stream=None) -> int:

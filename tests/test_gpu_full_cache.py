@@ -537,3 +537,18 @@ def test_pages_whose_offsets_pass_32_bits():
         km, vm = F.values(moved[:, head:head + 1], np.arange(keep), d)
         np.testing.assert_array_equal(km[:, 0], kk[stay, head])
         np.testing.assert_array_equal(vm[:, 0], vv[stay, head])
+
+
+def test_calls_behind_close_are_refused():
+    S = skv()
+    kv = context(8, 2, 64)
+    cache = kv.new_kv4_cache(4)
+    q, one = torch.zeros((1, 8, 64), dtype=torch.bfloat16, device="cuda"), i32([1])
+    k = q[:, :2].contiguous()
+    kv.kv4_decode(cache, q, i32([[0]]), one)
+    kv.close()
+    for call in (lambda: kv.kv4_decode(cache, q, i32([[0]]), one), lambda: kv.prompt(q, k, k, i32([0, 1]), i32([0, 1]), 1),
+                 lambda: kv.kv4_append(cache, k, k, torch.zeros(1, dtype=torch.int64, device="cuda"))):
+        with pytest.raises(S.StarKVError) as e:
+            call()
+        assert e.value.code == S.ERR_INVALID_ARG
