@@ -18,6 +18,9 @@
  *   - A row stride counts elements between one token's row and the next, so that
  *     q, k and v may be parts of one projection's output; a row's heads are dense:
  *     head h at h * head_dim.  Strides are multiples of 8, pointers 16-byte aligned.
+ *   - Scores are held in fp32, so a probability is good to about 2^-22 of its score's
+ *     magnitude.  The prompt entries take scores of magnitudes below 2^30 (a row with
+ *     larger ones may be NaN).
  *   - Entries here neither allocate device memory nor keep state between calls;
  *     calls on different streams may overlap when their outputs and workspaces
  *     are different, and every call can be captured into a CUDA graph.
@@ -98,8 +101,9 @@ STARKV_API starkv_status starkv_kv4_read(starkv_ctx* ctx, const starkv_kv4_cache
                                          int64_t total, void* k_out, void* v_out, starkv_stream_t stream);
 
 /* Single-query attention over the 4-bit cache.  q: device bf16
- * [batch][num_q_heads][head_dim] (dense); sequence b's query attends to tokens
- * [0, seq_lens[b]).  out: device bf16 [batch][num_q_heads][head_dim]; seq_len 0 gives a
+ * [batch][num_q_heads][head_dim] (dense), of magnitudes below 2^115 (beyond, and for NaN,
+ * the head's row may be NaN); sequence b's query attends to tokens [0, seq_lens[b]).
+ * out: device bf16 [batch][num_q_heads][head_dim]; seq_len 0 gives a
  * zero row.  accumulate != 0: cache.weights of each attended token gains the
  * probabilities that the query heads of its KV head gave it.  A page that stands in two
  * tables gains both sequences' share; the order of those additions is not fixed, all else

@@ -47,7 +47,7 @@ constexpr int kWholePages = 32;
 constexpr int kWholePagesMany = 128;
 constexpr int kManyUnits = 64;
 constexpr float kMoveMax = 8.f;      // the running maximum moves when a score passes it by this (log2)
-constexpr float kNoMax = -1e30f;     // running maximum before the first score
+constexpr float kNoMax = -3.402823466e38f;  // running maximum before the first score: finite, and below all scores
 
 struct DecodeArgs {
   const __nv_bfloat16* q;

@@ -205,6 +205,37 @@ def test_decode_with_scores_far_apart():
     check_decode((8, 2, 128), [400, 90], True, seed=2, q_scale=1e-3)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale", [2.0**90, 2.0**112])
+def test_decode_with_queries_of_large_magnitude(d, scale):
+    """Scores of either sign and up to 2^118: a single token takes all of its heads' weight, however low its score."""
+    S = skv()
+    H, h = 8, 2
+    rng = np.random.default_rng(d)
+    kv = context(H, h, d)
+    lens = [1] * 12 + [40]
+    pages, t, _ = fill(rng, lens, h, d)
+    qd, q = bf16(rng, len(lens), H, d, scale=scale)
+    assert np.abs(q).max() < 2.0**115
+    cache = S.KV4Cache(kv.cfg, pages=torch.from_numpy(pages).cuda(), weights=torch.zeros((len(pages), h, 16), device="cuda"))
+    out = kv.kv4_decode(cache, qd, i32(t), i32(lens), accumulate=True).double().cpu().numpy()
+    assert kv.status() == 0
+    w = cache.weights.double().cpu().numpy()
+    seen = set()
+    for b, n in enumerate(lens):
+        k, v = F.values(pages, F.slots_of(t[b], n), d)
+        if n == 1:
+            want = np.repeat(v[0], H // h, 0)
+            seen |= set(np.sign((q[b].reshape(h, -1, d) * k[0][:, None]).sum(-1)).ravel())
+            # p = 1 exactly; v in fp16 and the output in bf16, half a step each
+            assert (np.abs(out[b] - want) <= 2.0**-8 * np.abs(want) + 2.0**-10 * np.abs(v).max()).all(), b
+            assert (w[t[b, 0], :, 0] == H // h).all()
+        else:
+            assert np.isfinite(out[b]).all() and (np.abs(out[b]) <= 1.01 * np.abs(v).max()).all()
+            assert abs(w[t[b, :3]].sum() - H) < 1e-4
+    assert seen == {-1.0, 1.0}
+
+
 def test_decode_of_empty_sequences_only():
     check_decode((8, 2, 64), [0, 0, 0], True)
 
