@@ -122,6 +122,29 @@ def test_prompt_with_scores_far_apart():
     run((8, 2, 128), [200], [200], window=200, q_scale=1e-4)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_with_scores_of_large_magnitude(d):
+    """Scores of either sign and up to 2^30: a query that sees one key has its value, however low the score."""
+    shape = H, h, _ = 8, 2, d
+    rng = np.random.default_rng(d)
+    kv = context(*shape)
+    n = [1] * 20 + [30]
+    q, k, v = inputs(rng, shape, n, n, q_scale=2.0**23)
+    scores = (q.double() * k.double().repeat_interleave(H // h, 1)).sum(-1) / d**0.5
+    one = scores[:20]
+    assert one.min() < -2.0**23 and one.max() > 2.0**23
+    bound = q.double().norm(dim=-1).max() * k.double().norm(dim=-1).max() / d**0.5  # of all scores, and of their terms' sums
+    assert bound < 2.0**30
+    cu = i32(cu_of(n))
+    out, lse = kv.prompt(q, k, v, cu, cu, 30)
+    assert kv.status() == 0
+    want = v.double().repeat_interleave(H // h, 1)[:20]
+    # p in bf16 and the output in bf16, half a step each
+    assert ((out.double()[:20] - want).abs() <= 2.0**-7 * want.abs()).all()
+    assert ((lse.double()[:20] - one).abs() <= 2.0**-20 * (one.abs() + bound)).all()
+    assert torch.isfinite(out).all() and (out[20:].abs() <= 1.01 * v[20:].abs().max()).all()
+
+
 def test_prompt_rising_scores_move_the_maximum():
     """Keys that grow along the sequence: each tile's scores pass those before by far more than 2^8."""
     shape = (4, 4, 64)
