@@ -641,20 +641,24 @@ class KV4Cache:
         return self.pages.numel() + (0 if self.weights is None else 4 * self.weights.numel())
 
 
-def _lent(t, stream):
-    """A new tensor that a call on `stream` uses: it is given back behind that stream's work."""
-    if stream is not None:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                        torch.cuda.ExternalStream(int(stream), device=t.device))
+def _new(like, shape, dtype, stream):
+    """A new tensor that a call on `stream` writes: memory in that stream's order (what the current stream gave
+    back, its own pending work may still use), given back behind the current stream's work too."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    here = torch.cuda.current_stream()
+    if not isinstance(stream, torch.cuda.Stream):
+        at = int(stream)
+        stream = torch.cuda.ExternalStream(at, device=here.device) if at else torch.cuda.default_stream(here.device)
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    if stream.cuda_stream != here.cuda_stream:
+        t.record_stream(here)
     return t
 
 
-def _new(like, shape, dtype, stream):
-    return _lent(like.new_empty(shape, dtype=dtype), stream)
-
-
 def _new_like(t, stream):
-    return _lent(torch.empty_like(t, memory_format=torch.contiguous_format), stream)
+    return torch.empty_like(t, memory_format=torch.contiguous_format) if stream is None else _new(t, t.shape, t.dtype, stream)
 
 
 class StarKV:

@@ -272,6 +272,32 @@ def test_prompt_captured_and_on_another_stream():
     assert kv.status() == 0
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_results_on_another_stream_take_no_memory_that_pending_work_still_writes(handle):
+    """Tensors given back on the current stream, whose last writes are still to come, while the call's stream is free."""
+    shape = H, h, d = 8, 2, 64
+    rng = np.random.default_rng(21)
+    kv = context(*shape)
+    q, k, v = inputs(rng, shape, [300], [1500])
+    cq, ck = i32([0, 300]), i32([0, 1500])
+    want, want_lse = kv.prompt(q, k, v, cq, ck, 300)
+    sizes = [want.shape, want_lse.shape]
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        old = [torch.empty(s, dtype=t, device="cuda") for s in sizes for t in (torch.bfloat16, torch.float32)]
+        for x in old:
+            x.fill_(7.0)
+        del old, x
+        out, lse = kv.prompt(q, k, v, cq, ck, 300, stream=side.cuda_stream if handle else side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    out, lse = kv.prompt(q, k, v, cq, ck, 300, stream=0)  # the default stream by its handle
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse) and kv.status() == 0
+
+
 @pytest.mark.parametrize("shape", [(8, 2, 64), (8, 4, 128)])
 def test_from_a_prompt_in_two_chunks_to_decode_behind_an_eviction(shape):
     """A full-width layer's life: a first chunk attends and is cached, a second chunk attends to the cache read back and
