@@ -105,6 +105,13 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Adds to four floats, each atomically; p is 16-byte aligned.
+__device__ __forceinline__ void red_add4(float* p, const float (&x)[4]) {
+  asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+               "f"(x[3])
+               : "memory");
+}
+
 // 8 x 8 transpose of 16-bit elements across the warp
 __device__ __forceinline__ uint32_t movm_trans(uint32_t x) {
   uint32_t y;
@@ -600,14 +607,18 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_decode_kernel(const Decod
 // ---------------------------------------------------------------------------
 // Join of the parts, and the weights.  Block x = 0 of a (sequence, KV head) joins the
 // outputs of its units that a cut went through (and writes an empty sequence's zero
-// rows); blocks x >= 1 add the probabilities of 1024 tokens each.
+// rows); blocks x >= 1 add the probabilities of 1024 tokens each: a warp reads the scores of
+// 32 tokens at a time, and a transpose among four lanes gives each lane four neighbours of one
+// page, which it adds at once: one page to look up and one addition of 16 bytes.  (Decode and
+// join of 32 sequences of 4096 to 8192 tokens, 32 heads over 8: 90 us, with a token a lane 92;
+// with six blocks an SM 89.)
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
-constexpr int kJoinTokens = 1024;
+constexpr int kJoinTokens = 4 * kJoinThreads;
 constexpr int kJoinHeads = 32;  // heads whose maximum and 1 / sum a pass holds
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kJoinThreads, 6) kv4_join_kernel(const DecodeArgs a) {
   __shared__ float2 norm[kJoinHeads];  // maximum, 1 / sum
   __shared__ float4 acc[kJoinThreads];
   const int tid = threadIdx.x;
@@ -625,21 +636,17 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const DecodeArgs
     return;
   }
   const int64_t before = a.ctas > 0 ? a.before[b] * a.units : 0, total = a.ctas > 0 ? a.before[a.batch] * a.units : 0;
-  int64_t page_of[kJoinTokens / kJoinThreads];  // asked for before the sums are
-#pragma unroll
-  for (int i = 0; i < kJoinTokens / kJoinThreads; ++i) {
-    const int tok = token0 + i * kJoinThreads + tid;
-    page_of[i] = blockIdx.x > 0 && tok < len ? a.block_table[(int64_t)b * a.max_pages + tok / kPage] : -1;
-  }
+  // the lane's scores are those of tokens at + 32 i, its sums in the end those of tokens quad .. quad + 3
+  const int lane = tid & 31, at = token0 + (tid >> 5) * 128 + lane, quad = at - lane + (lane & 3) * 32 + (lane >> 2) * 4;
+  // (asked for before the sums are)
+  const int64_t page = blockIdx.x > 0 && quad < len ? a.block_table[(int64_t)b * a.max_pages + quad / kPage] : -1;
   // the CTAs whose stretches hold unit u's first and last page
   auto ctas_of = [&](int u, int64_t& c0, int64_t& c1) {
     const int64_t first = before + (int64_t)u * pages;
     c0 = a.ctas > 0 ? cta_of(first, total, a.ctas) : 0;
     c1 = a.ctas > 0 ? cta_of(first + pages - 1, total, a.ctas) : 0;
   };
-  float add[kJoinTokens / kJoinThreads];
-#pragma unroll
-  for (int i = 0; i < kJoinTokens / kJoinThreads; ++i) add[i] = 0.f;
+  float add[4] = {0.f, 0.f, 0.f, 0.f};
   for (int h0 = 0; h0 < a.group; h0 += kJoinHeads) {
     const int heads = min(kJoinHeads, a.group - h0);
     __syncthreads();
@@ -722,8 +729,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const DecodeArgs
     } else {
       const float* rows = a.scores + (((int64_t)b * a.pool.h_kv + kv) * a.max_pages * kPage) * a.score_heads + h0;
 #pragma unroll
-      for (int i = 0; i < kJoinTokens / kJoinThreads; ++i) {
-        const int tok = token0 + i * kJoinThreads + tid;
+      for (int i = 0; i < 4; ++i) {
+        const int tok = at + i * 32;
         if (tok >= len) continue;
         const float* row = rows + (int64_t)tok * a.score_heads;
         if (a.score_heads == 1) {
@@ -744,13 +751,26 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const DecodeArgs
     }
   }
   if (blockIdx.x == 0) return;
+  // 4 x 4 transpose among the lanes 4 q .. 4 q + 3
 #pragma unroll
-  for (int i = 0; i < kJoinTokens / kJoinThreads; ++i) {
-    const int tok = token0 + i * kJoinThreads + tid;
-    const int64_t page = page_of[i];  // (-1 behind the last token)
-    if (page < 0 || page >= a.pool.n_pages) continue;
-    // one addition a token and call: atomic only for a page that two tables share
-    atomicAdd(&a.pool.weights[(page * a.pool.h_kv + kv) * kPage + tok % kPage], add[i]);
+  for (int w = 1; w < 4; w <<= 1) {
+    const bool up = lane & w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!(i & w)) {
+        const float got = __shfl_xor_sync(0xffffffffu, up ? add[i] : add[i | w], w);
+        (up ? add[i] : add[i | w]) = got;
+      }
+  }
+  if (page < 0 || page >= a.pool.n_pages) return;  // (-1 behind the last token)
+  // one addition a token and call: atomic only for a page that two tables share
+  float* to = &a.pool.weights[(page * a.pool.h_kv + kv) * kPage + quad % kPage];
+  if (quad + 4 <= len) {
+    red_add4(to, add);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+      if (quad + e < len) atomicAdd(to + e, add[e]);
   }
 }
 
