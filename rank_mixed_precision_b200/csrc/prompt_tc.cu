@@ -1548,8 +1548,13 @@ cudaError_t launch_weights_d(const CUtensorMap& qm, const CUtensorMap& km, Promp
   const int64_t most = ((int64_t)(a.window < a.max_k ? a.window : a.max_k) + a.R - 1) / a.R * a.head_blocks;
   a.mode = most <= WeightSmem<D>::kStages ? kResident : kStreamed;
   unsigned grid = (unsigned)(items < sms ? items : sms), cluster = 1;
-  if (a.mode == kStreamed && items * 2 <= sms) {
+  if (a.mode == kStreamed) {
     while (cluster < 8 && items * cluster * 2 <= sms && cluster * 2 <= most) cluster *= 2;
+    // Pairs of CTAs where they come in two rounds, too, if all queries count: the items' steps then fall evenly
+    // from `most` to none, and a pair that ends takes one of the short ones.  That spares most * sms / (4 items)
+    // steps and costs a second round's start, 14 steps.  (Queries of 32 heads over 8: 1300 31 and 21 us, 2000 46
+    // and 34, 256 of 2048 12 and 20; 4000 of 4 heads of 64, 25 and 24.)
+    if (items * 2 > sms && items <= sms && a.window >= a.max_k && most * sms > 56 * items) cluster = 2;
     if (cluster > 1) {
       a.mode = (int)cluster;
       grid = (unsigned)items * cluster;

@@ -410,6 +410,16 @@ def test_weights_of_every_way_to_share_the_work(shape, n_q, n_k, window):
                 assert ((got - want).abs() <= tol).all(), (b, head, (got - want).abs().max())
 
 
+@pytest.mark.parametrize("shape,n_q,n_k", [
+    ((16, 4, 64), [2500], [2500]),
+    ((16, 4, 128), [1500, 300], [1500, 300]),
+    ((16, 4, 64), [600, 1500], [1500, 1500]),
+    ((20, 1, 128), [1, 1490, 0, 33], [700, 1500, 5, 33]),
+])
+def test_weights_of_items_shared_by_pairs_in_two_rounds(shape, n_q, n_k):
+    test_weights_of_every_way_to_share_the_work(shape, n_q, n_k, 4000)
+
+
 def test_prompt_whose_keys_leave_the_cache():
     """Keys and values of more than 96 MB with units for every SM: whole units a CTA, the longest first."""
     shape = H, h, d = 32, 32, 128
