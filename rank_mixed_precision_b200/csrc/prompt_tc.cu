@@ -923,8 +923,7 @@ __global__ void __launch_bounds__(kMergeThreads) prompt_join_kernel(const Prompt
 // columns each (four warps a scheduler keep the exponentials going while others wait for
 // their columns); warp 16 copies, warp 17 issues the products, warps 18 and 19 lay out each
 // column's log-sum-exp and the last key it sees and note for each product what its sums go
-// by.  A note without a product makes up an item's number where it has to be even.  One CTA
-// an SM walks over many items, three ways:
+// by.  One CTA an SM walks over many items, three ways:
 //   resident  the counting queries of a (sequence, KV head) fit the ring (a window): a CTA
 //             takes an equal stretch of the items in (sequence, KV head, key) order and
 //             loads them once per (sequence, KV head); only K tiles stream.  (64 queries of
@@ -1056,7 +1055,8 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   uint64_t* sums = sempty + 4;     // [2][4] three warps' sums are there
   uint64_t* taken = sums + 8;      // [2][4] and have been added
   uint64_t* done = taken + 8;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* both = done + 1;       // resident: warps 18 and 19 have laid a (sequence, KV head)'s columns out
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(both + 1);
   float* lse2 = reinterpret_cast<float*>(sm + SM::kCols);
   int* last = reinterpret_cast<int*>(sm + SM::kCols + SM::kSlots * kTile * 4);
   float* other = reinterpret_cast<float*>(sm + SM::kSums);
@@ -1093,6 +1093,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       mbar_init(&taken[s], 1);
     }
     mbar_init(done, 1);
+    mbar_init(both, 2);
     fence_mbar_init();
   }
   pdl_wait();
@@ -1162,10 +1163,6 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   // Stage and phase of step v, the u-th of this CTA.  Resident: the stage is the step's number, and
   // `flips` holds the stages' phases (a stage turns when a (sequence, KV head) that used it is done).
   uint32_t flips = 0;
-  // A note without a product follows an item's steps where there is one alone (it ends the item for the
-  // other warps), and where a resident item's number is odd: a step's columns, which stay over many
-  // items, are then laid out by one warp and read by the same eight all the time.
-  auto made_up = [&](int steps) { return (rank < steps && rank + split >= steps) || (resident && steps % 2 == 1); };
   auto stage_of = [&](int v, int u) { return resident ? v : u % ST; };
   auto phase_of = [&](int v, int u) { return resident ? (flips >> v) & 1u : (uint32_t)(u / ST) & 1u; };
   float acc = 0.f;
@@ -1227,7 +1224,8 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       const bool free_q = uniform(!resident || !more || it.fresh);  // resident: the Q tiles' last use
       ok = uniform(__all_sync(0xffffffffu, mbar_wait_short(&kfull[ks], kph)));
       const uint64_t k0 = desc_at(kd, ks * SM::kTileBytes);
-      for (int v = rank; ok && v < steps; v += split, ++u) {
+      int v = rank;
+      for (; ok && v < steps; v += split, ++u) {
         const int s = resident ? v : st, w = u & 3;
         const uint32_t ph = resident ? (flips >> v) & 1u : sph;
         ok = uniform(__all_sync(0xffffffffu, mbar_wait_short(&full[s], ph) && mbar_wait_short(&sempty[w], ((u >> 2) & 1) ^ 1)));
@@ -1249,7 +1247,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
           sph ^= 1;
         }
       }
-      if (ok && made_up(steps)) {
+      if (ok && v == rank + split) {  // one step: a note without a product ends the item for the other warps
         const int w = u & 3;
         ok = __all_sync(0xffffffffu, mbar_wait_short(&sempty[w], ((u >> 2) & 1) ^ 1));
         if (lane == 0) mbar_arrive(&sfull[w]);
@@ -1274,7 +1272,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   } else if (warp >= 18) {
     // ---------------- columns and notes (and the zeros of keys that no counting query sees) ----------------
     // warp 18 does the even steps, warp 19 the odd ones: a step's work in one warp is longer than a step
-    int u = 0, laid = 0;  // notes and (streamed) columns so far
+    int u = 0, laid = 0, laid_units = 0;  // notes, (streamed) columns and (resident) (sequence, KV head)s so far
     auto my_turn = [&]() { return (u & 1) == warp - 18; };
     int col_r[4], col_h[4];  // the lane's columns: query within the tile, head within the block
 #pragma unroll
@@ -1374,8 +1372,13 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         }
         advance(hb, i0);
       }
-      if (ok && made_up(steps)) ok = note(Note{rank + split >= steps ? kLast : 0, 0, 0, key0, keys, 0, row});
+      if (ok && rank < steps && rank + split >= steps) ok = note(Note{kLast, 0, 0, key0, keys, 0, row});
       if (lay) flips ^= (1u << min(steps, ST)) - 1;
+      if (ok && resident && fresh) {  // the next item's notes may be the other warp's
+        if (lane == 0) mbar_arrive(both);
+        ok = __all_sync(0xffffffffu, mbar_wait_short(both, laid_units & 1));
+        ++laid_units;
+      }
     }
     for (int e = 0; ok && e < 2; ++e) ok = note(Note{kStop, 0, 0, 0, 0, 0, 0});
   } else {
