@@ -63,6 +63,7 @@ struct DecodeArgs {
   int64_t* before;         // [B + 1] pages before each sequence, and of all (ctas > 0)
   float* scores;           // [B][h_kv][max_pages * 16][score_heads], log2 units (NULL: not asked for)
   unsigned int* status;
+  int side, outs;          // the join: heads a block joins side by side, and its blocks of a (sequence, KV head) for that
 };
 
 template <int D>
@@ -605,9 +606,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_decode_kernel(const Decod
 }
 
 // ---------------------------------------------------------------------------
-// Join of the parts, and the weights.  Block x = 0 of a (sequence, KV head) joins the
-// outputs of its units that a cut went through (and writes an empty sequence's zero
-// rows); blocks x >= 1 add the probabilities of 1024 tokens each: a warp reads the scores of
+// Join of the parts, and the weights.  Blocks x < outs of a (sequence, KV head) join the
+// outputs of its units that a cut went through (and write an empty sequence's zero rows), `side`
+// heads each: the more parts a unit has, the fewer heads a block, and the more threads share a head's parts
+// out.  (Two sequences of 21648 tokens, 14 heads of 64 over 2, 148 parts a unit: 17 us; all
+// seven heads in one block 32.)  The other blocks add the probabilities of 1024 tokens each: a
+// warp reads the scores of
 // 32 tokens at a time, and a transpose among four lanes gives each lane four neighbours of one
 // page, which it adds at once: one page to look up and one addition of 16 bytes.  (Decode and
 // join of 32 sequences of 4096 to 8192 tokens, 32 heads over 8: 87 us; with a token a lane at a
@@ -627,19 +631,21 @@ __global__ void __launch_bounds__(kJoinThreads, 8) kv4_join_kernel(const DecodeA
   pdl_launch_dependents();
   const int pages = pages_of(a, b);
   const int len = pages > 0 ? a.seq_lens[b] : 0;
-  const int token0 = ((int)blockIdx.x - 1) * kJoinTokens;
-  if (blockIdx.x > 0 && token0 >= len) return;
+  const bool joins = (int)blockIdx.x < a.outs;
+  const int token0 = ((int)blockIdx.x - a.outs) * kJoinTokens;
+  if (!joins && token0 >= len) return;
+  const int first_head = joins ? (int)blockIdx.x * a.side : 0, last_head = joins ? min(first_head + a.side, a.group) : a.group;
   if (pages == 0) {
     uint32_t* out = reinterpret_cast<uint32_t*>(a.out + ((int64_t)b * a.H + kv * a.group) * D);
     if (a.ctas > 0)
-      for (int i = tid; i < a.group * (D / 2); i += kJoinThreads) out[i] = 0u;
+      for (int i = first_head * (D / 2) + tid; i < last_head * (D / 2); i += kJoinThreads) out[i] = 0u;
     return;
   }
   const int64_t before = a.ctas > 0 ? a.before[b] * a.units : 0, total = a.ctas > 0 ? a.before[a.batch] * a.units : 0;
   // the lane's scores are those of tokens at + 32 i, its sums in the end those of tokens quad .. quad + 3
   const int lane = tid & 31, at = token0 + (tid >> 5) * 128 + lane, quad = at - lane + (lane & 3) * 32 + (lane >> 2) * 4;
   // (asked for before the sums are)
-  const int64_t page = blockIdx.x > 0 && quad < len ? a.block_table[(int64_t)b * a.max_pages + quad / kPage] : -1;
+  const int64_t page = !joins && quad < len ? a.block_table[(int64_t)b * a.max_pages + quad / kPage] : -1;
   // the CTAs whose stretches hold unit u's first and last page
   auto ctas_of = [&](int u, int64_t& c0, int64_t& c1) {
     const int64_t first = before + (int64_t)u * pages;
@@ -647,13 +653,14 @@ __global__ void __launch_bounds__(kJoinThreads, 8) kv4_join_kernel(const DecodeA
     c1 = a.ctas > 0 ? cta_of(first + pages - 1, total, a.ctas) : 0;
   };
   float add[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int h0 = 0; h0 < a.group; h0 += kJoinHeads) {
-    const int heads = min(kJoinHeads, a.group - h0);
+  for (int h0 = first_head; h0 < last_head; h0 += kJoinHeads) {
+    const int heads = min(kJoinHeads, last_head - h0);
     __syncthreads();
-    // eight threads a head: the sequence's maximum and sum over its parts
+    // a warp, or eight threads, a head: the sequence's maximum and sum over its parts
     {
-      const int h = h0 + tid / 8;
-      const bool mine = tid / 8 < heads;
+      const int per = heads <= kJoinThreads / 32 ? 32 : 8, one = tid & (per - 1), hh = tid / per;
+      const int h = h0 + hh;
+      const bool mine = hh < heads;
       float top = kNoMax, sum = 0.f;
       int64_t c0 = 0, c1 = 0;
       const int u = kv * a.head_blocks + h / kHeads;
@@ -661,71 +668,65 @@ __global__ void __launch_bounds__(kJoinThreads, 8) kv4_join_kernel(const DecodeA
       const bool parts = mine && c0 < c1;
       auto ml = [&](int64_t c) { return a.part_ml[(c * 2 + (c == c0)) * kHeads + h % kHeads]; };
       if (parts)
-        for (int64_t c = c0 + (tid & 7); c <= c1; c += 8) top = fmaxf(top, ml(c).x);
-#pragma unroll
-      for (int w = 1; w < 8; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+        for (int64_t c = c0 + one; c <= c1; c += per) top = fmaxf(top, ml(c).x);
+      for (int w = 1; w < per; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
       if (parts)
-        for (int64_t c = c0 + (tid & 7); c <= c1; c += 8) {
+        for (int64_t c = c0 + one; c <= c1; c += per) {
           const float2 v = ml(c);
           sum = fmaf(v.y, ex2(v.x - top), sum);
         }
-#pragma unroll
-      for (int w = 1; w < 8; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+      for (int w = 1; w < per; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
       if (mine && !parts && a.unit_ml) {
         const float2 v = a.unit_ml[((int64_t)b * a.units + u) * kHeads + h % kHeads];
         top = v.x;
         sum = v.y;
       }
-      if (mine && (tid & 7) == 0) norm[tid / 8] = make_float2(top, sum == 0.f ? 0.f : 1.f / sum);
+      if (mine && one == 0) norm[hh] = make_float2(top, sum == 0.f ? 0.f : 1.f / sum);
     }
     __syncthreads();
-    if (blockIdx.x == 0) {
+    if (joins) {
       // kRow threads hold a head's row; `side` heads go side by side, and what threads are left share a head's
       // parts out, then add up
       constexpr int kRow = D / 4;
       constexpr int kRows = kJoinThreads / kRow;
-      int side = 1;
-      while (side < heads && side < kRows && side < kHeads) side *= 2;
-      const int ways = kRows / side;
-      const int c4 = (tid % kRow) * 4, way = tid / kRow / side;
-      for (int h1 = 0; h1 < heads; h1 += side) {
-        const int hh = h1 + tid / kRow % side, h = h0 + hh;
-        int64_t c0, c1;
-        ctas_of(kv * a.head_blocks + (h0 + h1) / kHeads, c0, c1);
-        if (c0 == c1) continue;  // (the same for the whole block: the heads side by side share a unit)
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (hh < heads)
-          for (int64_t c = c0 + way; c <= c1; c += ways) {
-            const int64_t row = (c * 2 + (c == c0)) * kHeads + h % kHeads;
-            const float r = ex2(a.part_ml[row].x - norm[hh].x);
-            const float4 x = *reinterpret_cast<const float4*>(a.part_o + row * D + c4);
-            v.x = fmaf(x.x, r, v.x);
-            v.y = fmaf(x.y, r, v.y);
-            v.z = fmaf(x.z, r, v.z);
-            v.w = fmaf(x.w, r, v.w);
-          }
-        if (ways > 1) {
-          __syncthreads();
-          acc[tid] = v;
-          __syncthreads();
+      const int side = a.side, ways = kRows / side;
+      const int c4 = (tid % kRow) * 4, way = tid / kRow / side, hh = tid / kRow % side, h = h0 + hh;
+      int64_t c0, c1;
+      ctas_of(kv * a.head_blocks + h0 / kHeads, c0, c1);
+      if (c0 == c1) return;  // (the same for the whole block: the heads side by side share a unit)
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (hh < heads)
+#pragma unroll 2
+        for (int64_t c = c0 + way; c <= c1; c += ways) {
+          const int64_t row = (c * 2 + (c == c0)) * kHeads + h % kHeads;
+          const float r = ex2(a.part_ml[row].x - norm[hh].x);
+          const float4 x = *reinterpret_cast<const float4*>(a.part_o + row * D + c4);
+          v.x = fmaf(x.x, r, v.x);
+          v.y = fmaf(x.y, r, v.y);
+          v.z = fmaf(x.z, r, v.z);
+          v.w = fmaf(x.w, r, v.w);
         }
-        if (way == 0 && hh < heads) {
-          for (int w = 1; w < ways && w <= c1 - c0; ++w) {
-            const float4 x = acc[w * side * kRow + tid];
-            v.x += x.x;
-            v.y += x.y;
-            v.z += x.z;
-            v.w += x.w;
-          }
-          const float inv = norm[hh].y;
-          const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * inv, v.y * inv);
-          const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z * inv, v.w * inv);
-          uint2 w2;
-          w2.x = *reinterpret_cast<const uint32_t*>(&lo);
-          w2.y = *reinterpret_cast<const uint32_t*>(&hi);
-          *reinterpret_cast<uint2*>(a.out + ((int64_t)b * a.H + kv * a.group + h) * D + c4) = w2;
-        }
+      if (ways > 1) {
+        acc[tid] = v;
+        __syncthreads();
       }
+      if (way == 0 && hh < heads) {
+        for (int w = 1; w < ways && w <= c1 - c0; ++w) {
+          const float4 x = acc[w * side * kRow + tid];
+          v.x += x.x;
+          v.y += x.y;
+          v.z += x.z;
+          v.w += x.w;
+        }
+        const float inv = norm[hh].y;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * inv, v.y * inv);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+        uint2 w2;
+        w2.x = *reinterpret_cast<const uint32_t*>(&lo);
+        w2.y = *reinterpret_cast<const uint32_t*>(&hi);
+        *reinterpret_cast<uint2*>(a.out + ((int64_t)b * a.H + kv * a.group + h) * D + c4) = w2;
+      }
+      return;
     } else {
       const float* row = a.scores + (((int64_t)b * a.pool.h_kv + kv) * a.max_pages * kPage + at) * a.score_heads + h0;
       if (a.score_heads <= 2) {
@@ -757,7 +758,6 @@ __global__ void __launch_bounds__(kJoinThreads, 8) kv4_join_kernel(const DecodeA
       }
     }
   }
-  if (blockIdx.x == 0) return;
   // 4 x 4 transpose among the lanes 4 q .. 4 q + 3
 #pragma unroll
   for (int w = 1; w < 4; w <<= 1) {
@@ -815,7 +815,7 @@ static cudaError_t launch_decode_d(const Ctx& c, const DecodeArgs& a, cudaStream
   e = launch_chained(kv4_decode_kernel<D>, dim3(blocks), dim3(kThreads), (size_t)smem, s, 1u, a);
   if (e != cudaSuccess || (a.ctas == 0 && !a.scores)) return e;
   const unsigned chunks = a.scores ? (unsigned)(((int64_t)a.max_pages * kPage + kJoinTokens - 1) / kJoinTokens) : 0;
-  return launch_chained(kv4_join_kernel<D>, dim3(1 + chunks, c.cfg.num_kv_heads, a.batch), dim3(kJoinThreads), 0, s, 1u,
+  return launch_chained(kv4_join_kernel<D>, dim3(a.outs + chunks, c.cfg.num_kv_heads, a.batch), dim3(kJoinThreads), 0, s, 1u,
                         a);
 }
 
@@ -844,6 +844,12 @@ cudaError_t launch_kv4_decode(const Ctx& c, const starkv_kv4_cache& cache, const
   a.before = (int64_t*)((char*)ws + plan.off_before);
   a.scores = accumulate ? (float*)((char*)ws + plan.off_scores) : nullptr;
   a.status = c.status;
+  // heads side by side in the join: at most a unit's, fewer where a head's threads would take more than two parts each
+  const int rows = kJoinThreads / (c.cfg.head_dim / 4), parts = plan.ctas / (batch * plan.units) + 1;
+  a.side = 1;
+  while (a.side < c.group && a.side < kHeads) a.side *= 2;
+  while (a.side > 1 && rows / a.side * 2 < parts) a.side /= 2;
+  a.outs = plan.ctas > 0 ? (c.group + a.side - 1) / a.side : 0;
   return c.cfg.head_dim == 64 ? launch_decode_d<64>(c, a, s) : launch_decode_d<128>(c, a, s);
 }
 
