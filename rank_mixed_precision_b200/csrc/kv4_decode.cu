@@ -25,6 +25,8 @@
 //   output   o[c, h] = sum_t v[t, c] p[t, h]
 //     A = V^T, widened to fp16 (code * s + z, one rounding), B = p in fp16 (at most 2^8
 //     against the running maximum, which moves only when it grows by more than that).
+#include <algorithm>
+
 #include "full.cuh"
 #include "sm100.cuh"
 
@@ -46,6 +48,9 @@ constexpr int kCtas = 4;             // CTAs of an SM
 constexpr int kWholePages = 32;
 constexpr int kWholePagesMany = 128;
 constexpr int kManyUnits = 64;
+// CTAs of a unit at most: more parts cost the join more than they spare.  (At most 32, 74, 148 and any
+// number, us: 8 heads of 128 over one, 100000 tokens 41, 26, 24, 46; 40 of 64 over one, 20000 tokens 14, 15, 19, 19.)
+constexpr int kMostParts = 74;
 constexpr float kMoveMax = 8.f;      // the running maximum moves when a score passes it by this (log2)
 constexpr float kNoMax = -3.402823466e38f;  // running maximum before the first score: finite, and below all scores
 
@@ -608,12 +613,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_decode_kernel(const Decod
 // ---------------------------------------------------------------------------
 // Join of the parts, and the weights.  Blocks x < outs of a (sequence, KV head) join the
 // outputs of its units that a cut went through (and write an empty sequence's zero rows), `side`
-// heads each: the more parts a unit has, the fewer heads a block, and the more threads share a head's parts
-// out.  (Two sequences of 21648 tokens, 14 heads of 64 over 2, 148 parts a unit: 17 us; all
-// seven heads in one block 32.)  The other blocks add the probabilities of 1024 tokens each: a
-// warp reads the scores of
-// 32 tokens at a time, and a transpose among four lanes gives each lane four neighbours of one
-// page, which it adds at once: one page to look up and one addition of 16 bytes.  (Decode and
+// heads each: the more parts a unit has, the fewer heads a block, and the more threads share a
+// head's parts out.  (Two sequences of 21648 tokens, 14 heads of 64 over 2, 148 parts a unit:
+// 17 us; all seven heads in one block 32.)  The other blocks add the probabilities of 1024 tokens
+// each: a warp reads the scores of 32 tokens at a time, and a transpose among four lanes gives
+// each lane four neighbours of one page, which it adds at once: one page to look up and one
+// addition of 16 bytes.  (Decode and
 // join of 32 sequences of 4096 to 8192 tokens, 32 heads over 8: 87 us; with a token a lane at a
 // time, and the norms read for each, 92; with six blocks an SM, not eight, 88.)
 // ---------------------------------------------------------------------------
@@ -790,10 +795,10 @@ Kv4DecodePlan plan_kv4_decode(const Ctx& c, int batch, int max_pages, bool accum
   p.units = f.num_kv_heads * p.head_blocks;
   int sms = 148;
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c.device);
-  // one round of CTAs, with 8 pages (a pair a warp) at least where the tables are full
+  // one round of CTAs at most, with 8 pages (a pair a warp) at least where the tables are full
   const bool whole = max_pages <= ((int64_t)batch * p.units >= kManyUnits ? kWholePagesMany : kWholePages);
   const int64_t most = (int64_t)batch * p.units * max_pages;
-  const int64_t round = (int64_t)sms * kCtas;
+  const int64_t round = std::min((int64_t)sms * kCtas, (int64_t)batch * p.units * kMostParts);
   p.ctas = whole ? 0 : (int)(most / 8 < round ? most / 8 : round);
   p.score_heads = !accumulate ? 0 : c.group <= 2 ? c.group : (c.group + 3) / 4 * 4;
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };

@@ -177,6 +177,13 @@ def test_decode_of_several_splits(shape, lens):
     check_decode(shape, lens, True, seed=len(lens))
 
 
+@pytest.mark.parametrize("shape,lens", [((14, 2, 64), [9000, 5003]), ((20, 1, 128), [12001]), ((8, 1, 64), [7000, 0, 40])])
+def test_decode_of_long_sequences_of_few_heads(shape, lens):
+    """A unit of many parts: their heads are joined in several blocks."""
+    check_decode(shape, lens, True, seed=lens[0])
+    check_decode(shape, lens, False, seed=lens[0])
+
+
 def test_decode_of_short_sequences_in_wide_tables():
     """A table with room for far more pages than its sequences hold: fewer pages than the work is cut into."""
     S = skv()
