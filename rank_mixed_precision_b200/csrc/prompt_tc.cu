@@ -891,14 +891,17 @@ __global__ void __launch_bounds__(kMergeThreads) prompt_join_kernel(const Prompt
     if (r >= a.R * a.gb || qi >= q.n || hh >= min(a.gb, a.group - c.hb * a.gb)) continue;
     auto slot = [&](int k) { return ((int64_t)k * 2 + (k == first)) * 2 * kTile + r2; };
     float m = -INFINITY;
+    // (unrolled: a unit may have a part on every SM, and a part's loads take a round trip)
+#pragma unroll 8
     for (int k = first; k <= c.last; ++k) m = fmaxf(m, a.part_ml[slot(k)].x);
     float l = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
     for (int k = first; k <= c.last; ++k) {
       const float2 ml = a.part_ml[slot(k)];
+      const float4 x = *reinterpret_cast<const float4*>(a.part_o + slot(k) * D + c4);
       if (ml.y == 0.f) continue;  // no scores of the row there
       const float f = m == -INFINITY ? 1.f : ex2((ml.x - m) * a.scale_log2);
-      const float4 x = *reinterpret_cast<const float4*>(a.part_o + slot(k) * D + c4);
       l = fmaf(ml.y, f, l);
       v.x = fmaf(x.x, f, v.x);
       v.y = fmaf(x.y, f, v.y);
