@@ -926,7 +926,7 @@ __global__ void __launch_bounds__(kMergeThreads) prompt_join_kernel(const Prompt
 // columns each (four warps a scheduler keep the exponentials going while others wait for
 // their columns); warp 16 copies, warp 17 issues the products, warps 18 and 19 lay out each
 // column's log-sum-exp and the last key it sees and note for each product what its sums go
-// by.  One CTA an SM walks over many items, three ways:
+// by.  A note without a product makes up an item's number where it has to be even.  One CTA an SM walks over many items, three ways:
 //   resident  the counting queries of a (sequence, KV head) fit the ring (a window): a CTA
 //             takes an equal stretch of the items in (sequence, KV head, key) order and
 //             loads them once per (sequence, KV head); only K tiles stream.  (64 queries of
@@ -1166,6 +1166,10 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   // Stage and phase of step v, the u-th of this CTA.  Resident: the stage is the step's number, and
   // `flips` holds the stages' phases (a stage turns when a (sequence, KV head) that used it is done).
   uint32_t flips = 0;
+  // A note without a product follows an item's steps where there is one alone (it ends the item for the
+  // other warps), and where a resident item's number is odd: its columns stay over many items and only the
+  // last item's readers say that they are done, so a step has to be read by the same eight warps in each.
+  auto made_up = [&](int steps) { return (rank < steps && rank + split >= steps) || (resident && steps % 2 == 1); };
   auto stage_of = [&](int v, int u) { return resident ? v : u % ST; };
   auto phase_of = [&](int v, int u) { return resident ? (flips >> v) & 1u : (uint32_t)(u / ST) & 1u; };
   float acc = 0.f;
@@ -1227,8 +1231,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       const bool free_q = uniform(!resident || !more || it.fresh);  // resident: the Q tiles' last use
       ok = uniform(__all_sync(0xffffffffu, mbar_wait_short(&kfull[ks], kph)));
       const uint64_t k0 = desc_at(kd, ks * SM::kTileBytes);
-      int v = rank;
-      for (; ok && v < steps; v += split, ++u) {
+      for (int v = rank; ok && v < steps; v += split, ++u) {
         const int s = resident ? v : st, w = u & 3;
         const uint32_t ph = resident ? (flips >> v) & 1u : sph;
         ok = uniform(__all_sync(0xffffffffu, mbar_wait_short(&full[s], ph) && mbar_wait_short(&sempty[w], ((u >> 2) & 1) ^ 1)));
@@ -1250,7 +1253,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
           sph ^= 1;
         }
       }
-      if (ok && v == rank + split) {  // one step: a note without a product ends the item for the other warps
+      if (ok && made_up(steps)) {
         const int w = u & 3;
         ok = __all_sync(0xffffffffu, mbar_wait_short(&sempty[w], ((u >> 2) & 1) ^ 1));
         if (lane == 0) mbar_arrive(&sfull[w]);
@@ -1375,9 +1378,11 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         }
         advance(hb, i0);
       }
-      if (ok && rank < steps && rank + split >= steps) ok = note(Note{kLast, 0, 0, key0, keys, 0, row});
+      if (ok && made_up(steps)) ok = note(Note{rank + split >= steps ? kLast : 0, 0, 0, key0, keys, 0, row});
       if (lay) flips ^= (1u << min(steps, ST)) - 1;
-      if (ok && resident && fresh) {  // the next item's notes may be the other warp's
+      // The two warps meet when a (sequence, KV head)'s columns are there.  (No order hangs on it; without it the
+      // last 64 queries of 4 x 32768 take 95 us for 89, 96 queries of each, three steps, 136 for 124.)
+      if (ok && resident && fresh) {
         if (lane == 0) mbar_arrive(both);
         ok = __all_sync(0xffffffffu, mbar_wait_short(both, laid_units & 1));
         ++laid_units;

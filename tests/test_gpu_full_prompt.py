@@ -439,3 +439,29 @@ def test_prompt_whose_keys_leave_the_cache():
         o, mag = p @ v[:, head].double(), p @ v[:, head].double().abs()
         assert ((out[:, head].double() - o).abs() <= 2.0**-8 * (o.abs() + mag) + mag * (2 * e + 2.0**-18)).all()
         assert ((lse[:, head].double() - torch.logsumexp(z, -1)).abs() <= e + 2.0**-18 + 2.0**-20).all()
+
+
+@pytest.mark.parametrize("shape,window", [
+    ((14, 2, 64), 50),   # 18 queries a step: three steps an item
+    ((14, 2, 64), 75),   # five
+    ((5, 1, 64), 60),    # 25 queries a step: three
+    ((32, 8, 128), 96),  # 32 queries a step: three
+    ((32, 8, 128), 64),  # two
+    ((32, 8, 128), 20),  # one
+])
+def test_weights_of_items_with_an_odd_number_of_steps(shape, window):
+    """Several items, of several (sequence, KV head)s, on each SM: a step's columns stay while the items go by."""
+    H, h, d = shape
+    lens = [100, 77, 130, 96, 101, 60, 20, 99, 100, 140, 100, 75]
+    keys_of = [8000, 7000, 8100, 130, 9000, 2000, 8500, 900, 7333, 2500, 4096, 75]
+    assert sum(-(-m // 128) for m in keys_of) * h > 2 * 148
+    test_weights_of_every_way_to_share_the_work(shape, lens, keys_of, window)
+    rng = np.random.default_rng(window)
+    kv = context(*shape)
+    q, k, v = inputs(rng, shape, lens, keys_of)
+    cq, ck = i32(cu_of(lens)), i32(cu_of(keys_of))
+    lse = kv.prompt(q, k, v, cq, ck, max(lens))[1]
+    first = kv.prompt_weights(q, k, lse, cq, ck, max(keys_of), window)
+    for _ in range(50):
+        assert torch.equal(kv.prompt_weights(q, k, lse, cq, ck, max(keys_of), window), first)
+    assert kv.status() == 0
