@@ -452,7 +452,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_decode_kernel(const Decod
       // ---- running maximum (per head; the same in the eight lanes that share its columns)
       const float c0 = fmaxf(fmaxf(sa[0][0], sb[0][0]), fmaxf(sa[1][0], sb[1][0]));
       const float c1 = fmaxf(fmaxf(sa[0][1], sb[0][1]), fmaxf(sa[1][1], sb[1][1]));
-      if (__any_sync(0xffffffffu, c0 > mx[0] + kMoveMax || c1 > mx[1] + kMoveMax)) {
+      // (the difference is exact where it matters; a sum with kMoveMax may round up past the score)
+      if (__any_sync(0xffffffffu, c0 - mx[0] > kMoveMax || c1 - mx[1] > kMoveMax)) {
         float n0 = fmaxf(mx[0], c0), n1 = fmaxf(mx[1], c1);
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) {

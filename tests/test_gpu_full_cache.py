@@ -590,3 +590,48 @@ def test_calls_behind_close_are_refused():
         with pytest.raises(S.StarKVError) as e:
             call()
         assert e.value.code == S.ERR_INVALID_ARG
+
+
+def test_decode_of_scores_one_step_of_fp32_apart():
+    """Scores of 2^27 to 2^28 (log2), where fp32 numbers are 16 apart, that rise by one such step at a time: as far as the
+    running maximum lets a score pass it, and no farther (a probability of 2^16 is infinite in fp16)."""
+    S = skv()
+    shape = H, h, d = 64, 8, 64
+    rng = np.random.default_rng(27)
+    kv = context(*shape)
+    B, n = 8, 2048  # 64 units of 128 pages: each by one CTA, whose warps take 32 tokens of every 128 in turn
+    k = np.zeros((n, h, d), np.float32)
+    k[:, :, :32] = 1024
+    k[:, :, 32:] = (np.arange(n) // 128)[:, None, None]
+    v = rng.standard_normal((n, h, d)).astype(np.float32)
+    pages = np.zeros((n // 16, h, F.page_bytes(d)), np.uint8)
+    slots = np.arange(n)
+    F.write(pages, k, v, slots)
+    q = np.zeros((B, H, d), np.float32)
+    q[:, :, 0] = 2.0**20 * (0.75 + rng.integers(0, 28, (B, H)) / 128)  # bf16 numbers: products of 0.75 to 0.97 of 2^30
+    q[:, :, 32] = 64                                                   # the step of fp32 there
+    scale = np.float32(1.4426950408889634 / 8)
+    dots = q[:, :, :1].astype(np.float64) * 1024 + 64 * (np.arange(n) // 128)  # [B, H, n], exact in fp32
+    z = (dots.astype(np.float32) * scale).astype(np.float32)
+    assert (z >= 2.0**27).all() and (z < 2.0**28).all()
+    steps = z[:, :, ::128]
+    up, even = steps[:, :, 1:] == steps[:, :, :-1] + np.float32(16), steps[:, :, :-1] % 32 == 0
+    assert (up & ~even).sum() > 100 and (up & even).sum() > 100  # the sum of an odd multiple of 16 and 8 rounds up
+    cache = S.KV4Cache(kv.cfg, pages=torch.from_numpy(pages).cuda(), weights=torch.zeros((n // 16, h, 16), device="cuda"))
+    t = np.tile(np.arange(n // 16, dtype=np.int32), (B, 1))
+    kk, vv = F.values(pages, slots, d)
+    np.testing.assert_array_equal(kk, k)
+    for accumulate in (False, True):
+        out = kv.kv4_decode(cache, torch.from_numpy(q).bfloat16().cuda(), i32(t), i32([n] * B), accumulate=accumulate)
+        assert kv.status() == 0 and torch.isfinite(out).all()
+        x = z.astype(np.float64)
+        p = np.exp2(x - x.max(-1, keepdims=True))
+        p /= p.sum(-1, keepdims=True)
+        for head in range(H):
+            o, mag = p[:, head] @ vv[:, head // 8], p[:, head] @ np.abs(vv[:, head // 8])
+            # the output in bf16, v and p in fp16, ex2 and fp32 sums
+            tol = 2.0**-8 * np.abs(o) + 2.0**-10 * (mag + np.abs(vv).max()) + 2.0**-18 * mag
+            assert (np.abs(out[:, head].double().cpu().numpy() - o) <= tol).all()
+    want = p.reshape(B, h, 8, n).sum((0, 2))  # [h, n]
+    got = cache.weights.double().cpu().numpy().transpose(1, 0, 2).reshape(h, n)
+    assert (np.abs(got - want) <= 2.0**-17 * want + 2.0**-30).all()
