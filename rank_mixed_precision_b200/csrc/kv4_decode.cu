@@ -7,7 +7,7 @@
 // that a cut goes through leaves partial results, which a second kernel joins; where the
 // tables are short, a CTA takes a whole unit and there is no second kernel.
 // A CTA's four warps take a stretch's pages two at a time in turn, each with its own ring of
-// bulk copies (one 16-token page of one head is one contiguous copy), its own running maximum
+// bulk copies (one 16-token page of one head is one contiguous copy), its own reference of p
 // and sum, and its own output accumulators.  Scores and outputs run on mma.sync
 // m16n8k16: the eight query heads are the N of both products, so a page's codes are read
 // once for all of them.  With N = 8 the products are small (2 x 16 x 8 x D per page) and
@@ -23,8 +23,11 @@
 //     products are exact and the sums fp32: the probabilities that are added to the
 //     cache's weights keep fp32 accuracy.
 //   output   o[c, h] = sum_t v[t, c] p[t, h]
-//     A = V^T, widened to fp16 (code * s + z, one rounding), B = p in fp16 (at most 2^8
-//     against the running maximum, which moves only when it grows by more than that).
+//     A = V^T, widened to fp16 (code * s + z, one rounding), B = p in fp16.  p is taken against a
+//     reference 2^7 below the largest score when that last moved it, and the reference moves when p
+//     would pass 2^15: fp16 then holds probabilities down to 2^-32 of the largest (half a step; with the
+//     maximum itself as reference 2^-25, and the tail of a context of millions of tokens fell out of the
+//     output while the sum, in fp32, still held it).
 #include <algorithm>
 
 #include "full.cuh"
@@ -51,8 +54,9 @@ constexpr int kManyUnits = 64;
 // CTAs of a unit at most: more parts cost the join more than they spare.  (At most 32, 74, 148 and any
 // number, us: 8 heads of 128 over one, 100000 tokens 41, 26, 24, 46; 40 of 64 over one, 20000 tokens 14, 15, 19, 19.)
 constexpr int kMostParts = 74;
-constexpr float kMoveMax = 8.f;      // the running maximum moves when a score passes it by this (log2)
-constexpr float kNoMax = -3.402823466e38f;  // running maximum before the first score: finite, and below all scores
+constexpr float kBelow = 7.f;        // the reference of p, below the largest score (log2),
+constexpr float kMoveMax = 15.f;     // and how far scores may pass it before it moves: p <= 2^15, fp16 ends at 2^16
+constexpr float kNoMax = -3.402823466e38f;  // reference before the first score: finite, and below all scores
 
 struct DecodeArgs {
   const __nv_bfloat16* q;
@@ -62,8 +66,8 @@ struct DecodeArgs {
   float scale_log2;        // log2(e) / sqrt(D)
   Kv4Pool pool;
   __nv_bfloat16* out;
-  float* part_o;           // [ctas][2][8][D], relative to the part's maximum: [0] of a unit that began before the
-  float2* part_ml;         // [ctas][2][8] (maximum, sum)                     CTA's stretch, [1] of one that goes on behind
+  float* part_o;           // [ctas][2][8][D], relative to the part's reference: [0] of a unit that began before the
+  float2* part_ml;         // [ctas][2][8] (reference, sum)                   CTA's stretch, [1] of one that goes on behind
   float2* unit_ml;         // [B][units][8], of units within one CTA (NULL: not asked for)
   int64_t* before;         // [B + 1] pages before each sequence, and of all (ctas > 0)
   float* scores;           // [B][h_kv][max_pages * 16][score_heads], log2 units (NULL: not asked for)
@@ -449,12 +453,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_decode_kernel(const Decod
       }
       if (srow) srow += 2 * kWarps * kPage * a.score_heads;
       left -= 2 * kWarps * kPage;
-      // ---- running maximum (per head; the same in the eight lanes that share its columns)
+      // ---- reference (per head; the same in the eight lanes that share its columns)
       const float c0 = fmaxf(fmaxf(sa[0][0], sb[0][0]), fmaxf(sa[1][0], sb[1][0]));
       const float c1 = fmaxf(fmaxf(sa[0][1], sb[0][1]), fmaxf(sa[1][1], sb[1][1]));
       // (the difference is exact where it matters; a sum with kMoveMax may round up past the score)
       if (__any_sync(0xffffffffu, c0 - mx[0] > kMoveMax || c1 - mx[1] > kMoveMax)) {
-        float n0 = fmaxf(mx[0], c0), n1 = fmaxf(mx[1], c1);
+        float n0 = fmaxf(mx[0], c0 - kBelow), n1 = fmaxf(mx[1], c1 - kBelow);
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) {
           n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, w));
@@ -625,11 +629,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_decode_kernel(const Decod
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 constexpr int kJoinTokens = 4 * kJoinThreads;
-constexpr int kJoinHeads = 32;  // heads whose maximum and 1 / sum a pass holds
+constexpr int kJoinHeads = 32;  // heads whose reference and 1 / sum a pass holds
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads, 8) kv4_join_kernel(const DecodeArgs a) {
-  __shared__ float2 norm[kJoinHeads];  // maximum, 1 / sum
+  __shared__ float2 norm[kJoinHeads];  // reference, 1 / sum
   __shared__ float4 acc[kJoinThreads];
   const int tid = threadIdx.x;
   const int kv = blockIdx.y, b = blockIdx.z;
@@ -662,7 +666,7 @@ __global__ void __launch_bounds__(kJoinThreads, 8) kv4_join_kernel(const DecodeA
   for (int h0 = first_head; h0 < last_head; h0 += kJoinHeads) {
     const int heads = min(kJoinHeads, last_head - h0);
     __syncthreads();
-    // a warp, or eight threads, a head: the sequence's maximum and sum over its parts
+    // a warp, or eight threads, a head: the sequence's reference and sum over its parts
     {
       const int per = heads <= kJoinThreads / 32 ? 32 : 8, one = tid & (per - 1), hh = tid / per;
       const int h = h0 + hh;

@@ -635,3 +635,32 @@ def test_decode_of_scores_one_step_of_fp32_apart():
     want = p.reshape(B, h, 8, n).sum((0, 2))  # [h, n]
     got = cache.weights.double().cpu().numpy().transpose(1, 0, 2).reshape(h, n)
     assert (np.abs(got - want) <= 2.0**-17 * want + 2.0**-30).all()
+
+
+@pytest.mark.parametrize("shape,n,batch", [((8, 2, 64), 2000, 1), ((16, 2, 128), 2000, 1), ((14, 2, 64), 300, 3), ((64, 32, 128), 700, 3)])
+def test_decode_keeps_a_long_light_tail(shape, n, batch):
+    """One token in 32 takes nearly all of the weight, the others 2^-25 to 2^-30 of it each, and their values alone count."""
+    S = skv()
+    H, h, d = shape
+    kv = context(*shape)
+    tail = np.arange(n) % 32 != 5
+    k, v = np.zeros((n, h, d), np.float32), np.zeros((n, h, d), np.float32)
+    k[tail] = -32
+    v[tail] = 1
+    pages = np.zeros((-(-n // 16), h, F.page_bytes(d)), np.uint8)
+    F.write(pages, k, v, np.arange(n))
+    q = np.zeros((batch, H, d), np.float32)
+    q[:, :, 7] = 4.5 * (d / 64) ** 0.5 * (1 + np.arange(batch * H).reshape(batch, H) % 5 / 32)
+    qd = torch.from_numpy(q).bfloat16().cuda()
+    z = -32 * qd.double().cpu().numpy()[:, :, 7] / d**0.5 / np.log(2.0)
+    assert (z < -25).all() and (z > -30).all()
+    t = np.tile(np.arange(-(-n // 16), dtype=np.int32), (batch, 1))
+    cache = S.KV4Cache(kv.cfg, pages=torch.from_numpy(pages).cuda())
+    out = kv.kv4_decode(cache, qd, i32(t), i32([n] * batch)).double().cpu().numpy()
+    assert kv.status() == 0
+    p = np.exp2(z) * tail.sum()
+    want = (p / (p + (~tail).sum()))[..., None]
+    # the output in bf16; a probability's half step in fp16 against a maximum of 2^7 or more, 2^-32, each; score, ex2, sums
+    lost = tail.sum() / (~tail).sum() * 2.0**-32
+    assert (np.abs(out - want) <= want * (2.0**-8 + 2.0**-16) + lost).all()
+    assert (lost < want / 4).all()
