@@ -41,8 +41,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // 2^x for x <= 126 on the FMA pipe, for a part of the exponentials (the special function unit
 // takes 16 a cycle and SM, half as long again as the products of the same tile): x = n + f with
 // n = rint(x), 2^f by the polynomial of degree 5 of least relative error on [-1/2, 1/2] (Remez
-// exchange; 7.5e-8, in fp32 2.2e-7, as much as ex2.approx is off), 2^n from the bits of the sum
-// that rounds x.  Below -126.5 those bits are 0's; NaN passes through.
+// exchange; with its coefficients in fp32 1.55e-7, evaluated in fp32 2.14e-7, within ex2.approx's
+// 2^-22), 2^n from the bits of the sum that rounds x.  From -126.5 down those bits are 0's; NaN
+// passes through.
 __device__ __forceinline__ f32x2 ex2_fma(f32x2 x) {
   float2 y = unpair(x);
   x = pair(max_nan(y.x, -127.f), max_nan(y.y, -127.f));

@@ -465,3 +465,83 @@ def test_weights_of_items_with_an_odd_number_of_steps(shape, window):
     for _ in range(50):
         assert torch.equal(kv.prompt_weights(q, k, lse, cq, ck, max(keys_of), window), first)
     assert kv.status() == 0
+
+
+def test_weights_hold_the_bound_of_each_exponential():
+    """One column of a tile at a time: its weight is 2^x alone, x from -130 to 126, half-integers, and what is not finite."""
+    kv = context(4, 1, 64)
+    rng = np.random.default_rng(22)
+    B, n, m = 4096, 32, 160  # a sequence: one step of 32 queries x 4 heads, whose 128 columns all see the first 128 keys
+    scale, log2e = np.float32(1.4426950408889634 / 8), np.float32(1.4426950408889634)
+    s = ((np.arange(m) - 64) / 16).astype(np.float32)  # scores, bf16 numbers
+    base = rng.uniform(-130, 125, B).astype(np.float32)
+    base[:300] = np.arange(-130, 20)[np.arange(300) % 150] + np.float32(0.5)
+    lse = (base.astype(np.float64) / -np.float64(log2e)).astype(np.float32)
+    for step in range(-3, 4):  # lse whose product is the half-integer itself, where there is one
+        near = np.where(step < 0, -1, 1).astype(np.float32) * np.inf
+        y = lse[:300].copy()
+        for _ in range(abs(step)):
+            y = np.nextafter(y, near)
+        hit = (y * -log2e).astype(np.float32) == base[:300]
+        lse[:300][hit] = y[hit]
+    base = (lse * -log2e).astype(np.float32)
+    assert (base[:300] % 1 == 0.5).sum() > 150
+    lse[-2:] = np.nan, np.inf
+    col = np.concatenate([np.arange(300) // 150 + 2 + np.arange(300) % 8 * 16, np.arange(B - 300)]) % 128
+    q = torch.zeros((B, n, 4, 64), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1
+    k = torch.zeros((B, m, 1, 64), dtype=torch.bfloat16, device="cuda")
+    k[..., 0] = torch.from_numpy(s).cuda()[None, :, None]
+    ls = torch.full((B, n * 4), float("inf"), device="cuda")
+    ls[torch.arange(B), torch.from_numpy(col).cuda()] = torch.from_numpy(lse).cuda()
+    cq, ck = i32(np.arange(B + 1) * n), i32(np.arange(B + 1) * m)
+    w = kv.prompt_weights(q.view(B * n, 4, 64), k.view(B * m, 1, 64), ls.view(B * n, 4), cq, ck, m, n)
+    assert kv.status() == 0
+    w = w.view(B, m)[:, :128].cpu().numpy()
+    assert np.isnan(w[-2]).all() and (w[-1] == 0).all()
+    x = (s[:128].astype(np.longdouble) * np.longdouble(scale) + base[:-2, None].astype(np.longdouble)).astype(np.float32)
+    assert x.min() < -130 and x.max() > 125 and (x[:300] % 1 == 0.5).sum() > 150
+    want = np.exp2(x.astype(np.longdouble))
+    err = np.abs(w[:-2].astype(np.longdouble) - want)
+    # 2^-22 relative, of the special function unit's and of the polynomial; below 2^-126 either may be 0
+    bad = err > want * np.longdouble(2.0**-22) + np.where(x < -126, 2.0**-126, 0.0)
+    assert not bad.any(), (x[bad][:5], np.argwhere(bad)[:5], (err / want)[bad][:5])
+
+
+@pytest.mark.parametrize("shape,n_q,n_k,window", [
+    ((8, 2, 128), [64, 100], [1300, 700], 64),   # a window whose queries stay
+    ((14, 2, 64), [300, 90], [300, 400], 300),   # 126 columns of a tile hold heads
+    ((4, 4, 64), [700] * 40, [700] * 40, 700),   # items dealt to the SMs
+    ((16, 4, 64), [2500], [2500], 4000),         # pairs of CTAs
+])
+def test_weights_of_exact_scores(shape, n_q, n_k, window):
+    """Scores that fp32 holds exactly: what is left is the rounding of the exponent, of the exponential and of the sums."""
+    H, h, d = shape
+    G = H // h
+    kv = context(*shape)
+    g = torch.Generator(device="cuda").manual_seed(window)
+    q = torch.randint(-2, 3, (sum(n_q), H, d), generator=g, device="cuda").bfloat16()
+    k = torch.randint(-2, 3, (sum(n_k), h, d), generator=g, device="cuda").bfloat16()
+    cq, ck = cu_of(n_q), cu_of(n_k)
+    scale, log2e = float(np.float32(1.4426950408889634 / d**0.5)), 1.4426950408889634
+    lse = torch.empty((sum(n_q), H), device="cuda")
+    want = torch.zeros((sum(n_k), h), dtype=torch.float64, device="cuda")
+    tol = torch.zeros_like(want)
+    for b, (n, m) in enumerate(zip(n_q, n_k)):
+        seen = torch.arange(m, device="cuda")[None] <= (m - n + torch.arange(n, device="cuda"))[:, None]
+        first = max(0, n - window)
+        for i in range(H):
+            z = q[cq[b]:cq[b + 1], i].double() @ k[ck[b]:ck[b + 1], i // G].double().t()
+            l = torch.logsumexp(torch.where(seen, z, -torch.inf) / d**0.5, -1).float()
+            lse[cq[b]:cq[b + 1], i] = l
+            x = z * (log2e / d**0.5) - l[:, None].double() * log2e
+            p = torch.where(seen, torch.exp2(x), 0.0)[first:]
+            # the scale's half step, those of log2(e) and of its product with lse, and of the sum: all times ln 2; and 2^-22
+            e = ((z * scale).abs() + 2 * (l[:, None].double() * log2e).abs() + x.abs())[first:] * 2.0**-24 * 0.6932 + 2.0**-22
+            want[ck[b]:ck[b + 1], i // G] += p.sum(0)
+            tol[ck[b]:ck[b + 1], i // G] += (p * e).sum(0)
+    w = kv.prompt_weights(q, k, lse, i32(cq), i32(ck), max(n_k), window).double()
+    assert kv.status() == 0
+    # fp32 sums: 64 columns in four sums of 16, then those, the steps of an item, four groups of warps, eight CTAs
+    steps = max(n_q) // (128 // G) + 1
+    assert ((w - want).abs() <= tol + want * ((32 + 3 + steps + 4 + 8) * 2.0**-24) + 2.0**-126).all(), ((w - want).abs() / want).max()
