@@ -1,4 +1,6 @@
 // C entry points of full-width layers (include/starkv_full.h): argument checks and launches.
+#include <algorithm>
+
 #include "full.cuh"
 
 using namespace starkv;
@@ -191,6 +193,7 @@ starkv_status starkv_prompt_attn(starkv_ctx* ctx, const void* q, const void* k, 
   if (st) return st;
   if (!out || !aligned(out, 16) || !aligned(lse, 4))
     return fail(STARKV_ERR_INVALID_ARG, "out must be given and 16-byte aligned, lse 4-byte");
+  max_q_len = (int32_t)std::min<int64_t>(max_q_len, total_q);  // a loose bound launches no blocks of its own
   const PromptPlan plan = plan_prompt(*c, batch, total_q, total_k, max_q_len);
   if (plan.blocks > kMaxBlocks) return fail(STARKV_ERR_UNSUPPORTED_SHAPE, "too many blocks");
   if (plan.ws_bytes > 0 && (!workspace || workspace_bytes < plan.ws_bytes))
@@ -222,6 +225,7 @@ starkv_status starkv_prompt_weights(starkv_ctx* ctx, const void* q, const void* 
   if (st) return st;
   if ((total_q > 0 && !lse) || !weights || !aligned(lse, 4) || !aligned(weights, 4))
     return fail(STARKV_ERR_INVALID_ARG, "lse and weights must be given and 4-byte aligned");
+  max_k_len = (int32_t)std::min<int64_t>(max_k_len, total_k);
   if (weights_items(*c, batch, max_k_len) > kMaxBlocks) return fail(STARKV_ERR_UNSUPPORTED_SHAPE, "too many key tiles");
   PromptArgs a{(const __nv_bfloat16*)q, (const __nv_bfloat16*)k, nullptr, q_stride, k_stride, 0, cu_q, cu_k, batch,
                total_q, total_k};

@@ -1608,7 +1608,7 @@ cudaError_t launch_prompt_attn(const Ctx& c, const PromptArgs& p, int max_q_len,
                                void* ws, const PromptPlan& plan, cudaStream_t s) {
   PromptKArgs a = args_of(c, p);
   a.max_q = max_q_len;
-  a.qtiles = (max_q_len + 2 * a.R - 1) / (2 * a.R);
+  a.qtiles = (int)(((int64_t)max_q_len + 2 * a.R - 1) / (2 * a.R));
   a.out = out;
   a.lse = lse;
   a.ctas = plan.ctas;
@@ -1634,7 +1634,7 @@ cudaError_t launch_prompt_weights(const Ctx& c, const PromptArgs& p, const float
   if (!map_kv(c, p.k, p.k_stride, p.total_k, &km)) return cudaErrorInvalidValue;
   qm = km;  // no queries at all: nothing is copied
   if (p.total_q > 0 && !map_q(c, p, a, &qm)) return cudaErrorInvalidValue;
-  a.ktiles = (max_k_len + kTile - 1) / kTile;
+  a.ktiles = (int)(((int64_t)max_k_len + kTile - 1) / kTile);
   int sms = 148;
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c.device);
   return c.cfg.head_dim == 64 ? launch_weights_d<64>(qm, km, a, sms, s) : launch_weights_d<128>(qm, km, a, sms, s);

@@ -545,3 +545,23 @@ def test_weights_of_exact_scores(shape, n_q, n_k, window):
     # fp32 sums: 64 columns in four sums of 16, then those, the steps of an item, four groups of warps, eight CTAs
     steps = max(n_q) // (128 // G) + 1
     assert ((w - want).abs() <= tol + want * ((32 + 3 + steps + 4 + 8) * 2.0**-24) + 2.0**-126).all(), ((w - want).abs() / want).max()
+
+
+def test_prompt_and_weights_with_loose_bounds():
+    """max_q_len and max_k_len far above any length, up to 2^31 - 1."""
+    shape = (8, 2, 64)
+    rng = np.random.default_rng(31)
+    kv = context(*shape)
+    for n_q, n_k in (([70, 9, 130], [200, 9, 130]), ([300], [2000]), ([300], [300])):
+        q, k, v = inputs(rng, shape, n_q, n_k)
+        cq, ck = i32(cu_of(n_q)), i32(cu_of(n_k))
+        out, lse = kv.prompt(q, k, v, cq, ck, max(n_q))
+        check_prompt(kv, shape, q, k, v, n_q, n_k, out, lse)
+        for most in (max(n_q) + 1, 1 << 17, (1 << 31) - 1):
+            o2, l2 = kv.prompt(q, k, v, cq, ck, most)
+            assert torch.equal(out, o2) and torch.equal(lse, l2)
+        for window in (20, 10**6):
+            for most in (1 << 17, (1 << 31) - 1):
+                w = kv.prompt_weights(q, k, lse, cq, ck, most, window)
+                check_prompt(kv, shape, q, k, v, n_q, n_k, out, lse, w, window)
+    assert kv.status() == 0
