@@ -399,6 +399,14 @@ def _one_device(first, *others):
             raise ValueError(f"an argument is on {t.device}, the current device is cuda:{at}")
 
 
+def _int32(x, name):
+    """x as a C int32, which ctypes would cut to its low 32 bits."""
+    x = int(x)
+    if not -1 << 31 <= x < 1 << 31:
+        raise ValueError(f"{name} {x} does not fit into 32 bits")
+    return x
+
+
 def _on(stream):
     """The stream's handle; None: the current stream of the current device."""
     if stream is None:
@@ -507,9 +515,9 @@ def _check_evict(block_table, seq_lens, keep_lens, dst_block_table):
 
 def _call_evict(ctx, cache, block_table, seq_lens, keep_lens, recent, dst_block_table, new_lens, kept, stream):
     B, pages = block_table.shape
-    _check(lib().starkv_kv4_evict(ctx, ctypes.byref(cache), _at(block_table), _at(seq_lens), _at(keep_lens), int(recent),
-                                  B, pages, _at(dst_block_table), dst_block_table.shape[1], _at(new_lens), _at(kept),
-                                  _on(stream)))
+    _check(lib().starkv_kv4_evict(ctx, ctypes.byref(cache), _at(block_table), _at(seq_lens), _at(keep_lens),
+                                  _int32(recent, "recent"), B, pages, _at(dst_block_table), dst_block_table.shape[1],
+                                  _at(new_lens), _at(kept), _on(stream)))
 
 
 def starkv_kv4_evict(ctx, cfg, cache: starkv_kv4_cache, block_table, seq_lens, keep_lens, recent, dst_block_table,
@@ -551,8 +559,8 @@ def _check_prompt(cfg, q, k, v, cu_q, cu_k):
 
 def _call_prompt(ctx, q, k, v, strides, cu_q, cu_k, max_q_len, out, lse, workspace, stream):
     _check(lib().starkv_prompt_attn(ctx, _at(q), _at(k), _at(v), *strides, _at(cu_q), _at(cu_k), cu_q.shape[0] - 1,
-                                    q.shape[0], k.shape[0], int(max_q_len), _at(out), _at(lse), _at(workspace),
-                                    0 if workspace is None else workspace.numel(), _on(stream)))
+                                    q.shape[0], k.shape[0], _int32(max_q_len, "max_q_len"), _at(out), _at(lse),
+                                    _at(workspace), 0 if workspace is None else workspace.numel(), _on(stream)))
 
 
 def starkv_prompt_attn(ctx, cfg, q, k, v, cu_q, cu_k, max_q_len, out, lse=None, workspace=None, stream=None):
@@ -580,8 +588,8 @@ def starkv_prompt_weights(ctx, cfg, q, k, lse, cu_q, cu_k, max_k_len, window, we
         raise ValueError("lse must be [total_q, num_q_heads] and weights [total_k, num_kv_heads]")
     _one_device(q, k, lse, cu_q, cu_k, weights)
     _check(lib().starkv_prompt_weights(ctx, _at(q), _at(k), qs, ks, _at(lse), _at(cu_q), _at(cu_k), cu_q.shape[0] - 1,
-                                       q.shape[0], k.shape[0], int(max_k_len), int(window), _at(weights),
-                                       _on(stream)))
+                                       q.shape[0], k.shape[0], _int32(max_k_len, "max_k_len"), _int32(window, "window"),
+                                       _at(weights), _on(stream)))
 
 
 # ---------------------------------------------------------------------------

@@ -131,3 +131,10 @@ def test_oracle_eviction_against_a_sort():
         w2[n - min(keep, recent):] = 100
         want = np.sort(np.argsort(-w2, kind="stable")[:keep])
         np.testing.assert_array_equal(got, want)
+
+
+def test_whole_numbers_that_a_c_int_cannot_hold_are_refused(S):
+    assert S._int32((1 << 31) - 1, "window") == (1 << 31) - 1 and S._int32(np.int64(7), "window") == 7
+    for x in (1 << 31, 1 << 32, (1 << 32) + 5, -(1 << 31) - 1, 1 << 63):
+        with pytest.raises(ValueError):
+            S._int32(x, "window")

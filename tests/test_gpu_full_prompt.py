@@ -565,3 +565,20 @@ def test_prompt_and_weights_with_loose_bounds():
                 w = kv.prompt_weights(q, k, lse, cq, ck, most, window)
                 check_prompt(kv, shape, q, k, v, n_q, n_k, out, lse, w, window)
     assert kv.status() == 0
+
+
+def test_numbers_of_more_than_32_bits_are_refused():
+    """They would reach the library cut to their low 32 bits: a window of 2^32 as none."""
+    shape = (8, 2, 64)
+    kv = context(*shape)
+    q, k, v = inputs(np.random.default_rng(1), shape, [20], [20])
+    cu = i32([0, 20])
+    lse = kv.prompt(q, k, v, cu, cu, 20)[1]
+    cache = kv.new_kv4_cache(4, keep_weights=True)
+    table, lens = i32([[0, 1]]), i32([20])
+    for call in (lambda x: kv.prompt(q, k, v, cu, cu, x), lambda x: kv.prompt_weights(q, k, lse, cu, cu, x, 4),
+                 lambda x: kv.prompt_weights(q, k, lse, cu, cu, 20, x), lambda x: kv.kv4_evict(cache, table, lens, lens, x, i32([[2, 3]]))):
+        for x in (1 << 32, (1 << 32) + 20, 1 << 31):
+            with pytest.raises(ValueError):
+                call(x)
+    assert kv.status() == 0
