@@ -190,6 +190,9 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadArgs a)
   __shared__ int64_t slot_of[T];
   pdl_wait();
   pdl_launch_dependents();
+  if (blockIdx.x == 0 && blockIdx.y == 0)  // a row's own sequence does not show that another's bounds fall
+    for (int i = threadIdx.x; i < a.batch; i += kRowThreads)
+      if (a.cu[i + 1] < a.cu[i]) set_status(a.status, STARKV_DEV_BAD_QUERY_SPAN);
   const int64_t row0 = (int64_t)blockIdx.x * T;
   if (threadIdx.x < T) slot_of[threadIdx.x] = row0 + threadIdx.x < a.total ? slot_of_row(a, row0 + threadIdx.x) : -1;
   __syncthreads();

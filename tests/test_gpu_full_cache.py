@@ -664,3 +664,25 @@ def test_decode_keeps_a_long_light_tail(shape, n, batch):
     lost = tail.sum() / (~tail).sum() * 2.0**-32
     assert (np.abs(out - want) <= want * (2.0**-8 + 2.0**-16) + lost).all()
     assert (lost < want / 4).all()
+
+
+@pytest.mark.parametrize("batch,many", [(3, 1), (400, 100)])
+def test_read_reports_bounds_that_fall(batch, many):
+    """cu = 0 .. 5, 3 .. 9: every row lies in some sequence, but one sequence ends before it begins."""
+    S = skv()
+    H, h, d = 4, 2, 64
+    kv = context(H, h, d)
+    pages, t, _ = fill(np.random.default_rng(16), [40] * 4, h, d)
+    cache = S.KV4Cache(kv.cfg, pages=torch.from_numpy(pages).cuda())
+    table = i32(np.tile(t[:1], (batch, 1)))
+    good = np.zeros(batch + 1, np.int32)
+    good[batch - 2:batch], good[batch] = 5 * many, 9 * many
+    cu = good.copy()
+    cu[batch - 1] = 3 * many
+    starts = i32(np.zeros(batch))
+    if many > 1:
+        table = i32(np.tile(np.resize(t[0], (1, 64)), (batch, 1)))
+    kv.kv4_read(cache, table, i32(good), 9 * many, starts=starts)
+    assert kv.status() == 0
+    kv.kv4_read(cache, table, i32(cu), 9 * many, starts=starts)
+    assert kv.status() == S.DEV_BAD_QUERY_SPAN
