@@ -36,7 +36,7 @@ extern "C" {
 
 #define STARKV_KV4_GROUP 32 /* channels that share a scale and a zero */
 
-/* starkv_workspace_bytes, a further op. */
+/* starkv_workspace_bytes, a further op.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE (of the call). */
 enum {
   STARKV_OP_KV4_DECODE = 16 /* starkv_kv4_decode_attn; total_q: its `accumulate` */
 };
@@ -72,7 +72,8 @@ typedef struct starkv_kv4_sizes {
   int32_t groups;          /* d / 32                                     */
 } starkv_kv4_sizes;
 
-/* Host-only: sizes of a 4-bit cache of n_pages pages.  Errors: as starkv_cache_layout. */
+/* Host-only: sizes of a 4-bit cache of n_pages pages.  Errors: as starkv_cache_layout, and
+ * UNSUPPORTED_SHAPE for 2^63 bytes or more. */
 STARKV_API starkv_status starkv_kv4_layout(const starkv_config* cfg, int64_t n_pages, starkv_kv4_sizes* out);
 
 /* Quantise n tokens' keys and values into the cache.  k, v: device bf16
@@ -161,7 +162,8 @@ STARKV_API starkv_status starkv_prompt_attn(starkv_ctx* ctx, const void* q, cons
                                             void* workspace, size_t workspace_bytes, starkv_stream_t stream);
 
 /* Workspace bytes of starkv_prompt_attn for packed rows of these sizes (40 MB at most, where
- * units of its work are shared between SMs).  out: host.  Errors: INVALID_ARG. */
+ * units of its work are shared between SMs).  out: host.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE
+ * (more than 65535 sequences, 2^31 rows). */
 STARKV_API starkv_status starkv_prompt_workspace_bytes(const starkv_ctx* ctx, int32_t batch, int64_t total_q,
                                                        int64_t total_k, size_t* out);
 

@@ -534,8 +534,8 @@ starkv_status starkv_workspace_bytes(const starkv_ctx* ctx, int32_t op, int32_t 
     *out = decode_out_ws(*c, batch, max_pages).total;
   } else if (op == STARKV_OP_PREFILL) {
     *out = plan_prefill(*c, batch, max_pages, total_q).ws_bytes;
-  } else if (!full_workspace_bytes(*c, op, batch, max_pages, total_q, out)) {
-    return fail(STARKV_ERR_INVALID_ARG, "unknown op %d", op);
+  } else {
+    return full_workspace_bytes(*c, op, batch, max_pages, total_q, out);
   }
   return ok();
 }

@@ -1,5 +1,6 @@
 // C entry points of full-width layers (include/starkv_full.h): argument checks and launches.
 #include <algorithm>
+#include <cstdint>
 
 #include "full.cuh"
 
@@ -33,10 +34,16 @@ starkv_status check_cache(const starkv_kv4_cache* cache) {
   return STARKV_OK;
 }
 
-starkv_status check_tables(int32_t batch, int32_t max_pages) {
+starkv_status check_sizes(int32_t batch, int32_t max_pages) {
   if (batch < 0 || max_pages < 0) return fail(STARKV_ERR_INVALID_ARG, "negative size");
   if (batch > kMaxGrid) return fail(STARKV_ERR_UNSUPPORTED_SHAPE, "batch %d: at most %d", batch, kMaxGrid);
   if (max_pages > kMaxPages) return fail(STARKV_ERR_UNSUPPORTED_SHAPE, "max_pages %d: at most %d", max_pages, kMaxPages);
+  return STARKV_OK;
+}
+
+starkv_status check_tables(int32_t batch, int32_t max_pages) {
+  const starkv_status st = check_sizes(batch, max_pages);
+  if (st) return st;
   if (batch > 0 && max_pages == 0) return fail(STARKV_ERR_INVALID_ARG, "max_pages must be >= 1");
   return STARKV_OK;
 }
@@ -64,10 +71,12 @@ starkv_status check_packed(const Ctx* c, const void* q, const void* k, int64_t q
 }  // namespace
 
 namespace starkv {
-bool full_workspace_bytes(const Ctx& c, int op, int batch, int max_pages, int64_t total_q, size_t* out) {
-  if (op != STARKV_OP_KV4_DECODE) return false;
+starkv_status full_workspace_bytes(const Ctx& c, int op, int batch, int max_pages, int64_t total_q, size_t* out) {
+  if (op != STARKV_OP_KV4_DECODE) return fail(STARKV_ERR_INVALID_ARG, "unknown op %d", op);
+  const starkv_status st = check_sizes(batch, max_pages);
+  if (st) return st;
   *out = plan_kv4_decode(c, batch, max_pages, total_q != 0).ws_bytes;
-  return true;
+  return ok();
 }
 }  // namespace starkv
 
@@ -78,6 +87,8 @@ starkv_status starkv_kv4_layout(const starkv_config* cfg, int64_t n_pages, stark
   if (st) return st;
   if (!out) return fail(STARKV_ERR_INVALID_ARG, "out is NULL");
   if (n_pages < 0) return fail(STARKV_ERR_INVALID_ARG, "n_pages < 0");
+  if (n_pages > INT64_MAX / cfg->num_kv_heads / kv4_page_bytes(cfg->head_dim))
+    return fail(STARKV_ERR_UNSUPPORTED_SHAPE, "n_pages %lld: 2^63 bytes or more", (long long)n_pages);
   out->head_page_bytes = kv4_page_bytes(cfg->head_dim);
   out->groups = cfg->head_dim / STARKV_KV4_GROUP;
   out->pages_bytes = n_pages * cfg->num_kv_heads * out->head_page_bytes;
@@ -238,6 +249,8 @@ starkv_status starkv_prompt_workspace_bytes(const starkv_ctx* ctx, int32_t batch
                                             size_t* out) {
   if (!ctx || !out) return fail(STARKV_ERR_INVALID_ARG, "NULL argument");
   if (batch < 0 || total_q < 0 || total_k < 0) return fail(STARKV_ERR_INVALID_ARG, "negative size");
+  if (batch > kMaxGrid) return fail(STARKV_ERR_UNSUPPORTED_SHAPE, "batch %d: at most %d", batch, kMaxGrid);
+  if (total_q > 0x7fffffff || total_k > 0x7fffffff) return fail(STARKV_ERR_UNSUPPORTED_SHAPE, "2^31 rows or more");
   *out = batch == 0 || total_q == 0 ? 0 : plan_prompt(*reinterpret_cast<const Ctx*>(ctx), batch, total_q, total_k, 1).ws_bytes;
   return ok();
 }

@@ -100,8 +100,8 @@ starkv_status ok();
 starkv_status cuda_fail(cudaError_t e, const char* what);
 // Checks a configuration; key, val: the latents' geometry (NULL to skip).
 starkv_status check_config(const starkv_config* c, LatentGeom* key, LatentGeom* val);
-// Workspace of the full-width entries (full_api.cu); false for an op that is none of theirs.
-bool full_workspace_bytes(const Ctx& c, int op, int batch, int max_pages, int64_t total_q, size_t* out);
+// Workspace of the full-width entries (full_api.cu); refuses an op that is none of theirs.
+starkv_status full_workspace_bytes(const Ctx& c, int op, int batch, int max_pages, int64_t total_q, size_t* out);
 
 // 2-D TMA map over a row-major [rows][inner] array (no interleave, zero fill).
 bool encode_map_2d(CUtensorMap* map, CUtensorMapDataType type, void* base, uint64_t inner, uint64_t rows,

@@ -138,3 +138,13 @@ def test_whole_numbers_that_a_c_int_cannot_hold_are_refused(S):
     for x in (1 << 31, 1 << 32, (1 << 32) + 5, -(1 << 31) - 1, 1 << 63):
         with pytest.raises(ValueError):
             S._int32(x, "window")
+
+
+def test_layout_of_more_bytes_than_64_bits_count_is_refused(S):
+    cfg = S.make_config(8, 4, 64, 64, 16, 64, 16)
+    most = ((1 << 63) - 1) // (4 * F.page_bytes(64))
+    assert S.starkv_kv4_layout(cfg, most)["pages_bytes"] == most * 4 * F.page_bytes(64)
+    for n in (most + 1, 1 << 60, (1 << 63) - 1):
+        with pytest.raises(S.StarKVError) as e:
+            S.starkv_kv4_layout(cfg, n)
+        assert e.value.code == S.ERR_UNSUPPORTED_SHAPE

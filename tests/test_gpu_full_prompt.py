@@ -582,3 +582,25 @@ def test_numbers_of_more_than_32_bits_are_refused():
             with pytest.raises(ValueError):
                 call(x)
     assert kv.status() == 0
+
+
+def test_workspace_sizes_of_shapes_that_the_calls_refuse_are_refused():
+    S = skv()
+    kv = context(8, 2, 64)
+    most = (1 << 31) - 1
+    for call in (lambda: S.starkv_workspace_bytes(kv.ctx, S.OP_KV4_DECODE, 1 << 16, 10, 1),
+                 lambda: S.starkv_workspace_bytes(kv.ctx, S.OP_KV4_DECODE, most, most, 1),
+                 lambda: S.starkv_workspace_bytes(kv.ctx, S.OP_KV4_DECODE, 1, (1 << 26) + 1, 0),
+                 lambda: S.starkv_prompt_workspace_bytes(kv.ctx, 1 << 16, 100, 100),
+                 lambda: S.starkv_prompt_workspace_bytes(kv.ctx, 1, 1 << 31, 100),
+                 lambda: S.starkv_prompt_workspace_bytes(kv.ctx, 1, 100, 1 << 62)):
+        with pytest.raises(S.StarKVError) as e:
+            call()
+        assert e.value.code == S.ERR_UNSUPPORTED_SHAPE
+    with pytest.raises(S.StarKVError) as e:
+        S.starkv_workspace_bytes(kv.ctx, 99, 1, 1, 0)
+    assert e.value.code == S.ERR_INVALID_ARG
+    # the largest that they take: 4 bytes a token and query head, and the parts
+    assert 65535 * (1 << 26) * 16 * 8 * 4 <= S.starkv_workspace_bytes(kv.ctx, S.OP_KV4_DECODE, 65535, 1 << 26, 1) < 65535 * (1 << 26) * 16 * 8 * 5
+    assert S.starkv_workspace_bytes(kv.ctx, S.OP_KV4_DECODE, 0, 0, 0) >= 0 and S.starkv_prompt_workspace_bytes(kv.ctx, 0, 0, 0) == 0
+    assert S.starkv_prompt_workspace_bytes(kv.ctx, 65535, most, most) <= 40 << 20
