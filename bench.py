@@ -29,6 +29,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import socket
 import statistics
 import subprocess
@@ -54,6 +55,8 @@ HEADLINE = "llama3_8b_gqa_decode_b32_t4096to8192"
 SUBRECORDS = ["longchat7b_decode_b16_t4096", "longchat7b_stream_b1_t32768_s128",
               "longchat7b_prefill_b4_t30720_c2048"]
 CSRC = os.path.join(ROOT, "rank_mixed_precision_b200", "csrc")
+# the kernels of append, decode and prefill, and the context that plans them
+BENCH_SOURCES = ["api.cu", "append_tc.cu", "decode.cu", "decode_tc.cu", "prefill.cu", "prefill_tc.cu", "quant.cu"]
 TRAFFIC_TABLE = os.path.join(ROOT, "profiles", "dram_traffic.txt")
 
 
@@ -284,14 +287,27 @@ def measured_tensor_peak():
     return FALLBACK_BF16_TFLOPS_SUSTAINED, "fallback, sustained"
 
 
+def kernel_sources() -> list[str]:
+    """The CUDA sources that the timed calls are built from: BENCH_SOURCES and the
+    headers of csrc/ that they include, directly or through each other."""
+    todo, seen = [f for f in BENCH_SOURCES if os.path.exists(os.path.join(CSRC, f))], set()
+    while todo:
+        name = todo.pop()
+        if name in seen:
+            continue
+        seen.add(name)
+        text = open(os.path.join(CSRC, name)).read()
+        todo += [f for f in re.findall(r'^\s*#include\s+"([^"/]+)"', text, re.M) if os.path.exists(os.path.join(CSRC, f))]
+    return sorted(seen)
+
+
 def kernel_source_digest() -> str:
-    """Digest of the library's CUDA sources: DRAM traffic counted on one version
-    of the kernels is reported only while the sources are unchanged."""
+    """Digest of kernel_sources(): DRAM traffic counted on one version of the
+    kernels is reported only while their sources are unchanged."""
     h = hashlib.sha256()
-    for name in sorted(os.listdir(CSRC)):
-        if name.endswith((".cu", ".cuh", ".h")):
-            h.update(name.encode())
-            h.update(open(os.path.join(CSRC, name), "rb").read())
+    for name in kernel_sources():
+        h.update(name.encode())
+        h.update(open(os.path.join(CSRC, name), "rb").read())
     return h.hexdigest()[:16]
 
 

@@ -325,3 +325,22 @@ def test_traffic_is_reported_only_for_the_captured_kernels(tmp_path, monkeypatch
     assert bench.dram_traffic("wl2", "decode_call")[0] is None
     assert "changed" in bench.dram_traffic("wl2", "decode_call")[1]
     assert bench.dram_traffic("other", "decode_call")[0] is None
+
+
+def test_traffic_digest_covers_the_timed_kernels_sources_and_no_others(tmp_path, monkeypatch):
+    """A change to what the timed calls are built from voids a capture; one to the full-width entries does not."""
+    import shutil
+    own = {"full.cuh", "full_api.cu", "kv4.cu", "kv4_decode.cu", "prompt_tc.cu"}
+    assert set(bench.kernel_sources()) == set(os.listdir(bench.CSRC)) - own
+    csrc = tmp_path / "csrc"
+    shutil.copytree(bench.CSRC, csrc)
+    monkeypatch.setattr(bench, "CSRC", str(csrc))
+    before = bench.kernel_source_digest()
+    for name in sorted(os.listdir(csrc)):
+        with open(csrc / name, "a") as f:
+            f.write("// more\n")
+        after = bench.kernel_source_digest()
+        assert (after == before) == (name in own), name
+        before = after
+    (csrc / "other.cu").write_text("// a new source of another entry\n")
+    assert bench.kernel_source_digest() == before
