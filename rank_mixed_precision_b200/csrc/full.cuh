@@ -25,6 +25,32 @@ struct Kv4 {
 
 inline int kv4_page_bytes(int d) { return kPage * d + 2 * kPage * 4 * (d / STARKV_KV4_GROUP); }
 
+// 2^x on the special function unit (2^-22 relative; results below 2^-126 are 0).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Work laid end to end and cut evenly: the position at which CTA c's stretch begins, and the CTA
+// whose stretch holds position x < total.  Where there are fewer positions than CTAs, the last CTAs
+// have none: no stretch between two others is empty.
+__device__ __forceinline__ int64_t cut(int64_t c, int64_t total, int ctas) {
+  return total <= ctas ? min(c, total) : c * total / ctas;
+}
+__device__ __forceinline__ int64_t cta_of(int64_t x, int64_t total, int ctas) {
+  if (total <= ctas) return x;
+  const int64_t y = (x + 1) * ctas - 1;
+  // (a division in 64 bits is hundreds of cycles of a join's short life)
+  return (y | total) >> 32 == 0 ? (int64_t)((uint32_t)y / (uint32_t)total) : y / total;
+}
+
+inline int sm_count(const Ctx& c) {
+  int n = 148;
+  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, c.device);
+  return n;
+}
+
 struct Kv4Pool {
   uint8_t* pages;
   float* weights;

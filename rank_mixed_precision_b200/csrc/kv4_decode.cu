@@ -104,12 +104,6 @@ __device__ __forceinline__ int64_t block_sum(int64_t value, int64_t* sum) {
   return value;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -133,19 +127,6 @@ __device__ __forceinline__ uint32_t movm_trans(uint32_t x) {
 // bijection serves.  With this one the two rows of neighbouring lanes (e = 0, 1) lie in different
 // halves of the 32 banks, and so do V's four rows of a load (t = 0..3).
 __device__ __forceinline__ int token_of(int t, int e, int f) { return 8 * f + 4 * e + ((t + e) & 3); }
-
-// Position of the first page of CTA c's stretch, and the CTA whose stretch holds position x < total.
-// Where there are fewer pages than CTAs, the last CTAs have none: no stretch between two others
-// is empty.
-__device__ __forceinline__ int64_t cut(int64_t c, int64_t total, int ctas) {
-  return total <= ctas ? min(c, total) : c * total / ctas;
-}
-__device__ __forceinline__ int64_t cta_of(int64_t x, int64_t total, int ctas) {
-  if (total <= ctas) return x;
-  const int64_t y = (x + 1) * ctas - 1;
-  // (a division in 64 bits is hundreds of cycles of the join's short life)
-  return (y | total) >> 32 == 0 ? (int64_t)((uint32_t)y / (uint32_t)total) : y / total;
-}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, kCtas) kv4_decode_kernel(const DecodeArgs a) {
@@ -798,8 +779,7 @@ Kv4DecodePlan plan_kv4_decode(const Ctx& c, int batch, int max_pages, bool accum
   const starkv_config& f = c.cfg;
   p.head_blocks = (c.group + kHeads - 1) / kHeads;
   p.units = f.num_kv_heads * p.head_blocks;
-  int sms = 148;
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c.device);
+  const int sms = sm_count(c);
   // one round of CTAs at most, with 8 pages (a pair a warp) at least where the tables are full
   const bool whole = max_pages <= ((int64_t)batch * p.units >= kManyUnits ? kWholePagesMany : kWholePages);
   const int64_t most = (int64_t)batch * p.units * max_pages;

@@ -21,12 +21,6 @@ constexpr float kMoveMax = 8.f;       // the running maximum moves when a score 
 
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) { return p + ((1024u - (smem_u32(p) & 1023u)) & 1023u); }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -147,16 +141,6 @@ __device__ __forceinline__ SeqSpan span_of(const PromptKArgs& a, int b) {
   s.k0 = k0;
   s.keys = k1 - k0;
   return s;
-}
-
-// Position at which CTA c's stretch begins, and the CTA whose stretch holds position x < total.
-// Where there are fewer positions than CTAs, the last CTAs have none: no stretch between two
-// others is empty.
-__device__ __forceinline__ int64_t cut(int64_t c, int64_t total, int ctas) {
-  return total <= ctas ? min(c, total) : c * total / ctas;
-}
-__device__ __forceinline__ int64_t cta_of(int64_t x, int64_t total, int ctas) {
-  return total <= ctas ? x : ((x + 1) * ctas - 1) / total;
 }
 
 // ===========================================================================
@@ -1588,8 +1572,7 @@ PromptPlan plan_prompt(const Ctx& c, int batch, int64_t total_q, int64_t total_k
   const int64_t units = (int64_t)a.h_kv * a.head_blocks;
   p.blocks = ((int64_t)max_q_len + 2 * a.R - 1) / (2 * a.R) * units * batch;
   if (total_k <= kFewKeys) return p;
-  int sms = 148;
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c.device);
+  const int sms = sm_count(c);
   // at most so many pairs of query tiles, and key tiles of one
   const int64_t pairs = total_q / (2 * a.R) + batch, tiles = (total_k + kTile - 1) / kTile;
   if (total_k * a.h_kv * c.cfg.head_dim * 4 > kMostCached && total_q / (2 * a.R) * units >= sms) return p;
@@ -1635,8 +1618,7 @@ cudaError_t launch_prompt_weights(const Ctx& c, const PromptArgs& p, const float
   qm = km;  // no queries at all: nothing is copied
   if (p.total_q > 0 && !map_q(c, p, a, &qm)) return cudaErrorInvalidValue;
   a.ktiles = (int)(((int64_t)max_k_len + kTile - 1) / kTile);
-  int sms = 148;
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c.device);
+  const int sms = sm_count(c);
   return c.cfg.head_dim == 64 ? launch_weights_d<64>(qm, km, a, sms, s) : launch_weights_d<128>(qm, km, a, sms, s);
 }
 
