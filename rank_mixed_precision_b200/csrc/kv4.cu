@@ -658,7 +658,7 @@ cudaError_t launch_kv4_read(const Ctx& c, const starkv_kv4_cache& cache, const i
   const dim3 block(kRowThreads);
   // blocks of several tokens where they fill the GPU twice over, else of one, over more SMs (32 tokens: 2.0 us,
   // 2.9 in blocks of eight; 1000 tokens: equal)
-  if ((total + kReadTokens - 1) / kReadTokens * gy >= 2 * 148) {
+  if ((total + kReadTokens - 1) / kReadTokens * gy >= 2 * sm_count(c)) {
     const dim3 grid((unsigned)((total + kReadTokens - 1) / kReadTokens), gy);
     return launch_chained(d == 64 ? kv4_read_kernel<64, kReadTokens> : kv4_read_kernel<128, kReadTokens>, grid, block, 0,
                           s, 1u, a);
@@ -674,8 +674,9 @@ cudaError_t launch_kv4_evict(const Ctx& c, const starkv_kv4_cache& cache, const 
   EvictArgs a{block_table, seq_lens, keep_lens, recent, max_pages, dst_table, dst_max_pages, new_lens, kept,
               pool_of(c, cache), c.status, 1};
   // clusters where a list is long and there are few: two CTAs run on an SM
+  const int sms = sm_count(c);
   const int64_t most = (int64_t)max_pages * kPage, lists = (int64_t)c.cfg.num_kv_heads * batch;
-  while (a.cluster < kMostCluster && most / a.cluster > kStretch && lists * a.cluster * 2 <= 2 * 148) a.cluster *= 2;
+  while (a.cluster < kMostCluster && most / a.cluster > kStretch && lists * a.cluster * 2 <= 2 * sms) a.cluster *= 2;
   cudaError_t e = launch_chained(kv4_select_kernel, dim3(c.cfg.num_kv_heads * a.cluster, batch), dim3(kSelThreads), 0, s,
                                  (unsigned)a.cluster, a);
   if (e != cudaSuccess) return e;
