@@ -686,3 +686,79 @@ def test_read_reports_bounds_that_fall(batch, many):
     assert kv.status() == 0
     kv.kv4_read(cache, table, i32(cu), 9 * many, starts=starts)
     assert kv.status() == S.DEV_BAD_QUERY_SPAN
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 64), (2, 1, 128), (3, 1, 64), (1024, 8, 64), (256, 256, 64)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_decode_of_the_fewest_and_the_most_heads(shape, accumulate):
+    check_decode(shape, [37, 0, 600], accumulate, seed=shape[0])
+
+
+def test_evict_of_one_head_and_of_many():
+    check_evict((1, 1, 128), [70, 33], [30, 33], 5)
+    check_evict((300, 300, 64), [40], [17], 3)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_decode_of_more_sequences_than_a_block_has_threads(accumulate):
+    """Short sequences, empty ones and bad lengths in wide tables, whose pages are cut evenly: where a sequence begins is
+    summed over several rounds of a block's threads."""
+    S = skv()
+    shape = H, h, d = 8, 2, 64
+    rng = np.random.default_rng(41)
+    kv = context(*shape)
+    lens = rng.integers(0, 60, 301)
+    lens[rng.integers(0, 301, 60)] = 0
+    pages, t, _ = fill(rng, lens, h, d)
+    wide = np.full((301, 200), -1, np.int32)
+    wide[:, :t.shape[1]] = t
+    given = lens.copy()
+    given[[0, 150, 300]] = -1, 200 * 16 + 1, 1 << 30
+    qd, q = bf16(rng, 301, H, d)
+    cache = S.KV4Cache(kv.cfg, pages=torch.from_numpy(pages).cuda(), weights=torch.zeros((len(pages), h, 16), device="cuda"))
+    out = kv.kv4_decode(cache, qd, i32(wide), i32(given), accumulate=accumulate).double().cpu().numpy()
+    assert kv.status() == S.DEV_BAD_SEQ_LEN
+    w = cache.weights.double().cpu().numpy()
+    for b, n in enumerate(lens):
+        if given[b] != n or n == 0:
+            assert (out[b] == 0).all()
+            continue
+        slots = F.slots_of(t[b], n)
+        k, v = F.values(pages, slots, d)
+        o, _, p, mag = F.attend(q[b:b + 1].astype(np.float64), k, v, [n])
+        assert (np.abs(out[b] - o[0]) <= 2.0**-8 * np.abs(o[0]) + 2.0**-10 * (mag[0] + np.abs(v).max())).all(), b
+        if accumulate:
+            add = p[0].reshape(h, H // h, n).sum(1).T
+            es = score_error(q[b:b + 1], k)[0].max()
+            assert (np.abs(w[slots // 16, :, slots % 16] - add) <= add * (2 * es + 2.0**-18) + 2.0**-30).all(), b
+    if not accumulate:
+        assert (w == 0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_of_sequences_that_share_pages(d):
+    """A common beginning in the tables of all sequences, and a page that stands twice in one: each use adds its share."""
+    S = skv()
+    H, h = 8, 2
+    rng = np.random.default_rng(43)
+    kv = context(H, h, d)
+    pages, t, _ = fill(rng, [64, 80], h, d)
+    table = np.stack([t[0], t[0], np.concatenate([t[0, :4], t[1, 4:5]]), t[1, [0, 1, 0, 1, 2]]])  # [4, 5]
+    table[:, 4] = t[1, 4]
+    lens = [64, 50, 80, 70]
+    qd, q = bf16(rng, 4, H, d)
+    w0 = rng.random((len(pages), h, 16)).astype(np.float32)
+    cache = S.KV4Cache(kv.cfg, pages=torch.from_numpy(pages).cuda(), weights=torch.from_numpy(w0).cuda())
+    out = kv.kv4_decode(cache, qd, i32(table), i32(lens), accumulate=True).double().cpu().numpy()
+    assert kv.status() == 0
+    want, tol = w0.astype(np.float64), np.zeros(w0.shape)
+    for b, n in enumerate(lens):
+        slots = F.slots_of(table[b], n)
+        k, v = F.values(pages, slots, d)
+        o, _, p, mag = F.attend(q[b:b + 1].astype(np.float64), k, v, [n])
+        assert (np.abs(out[b] - o[0]) <= 2.0**-8 * np.abs(o[0]) + 2.0**-10 * (mag[0] + np.abs(v).max())).all(), b
+        add = p[0].reshape(h, H // h, n).sum(1).T
+        es = score_error(q[b:b + 1], k)[0].max()
+        np.add.at(want, (slots // 16, slice(None), slots % 16), add)
+        np.add.at(tol, (slots // 16, slice(None), slots % 16), add * (2 * es + 2.0**-18) + 2.0**-24)
+    assert (np.abs(cache.weights.double().cpu().numpy() - want) <= tol + 2.0**-22 * want).all()

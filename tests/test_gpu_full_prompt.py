@@ -604,3 +604,51 @@ def test_workspace_sizes_of_shapes_that_the_calls_refuse_are_refused():
     assert 65535 * (1 << 26) * 16 * 8 * 4 <= S.starkv_workspace_bytes(kv.ctx, S.OP_KV4_DECODE, 65535, 1 << 26, 1) < 65535 * (1 << 26) * 16 * 8 * 5
     assert S.starkv_workspace_bytes(kv.ctx, S.OP_KV4_DECODE, 0, 0, 0) >= 0 and S.starkv_prompt_workspace_bytes(kv.ctx, 0, 0, 0) == 0
     assert S.starkv_prompt_workspace_bytes(kv.ctx, 65535, most, most) <= 40 << 20
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 64), (2, 1, 128), (3, 1, 64), (1024, 8, 64), (200, 200, 64)])
+def test_prompt_of_the_fewest_and_the_most_heads(shape):
+    run(shape, [5, 0, 140], [9, 3, 140], window=50, seed=shape[0])
+    if shape[0] < 100:
+        run(shape, [300], [1900], window=290, seed=shape[0])
+
+
+@pytest.mark.parametrize("shape", [(8, 2, 64), (4, 4, 128)])
+def test_prompts_of_more_sequences_than_a_warp_has_lanes(shape):
+    """150 sequences, empty ones among them, whose work is cut evenly: where one begins is summed over rounds of 32."""
+    rng = np.random.default_rng(44)
+    n_q = rng.integers(0, 40, 150)
+    n_k = n_q + rng.integers(0, 30, 150) * (rng.random(150) < 0.5)
+    n_q[::7] = 0
+    n_k[::14] = 0
+    n_q[-1], n_k[-1] = 0, 0
+    run(shape, n_q.tolist(), n_k.tolist(), window=12, seed=44)     # a window's queries stay
+    run(shape, n_q.tolist(), n_k.tolist(), window=10**6, seed=44)
+
+
+def test_cut_prompts_captured_and_replayed_with_other_lengths():
+    """One graph for packed prompts of other lengths in the same rows: work is cut on the device."""
+    shape = (12, 4, 128)
+    rng = np.random.default_rng(45)
+    kv = context(*shape)
+    q, k, v = inputs(rng, shape, [700], [2300])
+    lens = [([700], [2300]), ([300, 400], [300, 2000]), ([0, 1, 699], [900, 1, 1399]), ([350, 0, 350], [1000, 50, 1250])]
+    batch = 3
+    cu = [[cu_of(list(x) + [0] * (batch - len(x))) for x in pair] for pair in lens]
+    cq, ck = i32(cu[0][0]), i32(cu[0][1])
+    plain = []
+    for a, b in cu:
+        out, lse = kv.prompt(q, k, v, i32(a), i32(b), 700)
+        plain.append((out, lse, kv.prompt_weights(q, k, lse, i32(a), i32(b), 2300, 20)))
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, lse = kv.prompt(q, k, v, cq, ck, 700)
+        w = kv.prompt_weights(q, k, lse, cq, ck, 2300, 20)
+    for i in (1, 2, 3, 0, 2):
+        cq.copy_(i32(cu[i][0]))
+        ck.copy_(i32(cu[i][1]))
+        g.replay()
+        assert torch.equal(out, plain[i][0]) and torch.equal(lse, plain[i][1]) and torch.equal(w, plain[i][2])
+        check_prompt(kv, shape, q, k, v, *lens[i], out, lse, w, 20)
+    assert kv.status() == 0
