@@ -1,4 +1,5 @@
 // The 4-bit cache of full-width layers: append, read back, eviction.
+// (Times in this file: a call's time on the GPU, calls back to back in a graph, unless a kernel's own.)
 #include "full.cuh"
 #include "sm100.cuh"
 
@@ -12,8 +13,8 @@ namespace {
 // Append.  A thread quantises one group of 32 channels (four 16-byte loads, four code words):
 // the group's scale is worked out once and no thread waits for another.  The kernel is bound by
 // its instructions, 127 a code word (with eight channels a thread, the group's ends by
-// shuffles and the scale worked out four times, it took 222, and 70 us instead of 46 for 8098
-// tokens of 32 heads of 128: 3.8 TB/s).
+// shuffles and the scale worked out four times, it took 222, and 70 us, the kernel alone, instead
+// of 46 for 8098 tokens of 32 heads of 128: 3.8 TB/s).
 // ---------------------------------------------------------------------------
 struct AppendArgs {
   const __nv_bfloat16* k;
@@ -142,8 +143,8 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const AppendArg
 
 // ---------------------------------------------------------------------------
 // Read back.  One code word per thread and token: 4 bytes and the group's scale and
-// zero in, eight bf16 values (16 bytes) out; blocks as in append, each row's slot
-// looked up once per block.
+// zero in, eight bf16 values (16 bytes) out.  A block takes 256 code words of the rows of
+// T tokens, whose slots it looks up once.
 // ---------------------------------------------------------------------------
 struct ReadArgs {
   const int32_t* block_table;
@@ -259,8 +260,8 @@ struct EvictArgs {
   int cluster;  // CTAs that share a (sequence, KV head) in the selection
 };
 
-// CTAs of a cluster at most: 32 lists of 32768 tokens take 49 us (with the move: 71) on one CTA each,
-// 35 on two, 32 on four, 40 on eight.
+// CTAs of a cluster at most: 32 lists of 32768 tokens take 69 us, the move among them, on one CTA each,
+// 56 on two, 54 on four, 62 on eight.
 constexpr int kMostCluster = 4;
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
@@ -292,7 +293,7 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t mine, uint32_t* sum, uin
   return __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u) + inc - mine;
 }
 
-// grid (num_kv_heads * cluster, batch)
+// grid (num_kv_heads * cluster, batch); two CTAs an SM at 64 registers a thread, of which 44 bytes spill
 __global__ void __launch_bounds__(kSelThreads, 2) kv4_select_kernel(const EvictArgs a) {
   __shared__ __align__(16) uint32_t bins[kBins];
   __shared__ uint32_t scan[2][kSelWarps];
@@ -531,7 +532,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) kv4_select_kernel(const EvictA
 // Eviction, step 2: gather the kept tokens' rows.  A warp fills kMovePages (destination
 // page, KV head)s: all their source slots are looked up first, and a page's rows are asked
 // for before the page before it is stored, so that the chain of dependent loads (kept index,
-// page, rows) is waited for once in four pages.
+// page, rows) is waited for once in four pages.  (At width 64 the compiler stays at 40 registers and spills 12 bytes.)
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 128;
 constexpr int kMovePages = 4;
@@ -656,8 +657,8 @@ cudaError_t launch_kv4_read(const Ctx& c, const starkv_kv4_cache& cache, const i
   const int d = c.cfg.head_dim;
   const unsigned gy = (unsigned)((c.cfg.num_kv_heads * (2 * d / 8) + kRowThreads - 1) / kRowThreads);
   const dim3 block(kRowThreads);
-  // blocks of several tokens where they fill the GPU twice over, else of one, over more SMs (32 tokens: 2.0 us,
-  // 2.9 in blocks of eight; 1000 tokens: equal)
+  // blocks of several tokens where they fill the GPU twice over, else of one, over more SMs (8 heads of 128,
+  // with the append before: 32 tokens 5.8 us, 6.6 in blocks of eight; 1000 tokens 9.2 and 8.3, within the rule's reach)
   if ((total + kReadTokens - 1) / kReadTokens * gy >= 2 * sm_count(c)) {
     const dim3 grid((unsigned)((total + kReadTokens - 1) / kReadTokens), gy);
     return launch_chained(d == 64 ? kv4_read_kernel<64, kReadTokens> : kv4_read_kernel<128, kReadTokens>, grid, block, 0,

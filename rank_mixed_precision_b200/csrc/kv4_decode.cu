@@ -2,7 +2,7 @@
 //
 // The batch's pages, laid end to end as (sequence, unit, page) with a unit = one KV head
 // and a block of at most eight of its query heads, are cut into equal stretches, one per
-// CTA (four or five CTAs an SM, one round): ragged lengths cost no idle SMs, and a CTA's
+// CTA (four CTAs an SM, one round): ragged lengths cost no idle SMs, and a CTA's
 // start (its queries, its first copies) is paid once for about a hundred pages.  A unit
 // that a cut goes through leaves partial results, which a second kernel joins; where the
 // tables are short, a CTA takes a whole unit and there is no second kernel.
@@ -14,6 +14,7 @@
 // their operands come out of 4-bit codes in registers, which tcgen05 (operands in shared
 // or tensor memory, N of a whole tile) could only take after a round trip through shared
 // memory.
+// (Times in this file: a call's time on the GPU, calls back to back in a graph.)
 //
 //   scores   s[t, h] = sum_g ( sc[t, g] * sum_{c in g} n[t, c] q[h, c] ) + sum_g z[t, g] * sum_{c in g} q[h, c]
 //     A = the codes n of the page's tokens, B = q.  A masked code (w & 0x000f000f) is
@@ -42,17 +43,19 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kHeads = 8;            // query heads of one CTA (the N of the products)
-constexpr int kCtas = 4;             // CTAs of an SM
+// CTAs of an SM: 128 registers a thread, of which 108 bytes spill at head width 128 (none at 64).  Five, with 102
+// registers, were slower (one sequence of 32768 tokens: 68 us for 59 at the time).
+constexpr int kCtas = 4;
 // A CTA takes a whole unit where tables hold at most kWholePages pages, or kWholePagesMany where there
 // are kManyUnits units or more; else the pages are cut evenly (a second segment's start in most CTAs,
-// and the join).  Whole and cut in us: 4 heads of 64, 512 tokens 6.2 and 8.4, 2048 tokens 15.4 and 9.1;
-// heads of 128, 64 units of 1024 tokens 12.9 and 14.5, 256 units of 2048 28.4 and 34.7, of 4096 52.8
-// and 52.9 (equal lengths: ragged ones favour the cut).
+// and the join).  Whole and cut in us: 4 heads of 64, 512 tokens 6.0 and 8.5, 2048 tokens 15.2 and 9.2;
+// heads of 128, 64 units of 1024 tokens 12.5 and 12.3, 256 units of 2048 28.3 and 33.5, of 4096 51.7
+// and 50.6 (equal lengths: ragged ones favour the cut).
 constexpr int kWholePages = 32;
 constexpr int kWholePagesMany = 128;
 constexpr int kManyUnits = 64;
 // CTAs of a unit at most: more parts cost the join more than they spare.  (At most 32, 74, 148 and any
-// number, us: 8 heads of 128 over one, 100000 tokens 41, 26, 24, 46; 40 of 64 over one, 20000 tokens 14, 15, 19, 19.)
+// number, us: 8 heads of 128 over one, 100000 tokens 38, 25, 22, 46; 40 of 64 over one, 20000 tokens 14, 15, 19, 19.)
 constexpr int kMostParts = 74;
 constexpr float kBelow = 7.f;        // the reference of p, below the largest score (log2),
 constexpr float kMoveMax = 15.f;     // and how far scores may pass it before it moves: p <= 2^15, fp16 ends at 2^16
@@ -600,13 +603,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_decode_kernel(const Decod
 // Join of the parts, and the weights.  Blocks x < outs of a (sequence, KV head) join the
 // outputs of its units that a cut went through (and write an empty sequence's zero rows), `side`
 // heads each: the more parts a unit has, the fewer heads a block, and the more threads share a
-// head's parts out.  (Two sequences of 21648 tokens, 14 heads of 64 over 2, 148 parts a unit:
-// 17 us; all seven heads in one block 32.)  The other blocks add the probabilities of 1024 tokens
+// head's parts out.  (Two sequences of 21648 tokens, 14 heads of 64 over 2, 74 parts a unit:
+// 14 us; all seven heads in one block 22.)  The other blocks add the probabilities of 1024 tokens
 // each: a warp reads the scores of 32 tokens at a time, and a transpose among four lanes gives
 // each lane four neighbours of one page, which it adds at once: one page to look up and one
 // addition of 16 bytes.  (Decode and
-// join of 32 sequences of 4096 to 8192 tokens, 32 heads over 8: 87 us; with a token a lane at a
-// time, and the norms read for each, 92; with six blocks an SM, not eight, 88.)
+// join of 32 sequences of 4096 to 8192 tokens, 32 heads over 8: 84 us; with a token a lane at a
+// time, and the norms read for each, 92 for 87 at the time; with six blocks an SM, not eight, 88.)
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 constexpr int kJoinTokens = 4 * kJoinThreads;

@@ -5,6 +5,11 @@
 // tile is query r / gb of the tile, head r % gb of the group (gb heads, R = 128 / gb
 // queries), which one 3-D TMA box per 64 channels brings in.  A tile's K and V then
 // serve every head of the group, and a causal tile wastes 128 / gb queries at most.
+//
+// Times in this file: of the large cases (sixteen packed prompts of 1 to 1999 tokens, 32 query
+// over 8 KV heads; 2048 queries over 32768 keys, 32 heads; the weights of the last 64 queries of
+// 4 x 32768 and of every query of 8001, 32 heads over 8) passes among others, a second and more of
+// them, under the power cap; of the others a call's time on the GPU, calls back to back in a graph.
 #include "full.cuh"
 #include "sm100.cuh"
 
@@ -162,19 +167,21 @@ __device__ __forceinline__ SeqSpan span_of(const PromptKArgs& a, int b) {
 //   than 2^8 only, and then the row's O is rescaled in place; S_t (j) complete implies
 //   that P_t V_(j-1) is, so no further barrier guards that.  The next unit's Q and first
 //   products run while the softmax warps write the last unit out.
-constexpr int kAttnThreads = 384;
+constexpr int kAttnThreads = 384;  // 168 registers a thread, 12 bytes of which spill
 // A CTA takes a whole unit where there are at most kFewKeys keys in all (32 query over 8 KV heads of 128,
-// 256 tokens: 11.2 us, 17.7 us cut and joined; 1000 tokens: 22.6 and 42.0; one query: equal), and where there are units for all SMs and the keys and values do not stay in L2: units
-// that start together then read the same tiles together, stretches do not (32768 keys of 32 heads: 1060 us
-// and 1178 us, for 65% and 26% of hits in L2; sixteen prompts that fit: 298 us and 291 us).
+// with the host's time: 256 tokens 23 us, 31 us cut and joined; 1000 tokens 25 and 42; one query of 1000
+// keys 19 and 24), and where there are units for all SMs and the keys and values do not stay in L2: units
+// that start together then read the same tiles together, stretches do not (32768 keys of 32 heads: 1046 us
+// and 1116 us, for 65% and 26% of hits in L2; sixteen prompts that fit: 294 us and 275 us).
 constexpr int kFewKeys = 1024;
 constexpr int64_t kMostCached = (int64_t)96 << 20;  // bytes of keys and values
 constexpr int kLeastTiles = 2;    // key tiles of a stretch, where there are few
 // Positions that a unit counts for beside its key tiles: its start and its end cost as much as two
-// (sixteen prompts of 1 to 1999 tokens: counted as 1, 2, 3, 4: 261, 243, 249, 255 us).
+// (sixteen packed prompts: counted as 1, 2, 3, 4: 285, 275, 275, 280 us).
 constexpr int kUnitCost = 2;
 // Pairs of exponentials that go to the FMA pipe: one of eight.  (2048 queries over 32768 keys: none
-// 914 us, one of eight 894, one of four 982, half 1070: the softmax warps' issue slots bound them too.)
+// 1051 us, one of eight 1045, one of four 1053, half 1146: the softmax warps' issue slots bound them too.
+// In short runs, below the power cap, 914, 894, 982 and 1070.)
 __device__ constexpr bool on_fma_pipe(int pair) { return pair % 8 == 7; }
 
 template <int D>
@@ -857,7 +864,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // ---------------------------------------------------------------------------
 // Join of the units that a cut went through: block (c, y) takes the y-th of the rows (as many as
 // its threads hold at once) of the unit that begins in CTA c's stretch and goes on behind it.
-// (16 queries of 32 heads over 8, 8000 keys: 25 us in all; 32 rows a block, one after the other, 55.)
+// (16 queries of 32 heads over 8, 8000 keys: 25 us in all; with 32 rows a block, one after the other, 55.)
 // ---------------------------------------------------------------------------
 constexpr int kMergeThreads = 256;
 
@@ -911,7 +918,8 @@ __global__ void __launch_bounds__(kMergeThreads) prompt_join_kernel(const Prompt
 // columns each (four warps a scheduler keep the exponentials going while others wait for
 // their columns); warp 16 copies, warp 17 issues the products, warps 18 and 19 lay out each
 // column's log-sum-exp and the last key it sees and note for each product what its sums go
-// by.  A note without a product makes up an item's number where it has to be even.  One CTA an SM walks over many items, three ways:
+// by.  A note without a product makes up an item's number where it has to be even.  One CTA an SM
+// walks over many items, three ways:
 //   resident  the counting queries of a (sequence, KV head) fit the ring (a window): a CTA
 //             takes an equal stretch of the items in (sequence, KV head, key) order and
 //             loads them once per (sequence, KV head); only K tiles stream.  (64 queries of
@@ -920,7 +928,7 @@ __global__ void __launch_bounds__(kMergeThreads) prompt_join_kernel(const Prompt
 //             steps), dealt forth and back, so that the CTAs' sums of steps come out alike.
 //   split     where there are few items, a cluster shares one item's steps out and adds the
 //             sums through distributed shared memory, in rank order.  (2000 queries of 16
-//             heads over one: 27 us, unsplit 159.)
+//             heads over one: 26 us, unsplit 160.)
 constexpr int kWeightThreads = 640;
 constexpr int kColNone = -(1 << 30);  // a column that sees no key
 enum { kResident = 0, kStreamed = 1 };  // > 1: split over so many CTAs
@@ -1366,7 +1374,8 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       if (ok && made_up(steps)) ok = note(Note{rank + split >= steps ? kLast : 0, 0, 0, key0, keys, 0, row});
       if (lay) flips ^= (1u << min(steps, ST)) - 1;
       // The two warps meet when a (sequence, KV head)'s columns are there.  (No order hangs on it; without it the
-      // last 64 queries of 4 x 32768 take 95 us for 89, 96 queries of each, three steps, 136 for 124.)
+      // last 64 queries of 4 x 32768 take, in short runs in turn, 98 us for 89, 96 queries of each, three steps,
+      // 136 for 124.)
       if (ok && resident && fresh) {
         if (lane == 0) mbar_arrive(both);
         ok = __all_sync(0xffffffffu, mbar_wait_short(both, laid_units & 1));
@@ -1409,8 +1418,8 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
           const f32x2 t0 = fma2(pair(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), scale, pair(z.x, z.y));
           const f32x2 t1 = fma2(pair(__uint_as_float(y[e + 2]), __uint_as_float(y[e + 3])), scale, pair(z.z, z.w));
           two[0] = add2(two[0], ex2_sfu(t0));
-          // one pair of eight on the FMA pipe (every query of 8001: 303 us, none 317, one of four 303 and
-          // slower where the queries are few: 102 us for 92)
+          // one pair of eight on the FMA pipe (every query of 8001: 338 us, none 344, one of four 342; the last 64
+          // of 4 x 32768: 100, 103 and 110)
           two[1] = add2(two[1], e % 16 == 0 ? ex2_fma(t1) : ex2_sfu(t1));
         }
         const float2 a0 = unpair(two[0]), a1 = unpair(two[1]);
@@ -1549,8 +1558,8 @@ cudaError_t launch_weights_d(const CUtensorMap& qm, const CUtensorMap& km, Promp
     while (cluster < 8 && items * cluster * 2 <= sms && cluster * 2 <= most) cluster *= 2;
     // Pairs of CTAs where they come in two rounds, too, if all queries count: the items' steps then fall evenly
     // from `most` to none, and a pair that ends takes one of the short ones.  That spares most * sms / (4 items)
-    // steps and costs a second round's start, 14 steps.  (Queries of 32 heads over 8: 1300 31 and 21 us, 2000 46
-    // and 34, 256 of 2048 12 and 20; 4000 of 4 heads of 64, 25 and 24.)
+    // steps and costs a second round's start, 14 steps.  (Queries of 32 heads over 8: 1300 30 and 21 us, 2000 45
+    // and 33, 256 of 2048 11 and, in pairs, 20; 4000 of 4 heads of 64 24 and 24.)
     if (items * 2 > sms && items <= sms && a.window >= a.max_k && most * sms > 56 * items) cluster = 2;
     if (cluster > 1) {
       a.mode = (int)cluster;
