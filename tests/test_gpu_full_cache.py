@@ -762,3 +762,91 @@ def test_decode_of_sequences_that_share_pages(d):
         np.add.at(want, (slots // 16, slice(None), slots % 16), add)
         np.add.at(tol, (slots // 16, slice(None), slots % 16), add * (2 * es + 2.0**-18) + 2.0**-24)
     assert (np.abs(cache.weights.double().cpu().numpy() - want) <= tol + 2.0**-22 * want).all()
+
+
+def all_values(pages, d):
+    """(k, v) fp64 [tokens, d] on the GPU of every slot of pages [P, 1, page bytes], in order."""
+    P, ng = pages.shape[0], d // 32
+    w = pages[:, 0].contiguous().view(torch.int32)
+    shift = 4 * torch.arange(8, device=pages.device, dtype=torch.int32)
+    out = []
+    for x, order, at in ((w[:, :2 * d].reshape(P, 16, 4, ng), (0, 1, 3, 2, 4), 4 * d), (w[:, 2 * d:4 * d].reshape(P, 16, ng, 4), (0, 1, 2, 3, 4), 4 * d + 16 * ng)):
+        code = ((x[..., None] >> shift) & 15).permute(order).reshape(P, 16, ng, 32).double()
+        meta = w[:, at:at + 16 * ng].contiguous().view(torch.float16).view(P, 16, ng, 2).double()
+        out.append((code * meta[..., :1] + meta[..., 1:]).reshape(P * 16, d))
+    return out
+
+
+def test_a_sequence_of_a_million_tokens():
+    """Written, decoded with its weights, evicted: 8 heads over one, one sequence of 2^20 + 12345 tokens in pages in order."""
+    S = skv()
+    H, h, d = 8, 1, 64
+    kv = context(H, h, d)
+    n, keep, recent = (1 << 20) + 12345, 300001, 1000
+    used, room = -(-n // 16), -(-keep // 16)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    cache = kv.new_kv4_cache(used + room, keep_weights=True)
+    k, v = (torch.randn((n, h, d), generator=g, device="cuda").bfloat16() for _ in range(2))
+    w0 = torch.rand((n, h), generator=g, device="cuda")
+    kv.kv4_append(cache, k, v, torch.arange(n, device="cuda"), w0)
+    q = (2 * torch.randn((1, H, d), generator=g, device="cuda")).bfloat16()
+    table, lens = torch.arange(used, device="cuda", dtype=torch.int32)[None], i32([n])
+    out = kv.kv4_decode(cache, q, table, lens, accumulate=True)
+    assert kv.status() == 0
+    kk, vv = (x[:n] for x in all_values(cache.pages[:used], d))
+    z = q[0].double() @ kk.t() / 8
+    es = (q[0].double().abs() @ kk.abs().t()).amax(-1) * 2.0**-20 / 8
+    p = torch.softmax(z, -1)
+    o, mag = p @ vv, p @ vv.abs()
+    # the output in bf16, v in fp16, p in fp16 (2^-11, and 2^-32 of the largest a token), the score's error, ex2 and sums
+    lost = (p.amax(-1) * n * 2.0**-32)[:, None] * vv.abs().max()
+    tol = 2.0**-8 * o.abs() + (mag + vv.abs().max()) * 2.0**-11 + mag * (2.0**-11 + 2 * es[:, None] + 2.0**-17) + lost
+    assert ((out[0].double() - o).abs() <= tol).all()
+    w = cache.weights[:used].reshape(-1)[:n]
+    add = p.sum(0)
+    assert ((w.double() - (w0[:, 0].double() + add)).abs() <= (p * (2 * es[:, None] + 2.0**-17)).sum(0) + 2.0**-23).all()
+    dst = torch.arange(used, used + room, device="cuda", dtype=torch.int32)[None]
+    new, kept = kv.kv4_evict(cache, table, lens, i32([keep]), recent, dst)
+    assert kv.status() == 0 and new.tolist() == [keep]
+    heavy = torch.sort(w[:n - recent], descending=True, stable=True).indices[:keep - recent].sort().values
+    stay = torch.cat([heavy, torch.arange(n - recent, n, device="cuda")])
+    assert torch.equal(kept[0, 0, :keep].long(), stay) and (kept[0, 0, keep:] == -1).all()
+    moved = all_values(cache.pages[used:], d)
+    assert torch.equal(moved[0][:keep], kk[stay]) and torch.equal(moved[1][:keep], vv[stay])
+    assert torch.equal(cache.weights[used:].reshape(-1)[:keep], w[stay])
+
+
+def test_every_call_on_another_stream():
+    """Append, read, decode into a given output and eviction on a stream of their own: as on the current one."""
+    S = skv()
+    H, h, d = 8, 2, 128
+    rng = np.random.default_rng(51)
+    kv = context(H, h, d)
+    n = [700, 90]
+    t, spare, n_pages = tables(rng, n, extra=30)
+    kd, _ = keys(rng, sum(n), h, d)
+    vd, _ = bf16(rng, sum(n), h, d)
+    qd, _ = bf16(rng, 2, H, d)
+    slots = torch.from_numpy(np.concatenate([F.slots_of(t[b], m) for b, m in enumerate(n)])).cuda()
+    first = torch.rand((sum(n), h), device="cuda")
+    dst = np.zeros((2, 25), np.int32)
+    dst[0], dst[1, :5] = spare[:25], spare[25:]
+    td, ld, keeps, dd, cu = i32(t), i32(n), i32([400, 80]), i32(dst), i32(cu_of(n))
+
+    def life(stream):
+        cache = kv.new_kv4_cache(n_pages, keep_weights=True)
+        out = torch.full_like(qd, 7)
+        torch.cuda.synchronize()
+        kv.kv4_append(cache, kd, vd, slots, first, stream=stream)
+        k, v = kv.kv4_read(cache, td, cu, sum(n), stream=stream)
+        assert kv.kv4_decode(cache, qd, td, ld, accumulate=True, out=out, stream=stream) is out
+        lens, kept = kv.kv4_evict(cache, td, ld, keeps, 9, dd, stream=stream)
+        torch.cuda.synchronize()
+        return k, v, out, lens, kept, cache.pages, cache.weights
+
+    want = life(None)
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream, 0):
+        for x, y in zip(life(stream), want):
+            assert torch.equal(x, y)
+    assert kv.status() == 0

@@ -652,3 +652,39 @@ def test_cut_prompts_captured_and_replayed_with_other_lengths():
         assert torch.equal(out, plain[i][0]) and torch.equal(lse, plain[i][1]) and torch.equal(w, plain[i][2])
         check_prompt(kv, shape, q, k, v, *lens[i], out, lse, w, 20)
     assert kv.status() == 0
+
+
+def test_prompt_of_one_chunk_behind_a_million_keys():
+    """37 queries of 8 heads over one behind 2^20 keys, on every SM, into a given output; and what they look at."""
+    S = skv()
+    H, h, d, n, m = 8, 1, 64, 37, (1 << 20) + 37
+    kv = context(H, h, d)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    q, k, v = ((s * torch.randn(x, generator=g, device="cuda")).bfloat16() for s, x in ((2, (n, H, d)), (1, (m, h, d)), (1, (m, h, d))))
+    cq, ck = i32([0, n]), i32([0, m])
+    given = torch.full_like(q, 7)
+    out, lse = kv.prompt(q, k, v, cq, ck, n, out=given)
+    assert out is given
+    w = kv.prompt_weights(q, k, lse, cq, ck, m, 16)
+    assert kv.status() == 0
+    bare = torch.empty_like(q)  # without the log-sum-exp
+    ws = torch.empty(S.starkv_prompt_workspace_bytes(kv.ctx, 1, n, m), dtype=torch.uint8, device="cuda")
+    S.starkv_prompt_attn(kv.ctx, kv.cfg, q, k, v, cq, ck, n, bare, None, ws)
+    assert torch.equal(bare, out) and kv.status() == 0
+    seen = torch.arange(m, device="cuda")[None] <= (m - n + torch.arange(n, device="cuda"))[:, None]
+    kk, vv = k[:, 0].double(), v[:, 0].double()
+    want = torch.zeros(m, dtype=torch.float64, device="cuda")
+    tol = torch.zeros_like(want)
+    for i in range(H):
+        z = torch.where(seen, q[:, i].double() @ kk.t() / 8, -torch.inf)
+        es = (q[:, i].double().abs() @ kk.abs().t()).amax() * 2.0**-20 / 8
+        p = torch.softmax(z, -1)
+        o, mag = p @ vv, p @ vv.abs()
+        # p in bf16 and the output in bf16; the score's error twice, ex2 and fp32 sums of parts
+        assert ((out[:, i].double() - o).abs() <= 2.0**-8 * (o.abs() + mag) + mag * (2 * es + 2.0**-16)).all()
+        ls = torch.logsumexp(z, -1)
+        assert ((lse[:, i].double() - ls).abs() <= es + 2.0**-16 + 2.0**-22 * ls.abs()).all()
+        x = torch.exp(z - lse[:, i].double()[:, None])[n - 16:]
+        want += x.sum(0)
+        tol += x.sum(0) * (es + 2.0**-17)
+    assert ((w[:, 0].double() - want).abs() <= tol + 2.0**-30).all()
