@@ -658,7 +658,8 @@ cudaError_t launch_kv4_read(const Ctx& c, const starkv_kv4_cache& cache, const i
   const unsigned gy = (unsigned)((c.cfg.num_kv_heads * (2 * d / 8) + kRowThreads - 1) / kRowThreads);
   const dim3 block(kRowThreads);
   // blocks of several tokens where they fill the GPU twice over, else of one, over more SMs (8 heads of 128,
-  // with the append before: 32 tokens 5.8 us, 6.6 in blocks of eight; 1000 tokens 9.2 and 8.3, within the rule's reach)
+  // with the append before: 32 tokens 5.8 us, 6.6 in blocks of eight; 1000 tokens 9.2 and
+  // 8.3: the rule could switch a little earlier)
   if ((total + kReadTokens - 1) / kReadTokens * gy >= 2 * sm_count(c)) {
     const dim3 grid((unsigned)((total + kReadTokens - 1) / kReadTokens), gy);
     return launch_chained(d == 64 ? kv4_read_kernel<64, kReadTokens> : kv4_read_kernel<128, kReadTokens>, grid, block, 0,
